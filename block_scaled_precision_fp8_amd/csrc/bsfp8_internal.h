@@ -145,13 +145,171 @@ __device__ __forceinline__ void wait_lgkmcnt0() {
   __builtin_amdgcn_s_waitcnt(0xF | (0x7 << 4) | (0x0 << 8) | (0x3 << 14));
 }
 
+// ------------------------------- eight-value encoders, MFMA steps, scale loads
+
+namespace detail {
+
+struct Unpacked { float f[8]; };
+
+__device__ __forceinline__ Unpacked unpack8(uint4 v) {
+  Unpacked u;
+  u.f[0] = bf16_lo(v.x); u.f[1] = bf16_hi(v.x);
+  u.f[2] = bf16_lo(v.y); u.f[3] = bf16_hi(v.y);
+  u.f[4] = bf16_lo(v.z); u.f[5] = bf16_hi(v.z);
+  u.f[6] = bf16_lo(v.w); u.f[7] = bf16_hi(v.w);
+  return u;
+}
+
+__device__ __forceinline__ float amax8(const Unpacked& u) {
+  float a = fabsf(u.f[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) a = fmaxf(a, fabsf(u.f[i]));
+  return a;
+}
+
+// Encode eight values of one group with the group's scale.  Returns the
+// codes packed little-endian; writes the stored scale representation.
+// fp32 scales divide by the correctly rounded reciprocal with one exact
+// correction (div_by_rcp: the same E4M3 codes as IEEE x / s for a normal s,
+// at four operations per value instead of an IEEE division each); a
+// subnormal scale divides directly.
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(const Unpacked& u, float amax, float* s_f32, int* s_exp) {
+  const float s = FMT == 0 ? act_scale_f32(amax) : 0.0f;
+  const int e = FMT == 0 ? 0 : ue8m0_exp(amax);
+  *s_f32 = s;
+  *s_exp = e;
+  uint2 r;
+  if (FMT == 0 && s >= kMinNormal) {
+    const RcpDiv dv = rcp_div(s);
+    r.x = act_encode4_rcp<FMT>(u.f[0], u.f[1], u.f[2], u.f[3], dv, e);
+    r.y = act_encode4_rcp<FMT>(u.f[4], u.f[5], u.f[6], u.f[7], dv, e);
+  } else {
+    r.x = act_encode4<FMT>(u.f[0], u.f[1], u.f[2], u.f[3], s, e);
+    r.y = act_encode4<FMT>(u.f[4], u.f[5], u.f[6], u.f[7], s, e);
+  }
+  return r;
+}
+
+__device__ __forceinline__ v8i join(uint4 a, uint4 b) {
+  v8i r;
+  r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+  r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+  return r;
+}
+
+template <int FMT>
+__device__ __forceinline__ float load_scale(const void* p, int64_t idx) {
+  if (FMT == 0) return ((const float*)p)[idx];
+  return __int_as_float(((const uint8_t*)p)[idx]);   // carries the byte
+}
+
+__device__ __forceinline__ float e8m0_f32(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b << 23);   // 2^(b - 127)
+}
+
+// MFMA step for one 16x16 tile and one K block.
+template <int FMT>
+__device__ __forceinline__ v4f mfma_step(v4f acc, const v8i& a, const v8i& b, float sa,
+                                         float sw) {
+  if (FMT == 0) {
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+    v4f t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 127, 0, 127);
+    const float c = sa * sw;
+    acc[0] = fmaf(t[0], c, acc[0]);
+    acc[1] = fmaf(t[1], c, acc[1]);
+    acc[2] = fmaf(t[2], c, acc[2]);
+    acc[3] = fmaf(t[3], c, acc[3]);
+    return acc;
+  } else {
+    // A = W (scale S_w), B = X (scale S_a); E8M0 bytes in bits [7:0].
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        a, b, acc, 0, 0, 0, __float_as_int(sw), 0, __float_as_int(sa));
+  }
+}
+
+// MFMA step with an MXFP4 weight fragment (A operand, format E2M1: 16
+// bytes per lane in the low half of the register block) and its lane's
+// E8M0 block scale (the 32 weights this lane carries); X stays FP8.
+template <int FMT>
+__device__ __forceinline__ v4f mfma_step_w4(v4f acc, const v8i& a, const v8i& b, float sa,
+                                            int sw4) {
+  if (FMT == 0) {
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+    v4f t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 4, 0, 0, sw4, 0, 127);
+    acc[0] = fmaf(t[0], sa, acc[0]);
+    acc[1] = fmaf(t[1], sa, acc[1]);
+    acc[2] = fmaf(t[2], sa, acc[2]);
+    acc[3] = fmaf(t[3], sa, acc[3]);
+    return acc;
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sw4, 0,
+                                                            __float_as_int(sa));
+  }
+}
+
+}  // namespace detail
+
 // ---------------------------------------------------------------- host
+
+struct NormArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* res;       // null: h = x
+  uint16_t* res_out;         // row stride ldr, like res
+  int64_t ldr;
+  const uint16_t* w;         // [K]
+  uint16_t* y;               // bf16 [M][K] or null
+  uint8_t* xq;               // [M][K], or null: no quantized output
+  void* xs;
+  const void* xstat;         // the static scheme's scale, or null
+  float eps;
+  int64_t M, K;
+  int fmt, group_k;
+};
+
+struct RouteArgs {
+  const void* logits;        // [T][ldl] fp32 or bf16
+  int64_t ldl;
+  bool bf16;
+  const float* bias;         // [E] or null
+  int64_t T;
+  int E, k, score, renorm;
+  float scale;
+  int n_group, topk_group;
+  int32_t* ids;              // [T][k]
+  float* weights;            // [T][k]
+};
+
+constexpr int kMoeMaxTokens = 128;   // tokens of one moe_decode call
+constexpr int kMoeMaxChoices = 16;   // experts per token
+struct MoeArgs {
+  const uint8_t* xq;         // [T][H] and its scales
+  const void* xs;
+  const int32_t* ids;        // [T][k]
+  const float* wt;           // [T][k]
+  const uint8_t* w13;        // [E][2I][H] codes (w4: [E][2I][H/2])
+  const void* s13;
+  const uint8_t* w2;         // [E][H][I] codes (w4: [E][H][I/2])
+  const void* s2;
+  const uint16_t* addend;    // bf16 [T][H] or null
+  uint16_t* y;               // bf16 [T][H]
+  int T, k, E;
+  int64_t H, I;
+  int fmt;
+  bool w4;
+  void* workspace;
+};
 
 // static_scale: null for dynamic 1x128 groups, else the device address of
 // one calibrated per-tensor scale (fp32, or the E8M0 byte).
 hipError_t launch_quant_act(const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
                             int fmt, uint8_t* xq, void* scale, hipStream_t s,
                             const void* static_scale = nullptr, int group_k = 128);
+hipError_t launch_add_rmsnorm_quant(const NormArgs& a, hipStream_t s);
+hipError_t launch_route_topk(const RouteArgs& a, hipStream_t s);
+hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t s);
+size_t moe_decode_workspace_bytes(int64_t slots, int64_t I);
 hipError_t launch_dequant_weight(const uint8_t* wq, int64_t N, int64_t K, int fmt,
                                  const void* scale, uint16_t* w, hipStream_t s, int blk = 128);
 hipError_t launch_pow2_to_ue8m0(const float* in, int64_t n, uint8_t* out, hipStream_t s);

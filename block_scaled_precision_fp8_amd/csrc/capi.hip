@@ -150,6 +150,42 @@ int32_t linear_launch(const void* x, int64_t ldx, const void* wq, const void* w_
   return hip_status(launch_block_gemm(a, st));
 }
 
+// ---- fp8_moe_decode, fp8_fp4_moe_decode: checks and launches
+
+static int32_t moe_decode_call(const void* xq, const void* xs, const int32_t* ids, const float* wt,
+                               const void* w13, const void* s13, const void* w2, const void* s2,
+                               const void* addend, void* y, int64_t T, int32_t k, int64_t H,
+                               int64_t I, int32_t E, int32_t fmt, bool w4, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (E < 1 || E > 1024 || k < 1 || T < 0) return BSFP8_EINVAL;
+  if (I <= 0 || I % 128 != 0 || !fits_i32(2 * I)) return BSFP8_EINVAL;
+  // the gate/up product's operands, then the down product's (its input is
+  // staged in the workspace)
+  static const uint8_t dummy[16] __attribute__((aligned(16))) = {0};
+  int32_t r = check_gemm(xq, xs, w13, s13, nullptr, dummy, T, 2 * I, H, 128, 128, fmt);
+  if (r != BSFP8_OK) return r;
+  r = check_gemm(dummy, dummy, w2, s2, addend, y, T, H, I, 128, 128, fmt);
+  if (r != BSFP8_OK) return r;
+  if (H % (w4 ? 32 : 16) != 0) return BSFP8_EINVAL;
+  if (T > kMoeMaxTokens || k > kMoeMaxChoices) return BSFP8_ENOTSUP;
+  if (T == 0) return BSFP8_OK;
+  if (!ids || !wt || ((uintptr_t)ids & 3u) || ((uintptr_t)wt & 3u)) return BSFP8_EINVAL;
+  // the rows of h are addressed with 32-bit offsets from one base
+  if (T * k * I > 0x7fffffffLL) return BSFP8_ENOTSUP;
+  const size_t need = moe_decode_workspace_bytes(T * k, I);
+  if (workspace_bytes < need) return BSFP8_ENOSPC;
+  if (!workspace || !al16(workspace)) return BSFP8_EINVAL;
+  r = check_device(stream);
+  if (r != BSFP8_OK) return r;
+  MoeArgs a{};
+  a.xq = (const uint8_t*)xq; a.xs = xs; a.ids = ids; a.wt = wt;
+  a.w13 = (const uint8_t*)w13; a.s13 = s13; a.w2 = (const uint8_t*)w2; a.s2 = s2;
+  a.addend = (const uint16_t*)addend; a.y = (uint16_t*)y;
+  a.T = (int)T; a.k = k; a.E = E; a.H = H; a.I = I; a.fmt = fmt; a.w4 = w4;
+  a.workspace = workspace;
+  return hip_status(launch_moe_decode(a, (hipStream_t)stream));
+}
+
 }  // namespace bsfp8
 
 extern "C" {
@@ -177,6 +213,7 @@ size_t bsfp8_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int32_t
     case BSFP8_OP_FP4_GEMM: return fp4_gemm_workspace_bytes(M, N, K);
     case BSFP8_OP_FP8_FP4_GEMM: return fp8_fp4_workspace_bytes(M, N, K);
     case BSFP8_OP_LINEAR_B32: return linear_workspace_bytes(M, N, K, 32);
+    case BSFP8_OP_MOE_DECODE: return moe_decode_workspace_bytes(M, K);
     default: return (size_t)-1;
   }
 }
@@ -212,6 +249,69 @@ int32_t fp8_quant_act(const void* x, int64_t M, int64_t K, int64_t ldx, int32_t 
                                      x_scale, (hipStream_t)stream,
                                      act_scheme == BSFP8_ACT_STATIC ? x_scale : nullptr,
                                      group_k));
+}
+
+int32_t fp8_add_rmsnorm_quant(const void* x, int64_t ldx, const void* residual,
+                              void* residual_out, int64_t ldr, const void* weight, float eps,
+                              int64_t M, int64_t K, int32_t group_k, int32_t act_scheme,
+                              int32_t scale_fmt, const void* act_scale, void* y, void* xq,
+                              void* x_scale, void* stream) {
+  if (M < 0 || K < 0 || !fits_i32(M) || !fits_i32(K)) return BSFP8_EINVAL;
+  if (K % 16 != 0 || ldx < K || ldx % 8 != 0) return BSFP8_EINVAL;
+  if (!(eps > 0.0f) || !(eps <= 3.4028234663852886e38f)) return BSFP8_EINVAL;
+  if (act_scheme != BSFP8_ACT_DYNAMIC && act_scheme != BSFP8_ACT_STATIC) return BSFP8_EINVAL;
+  if (!valid_fmt(scale_fmt)) return BSFP8_EINVAL;
+  if (group_k <= 0) return BSFP8_EINVAL;
+  if (group_k != 128 && group_k != 32) return BSFP8_ENOTSUP;
+  const bool stat = act_scheme == BSFP8_ACT_STATIC;
+  if (stat && group_k != 128) return BSFP8_ENOTSUP;
+  if (M == 0) return BSFP8_OK;
+  if (K == 0) return BSFP8_EINVAL;
+  if (!x || !weight || (!residual) != (!residual_out) || (!xq) != (!x_scale) || (!xq && !y))
+    return BSFP8_EINVAL;
+  if (residual && (ldr < K || ldr % 8 != 0)) return BSFP8_EINVAL;
+  if (!al16(x) || !al16(residual) || !al16(residual_out) || !al16(weight) || !al16(y) ||
+      !al16(xq) || !al16(x_scale))
+    return BSFP8_EINVAL;
+  if (stat && xq && (!act_scale || (scale_fmt == BSFP8_SCALE_FLOAT && ((uintptr_t)act_scale & 3u))))
+    return BSFP8_EINVAL;
+  if (!fits_i32(M * ((K + group_k - 1) / group_k))) return BSFP8_EINVAL;
+  int32_t r = check_device(stream);
+  if (r != BSFP8_OK) return r;
+  NormArgs a{};
+  a.x = (const uint16_t*)x; a.ldx = ldx;
+  a.res = (const uint16_t*)residual; a.res_out = (uint16_t*)residual_out; a.ldr = ldr;
+  a.w = (const uint16_t*)weight; a.y = (uint16_t*)y; a.xq = (uint8_t*)xq; a.xs = x_scale;
+  a.xstat = stat ? act_scale : nullptr;
+  a.eps = eps; a.M = M; a.K = K; a.fmt = scale_fmt; a.group_k = group_k;
+  return hip_status(launch_add_rmsnorm_quant(a, (hipStream_t)stream));
+}
+
+int32_t moe_route_topk(const void* logits, int64_t ldl, int32_t logits_bf16, const float* bias,
+                       int64_t T, int32_t E, int32_t k, int32_t score, int32_t renorm,
+                       float scale, int32_t n_group, int32_t topk_group, int32_t* ids,
+                       float* weights, void* stream) {
+  if (T < 0 || !fits_i32(T)) return BSFP8_EINVAL;
+  if (E < 1 || E > 1024 || ldl < E) return BSFP8_EINVAL;
+  if (k < 1 || k > E) return BSFP8_EINVAL;
+  if (logits_bf16 != 0 && logits_bf16 != 1) return BSFP8_EINVAL;
+  if (renorm != 0 && renorm != 1) return BSFP8_EINVAL;
+  if (score != BSFP8_SCORE_SOFTMAX && score != BSFP8_SCORE_SIGMOID) return BSFP8_EINVAL;
+  if (n_group < 1 || E % n_group != 0 || topk_group < 1 || topk_group > n_group)
+    return BSFP8_EINVAL;
+  if (k > 64 || n_group > 64) return BSFP8_ENOTSUP;
+  if (T == 0) return BSFP8_OK;
+  if (!logits || !ids || !weights) return BSFP8_EINVAL;
+  if (((uintptr_t)logits & (logits_bf16 ? 1u : 3u)) || ((uintptr_t)bias & 3u) ||
+      ((uintptr_t)ids & 3u) || ((uintptr_t)weights & 3u))
+    return BSFP8_EINVAL;
+  int32_t r = check_device(stream);
+  if (r != BSFP8_OK) return r;
+  RouteArgs a{};
+  a.logits = logits; a.ldl = ldl; a.bf16 = logits_bf16 == 1; a.bias = bias; a.T = T; a.E = E;
+  a.k = k; a.score = score; a.renorm = renorm; a.scale = scale;
+  a.n_group = n_group; a.topk_group = topk_group; a.ids = ids; a.weights = weights;
+  return hip_status(launch_route_topk(a, (hipStream_t)stream));
 }
 
 int32_t fp8_dequant_weight(const void* wq, int64_t N, int64_t K, int32_t block_n,
@@ -406,6 +506,25 @@ int32_t fp8_grouped_gemm_silu_mul_quant(const void* xq, const void* x_scale, con
   a.seg = seg_offsets; a.E = E;
   a.hq = (uint8_t*)hq; a.hs = h_scale;
   return hip_status(launch_grouped_silu_mul_quant(a, (hipStream_t)stream));
+}
+
+int32_t fp8_moe_decode(const void* xq, const void* x_scale, const int32_t* ids,
+                       const float* weights, const void* w13, const void* w13_scale,
+                       const void* w2, const void* w2_scale, const void* addend, void* y,
+                       int64_t T, int32_t k, int64_t H, int64_t I, int32_t E, int32_t scale_fmt,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  return moe_decode_call(xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, addend, y, T, k,
+                         H, I, E, scale_fmt, false, workspace, workspace_bytes, stream);
+}
+
+int32_t fp8_fp4_moe_decode(const void* xq, const void* x_scale, const int32_t* ids,
+                           const float* weights, const void* w13, const void* w13_scale,
+                           const void* w2, const void* w2_scale, const void* addend, void* y,
+                           int64_t T, int32_t k, int64_t H, int64_t I, int32_t E,
+                           int32_t scale_fmt, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return moe_decode_call(xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, addend, y, T, k,
+                         H, I, E, scale_fmt, true, workspace, workspace_bytes, stream);
 }
 
 int32_t fp4_quant(const void* x, int64_t R, int64_t K, int32_t dynamic_tscale, void* q4,

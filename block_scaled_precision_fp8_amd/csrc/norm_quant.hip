@@ -1,0 +1,196 @@
+// Residual addition, RMS norm and FP8 quantization in one pass.
+//
+//   h  = bf16(x + residual)                 (h = x without a residual)
+//   rs = 1 / sqrt(sum_k h^2 / K + eps)
+//   y  = fl32(h w rs)
+//   codes, scales = the activation codec of fp8_quant_act on the fp32 y
+//
+// Bound by HBM: per element 2 bytes of x, 2 of the residual and 2 of h, 1
+// byte of codes (and 2 of the optional bf16 y).
+//
+// The sum of squares is held in 64 bits (a square of a bf16 value is exact
+// there, and the vector ALU has the time: one conversion and one FMA per
+// element under the loads).  h w is exact in fp32 (8 + 8 significant bits),
+// so with rs as a sum of two fp32 values y is the correctly rounded h w rs:
+// codes and scales do not depend on how a row is dealt to lanes.  y is not
+// rounded to bf16 before it is quantized: the codes then carry one rounding,
+// and a group's scale does not jump by a bf16 step.
+#include "bsfp8_internal.h"
+
+namespace bsfp8 {
+namespace detail {
+
+enum { kNormPlain = 0, kNormG128 = 1, kNormG32 = 2, kNormStatic = 3 };
+
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  return f32_to_bf16(bf16_lo(a) + bf16_lo(b)) | (f32_to_bf16(bf16_hi(a) + bf16_hi(b)) << 16);
+}
+__device__ __forceinline__ uint4 add_bf16x8(uint4 a, uint4 b) {
+  return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z),
+                    add_bf16x2(a.w, b.w));
+}
+
+__device__ __forceinline__ double square_sum8(uint4 v, double s) {
+  const Unpacked u = unpack8(v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fma((double)u.f[i], (double)u.f[i], s);
+  return s;
+}
+
+struct RowScale { float hi, lo; };   // rs = hi + lo
+
+// Eight values of a row: y, its codes and scale, the stores.  Called by all
+// lanes of the group together (lanes past the row pass valid = false).
+template <int FMT, int MODE>
+__device__ __forceinline__ void norm_out8(uint4 hv, uint4 wv, RowScale rs, bool valid, int c,
+                                          const void* xstat, uint16_t* y, uint8_t* xq, void* xs,
+                                          int64_t m, int64_t K) {
+  const Unpacked h = unpack8(hv), w = unpack8(wv);
+  Unpacked v;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float p = h.f[i] * w.f[i];
+    // the sign is p's: two zeros of unlike signs would add to +0
+    v.f[i] = valid ? copysignf(fmaf(p, rs.hi, p * rs.lo), p) : 0.0f;
+  }
+  const int64_t k0 = (int64_t)c * 8;
+  if (y && valid) {
+    uint4 o;
+    o.x = f32_to_bf16(v.f[0]) | (f32_to_bf16(v.f[1]) << 16);
+    o.y = f32_to_bf16(v.f[2]) | (f32_to_bf16(v.f[3]) << 16);
+    o.z = f32_to_bf16(v.f[4]) | (f32_to_bf16(v.f[5]) << 16);
+    o.w = f32_to_bf16(v.f[6]) | (f32_to_bf16(v.f[7]) << 16);
+    *(uint4*)(y + m * K + k0) = o;
+  }
+  if constexpr (MODE != kNormPlain) {
+    constexpr int GK = MODE == kNormG32 ? 32 : 128;
+    constexpr int LPG = GK / 8;
+    float sf = 0.0f;
+    int se = 0;
+    uint2 codes;
+    if constexpr (MODE == kNormStatic) {
+      if (FMT == 0) sf = *(const float*)xstat;
+      else se = (int)*(const uint8_t*)xstat - 127;
+      codes.x = act_encode4<FMT>(v.f[0], v.f[1], v.f[2], v.f[3], sf, se);
+      codes.y = act_encode4<FMT>(v.f[4], v.f[5], v.f[6], v.f[7], sf, se);
+    } else {
+      float amax = amax8(v);
+#pragma unroll
+      for (int o = 1; o < LPG; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 16));
+      codes = encode8<FMT>(v, amax, &sf, &se);
+    }
+    if (valid) {
+      *(uint2*)(xq + m * K + k0) = codes;
+      if ((c & (LPG - 1)) == 0) {
+        const int64_t gi = m * ((K + GK - 1) / GK) + k0 / GK;
+        if (FMT == 0) ((float*)xs)[gi] = sf;
+        else ((uint8_t*)xs)[gi] = (uint8_t)(se + 127);
+      }
+    }
+  }
+}
+
+// TPR lanes per row, NC chunks of eight values per lane held in registers;
+// NC = 0: rows of any length, h read a second time.
+template <int FMT, int MODE, int TPR, int NC>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_quant_kernel(NormArgs a) {
+  constexpr int RPW = TPR < 256 ? 256 / TPR : 1;   // rows per workgroup
+  constexpr int WPR = TPR / 64;                    // waves per row
+  __shared__ double red[WPR > 1 ? WPR : 1];
+  const int tr = threadIdx.x % TPR;
+  const int64_t m = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
+  if (m >= a.M) return;                            // whole waves: RPW > 1 has one wave per row
+  const int C = (int)(a.K / 8);
+  const uint16_t* xr = a.x + m * a.ldx;
+  const uint16_t* rr = a.res ? a.res + m * a.ldr : nullptr;
+  uint16_t* ro = a.res ? a.res_out + m * a.ldr : nullptr;
+  double ss = 0.0;
+  uint4 hv[NC > 0 ? NC : 1], wv[NC > 0 ? NC : 1];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if constexpr (NC > 0) {
+    uint4 rv[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tr + i * TPR;
+      hv[i] = c < C ? ld_stream16(xr + (int64_t)c * 8) : zero;
+      rv[i] = (rr && c < C) ? ld_stream16(rr + (int64_t)c * 8) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tr + i * TPR;
+      wv[i] = c < C ? *(const uint4*)(a.w + (int64_t)c * 8) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tr + i * TPR;
+      if (rr) {
+        hv[i] = add_bf16x8(hv[i], rv[i]);
+        if (c < C) *(uint4*)(ro + (int64_t)c * 8) = hv[i];
+      }
+      ss = square_sum8(hv[i], ss);
+    }
+  } else {
+    for (int c = tr; c < C; c += TPR) {
+      uint4 v = *(const uint4*)(xr + (int64_t)c * 8);
+      if (rr) {
+        v = add_bf16x8(v, *(const uint4*)(rr + (int64_t)c * 8));
+        *(uint4*)(ro + (int64_t)c * 8) = v;
+      }
+      ss = square_sum8(v, ss);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) ss += __shfl_xor(ss, o, 64);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ss;
+    __syncthreads();
+    ss = red[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) ss += red[i];
+  }
+  const double r = 1.0 / sqrt(ss / (double)a.K + (double)a.eps);
+  RowScale rs;
+  rs.hi = (float)r;
+  rs.lo = (float)(r - (double)rs.hi);
+  if constexpr (NC > 0) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tr + i * TPR;
+      norm_out8<FMT, MODE>(hv[i], wv[i], rs, c < C, c, a.xstat, a.y, a.xq, a.xs, m, a.K);
+    }
+  } else {
+    // the lane reads back what it wrote itself (or x again)
+    const uint16_t* hr = ro ? ro : xr;
+    for (int c0 = 0; c0 < C; c0 += TPR) {
+      const int c = c0 + tr;
+      const uint4 h = c < C ? *(const uint4*)(hr + (int64_t)c * 8) : zero;
+      const uint4 w = c < C ? *(const uint4*)(a.w + (int64_t)c * 8) : zero;
+      norm_out8<FMT, MODE>(h, w, rs, c < C, c, a.xstat, a.y, a.xq, a.xs, m, a.K);
+    }
+  }
+}
+
+template <int FMT, int MODE>
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+#define BSFP8_NORM(TPR, NC)                                                                  \
+  hipLaunchKernelGGL((norm_quant_kernel<FMT, MODE, TPR, NC>),                                \
+                     dim3((unsigned)(TPR < 256 ? (a.M + 256 / TPR - 1) / (256 / TPR) : a.M)), \
+                     dim3(TPR < 256 ? 256 : TPR), 0, s, a)
+  const int64_t C = a.K / 8;
+  if (C <= 256 * 4) BSFP8_NORM(256, 4);
+  else BSFP8_NORM(256, 0);
+#undef BSFP8_NORM
+  return hipGetLastError();
+}
+
+}  // namespace detail
+using namespace detail;
+
+hipError_t launch_add_rmsnorm_quant(const NormArgs& a, hipStream_t s) {
+  if (!a.xq) return launch_norm<0, kNormPlain>(a, s);
+  if (a.xstat) return a.fmt == 0 ? launch_norm<0, kNormStatic>(a, s) : launch_norm<1, kNormStatic>(a, s);
+  if (a.group_k == 32) return a.fmt == 0 ? launch_norm<0, kNormG32>(a, s) : launch_norm<1, kNormG32>(a, s);
+  return a.fmt == 0 ? launch_norm<0, kNormG128>(a, s) : launch_norm<1, kNormG128>(a, s);
+}
+
+}  // namespace bsfp8

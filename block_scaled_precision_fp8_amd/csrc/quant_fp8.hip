@@ -24,48 +24,6 @@ namespace detail {
 constexpr int kActUnroll = 4;   // loads in flight per lane
 constexpr int kActRows = 2;     // row sets per workgroup
 
-struct Unpacked { float f[8]; };
-
-__device__ __forceinline__ Unpacked unpack8(uint4 v) {
-  Unpacked u;
-  u.f[0] = bf16_lo(v.x); u.f[1] = bf16_hi(v.x);
-  u.f[2] = bf16_lo(v.y); u.f[3] = bf16_hi(v.y);
-  u.f[4] = bf16_lo(v.z); u.f[5] = bf16_hi(v.z);
-  u.f[6] = bf16_lo(v.w); u.f[7] = bf16_hi(v.w);
-  return u;
-}
-
-__device__ __forceinline__ float amax8(const Unpacked& u) {
-  float a = fabsf(u.f[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) a = fmaxf(a, fabsf(u.f[i]));
-  return a;
-}
-
-// Encode eight values of one group with the group's scale.  Returns the
-// codes packed little-endian; writes the stored scale representation.
-// fp32 scales divide by the correctly rounded reciprocal with one exact
-// correction (div_by_rcp: the same E4M3 codes as IEEE x / s for a normal s,
-// at four operations per value instead of an IEEE division each); a
-// subnormal scale divides directly.
-template <int FMT>
-__device__ __forceinline__ uint2 encode8(const Unpacked& u, float amax, float* s_f32, int* s_exp) {
-  const float s = FMT == 0 ? act_scale_f32(amax) : 0.0f;
-  const int e = FMT == 0 ? 0 : ue8m0_exp(amax);
-  *s_f32 = s;
-  *s_exp = e;
-  uint2 r;
-  if (FMT == 0 && s >= kMinNormal) {
-    const RcpDiv dv = rcp_div(s);
-    r.x = act_encode4_rcp<FMT>(u.f[0], u.f[1], u.f[2], u.f[3], dv, e);
-    r.y = act_encode4_rcp<FMT>(u.f[4], u.f[5], u.f[6], u.f[7], dv, e);
-  } else {
-    r.x = act_encode4<FMT>(u.f[0], u.f[1], u.f[2], u.f[3], s, e);
-    r.y = act_encode4<FMT>(u.f[4], u.f[5], u.f[6], u.f[7], s, e);
-  }
-  return r;
-}
-
 // One 16-lane quarter-wave owns 128 consecutive values of one row: each lane
 // holds eight consecutive bf16 values (one 16-byte load).  A workgroup of 16
 // quarters covers QG consecutive 128-value chunks of RQ rows (QG * RQ = 16)

@@ -20,13 +20,16 @@ ACT_DYNAMIC, ACT_STATIC = 0, 1
 OP_BLOCK_GEMM, OP_LINEAR, OP_GROUPED_GEMM, OP_FP4_QUANT, OP_FP4_GEMM, OP_FP8_FP4_GEMM = \
     0, 1, 2, 3, 4, 5
 OP_LINEAR_B32 = 6
+OP_MOE_DECODE = 7
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GEMM_NONE, GEMM_TILE_128x256, GEMM_TILE_256x256, GEMM_DECODE = 0, 2, 3, 4
 
 EXPORTS = ("bsfp8_version", "bsfp8_status_string", "bsfp8_workspace_size", "bsfp8_gemm_kernel",
            "fp8_quant_act", "fp8_quant_weight", "fp8_block_gemm", "fp8_linear",
            "fp8_grouped_gemm", "fp4_quant", "fp4_group_gemm", "fp8_dequant_weight",
            "fp8_scale_to_ue8m0", "mxfp4_quant_weight", "fp8_fp4_gemm",
-           "fp8_grouped_gemm_silu_mul_quant", "fp8_linear_noalloc", "fp8_fp4_grouped_gemm")
+           "fp8_grouped_gemm_silu_mul_quant", "fp8_linear_noalloc", "fp8_fp4_grouped_gemm",
+           "fp8_add_rmsnorm_quant", "moe_route_topk", "fp8_moe_decode", "fp8_fp4_moe_decode")
 NOALLOC_SCRATCH_BYTES = 32 << 20     # BSFP8_NOALLOC_SCRATCH_BYTES
 
 
@@ -39,6 +42,7 @@ class BsFp8Error(RuntimeError):
 _lib = None
 
 _P = ctypes.c_void_p
+_F32 = ctypes.c_float
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
@@ -65,6 +69,14 @@ _SIGS = {
     "fp8_fp4_grouped_gemm": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _I32, _P]),
     "fp8_grouped_gemm": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _I32, _I32,
                                 _I32, _P, _SZ, _P]),
+    "fp8_add_rmsnorm_quant": (_I32, [_P, _I64, _P, _P, _I64, _P, _F32, _I64, _I64, _I32, _I32,
+                                     _I32, _P, _P, _P, _P, _P]),
+    "moe_route_topk": (_I32, [_P, _I64, _I32, _P, _I64, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
+                              _P, _P, _P]),
+    "fp8_moe_decode": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64,
+                              _I32, _I32, _P, _SZ, _P]),
+    "fp8_fp4_moe_decode": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64,
+                                  _I32, _I32, _P, _SZ, _P]),
     "fp4_quant": (_I32, [_P, _I64, _I64, _I32, _P, _P, _P, _P, _SZ, _P]),
     "fp4_group_gemm": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
 }
@@ -262,3 +274,58 @@ def fp4_group_gemm(xq4, x_gscale, x_tscale, wq4, w_gscale, w_tscale, y, workspac
     _check("fp4_group_gemm", load().fp4_group_gemm(
         _ptr(xq4), _ptr(x_gscale), _ptr(x_tscale), _ptr(wq4), _ptr(w_gscale), _ptr(w_tscale),
         _ptr(y), M, N, K, _ptr(ws), wsb, _stream(stream)))
+
+
+def fp8_add_rmsnorm_quant(x, weight, xq, x_scale, residual=None, residual_out=None, y=None,
+                          eps=1e-6, group_k=128, act_scheme=ACT_DYNAMIC, scale_fmt=SCALE_FLOAT,
+                          act_scale=None, stream=None):
+    """x: bf16 (M, K) with row stride ldx; weight bf16 (K,); residual and
+    residual_out bf16 (M, K) with one row stride; y bf16 (M, K) out or None;
+    xq uint8 (M, K) and x_scale (M, G) out, or both None; act_scale as for
+    fp8_linear."""
+    M, K = x.shape
+    ldr = K if residual is None else residual.stride(0)
+    if residual is not None and residual_out is not None and residual_out.stride(0) != ldr and M > 1:
+        raise ValueError("residual and residual_out need the same row stride")
+    _check("fp8_add_rmsnorm_quant", load().fp8_add_rmsnorm_quant(
+        _ptr(x), x.stride(0), _ptr(residual), _ptr(residual_out), ldr, _ptr(weight), eps, M, K,
+        group_k, act_scheme, scale_fmt, _ptr(act_scale), _ptr(y), _ptr(xq), _ptr(x_scale),
+        _stream(stream)))
+
+
+def moe_route_topk(logits, ids, weights, bias=None, score=SCORE_SOFTMAX, renorm=True, scale=1.0,
+                   n_group=1, topk_group=1, stream=None):
+    """logits: fp32 or bf16 (T, E) with row stride ldl; bias fp32 (E,) or
+    None; ids int32 (T, k) out; weights fp32 (T, k) out."""
+    T, E = logits.shape
+    _check("moe_route_topk", load().moe_route_topk(
+        _ptr(logits), logits.stride(0), int(logits.element_size() == 2), _ptr(bias), T, E,
+        ids.shape[1], score, int(renorm), scale, n_group, topk_group, _ptr(ids), _ptr(weights),
+        _stream(stream)))
+
+
+def _moe_decode(fn, xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, I, addend,
+                scale_fmt, workspace, stream):
+    T, H = xq.shape
+    k = ids.shape[1]
+    ws, wsb = _workspace(OP_MOE_DECODE, T * k, H, I, 0, workspace, xq.device)
+    _check(fn, getattr(load(), fn)(
+        _ptr(xq), _ptr(x_scale), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(w13_scale), _ptr(w2),
+        _ptr(w2_scale), _ptr(addend), _ptr(y), T, k, H, I, w13.shape[0], scale_fmt, _ptr(ws), wsb,
+        _stream(stream)))
+
+
+def fp8_moe_decode(xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, addend=None,
+                   scale_fmt=SCALE_FLOAT, workspace=None, stream=None):
+    """xq (T, H) E4M3; ids int32 (T, k); weights fp32 (T, k); w13 (E, 2I, H);
+    w2 (E, H, I); addend bf16 (T, H) or None; y bf16 (T, H) out."""
+    _moe_decode("fp8_moe_decode", xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y,
+                w2.shape[2], addend, scale_fmt, workspace, stream)
+
+
+def fp8_fp4_moe_decode(xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, addend=None,
+                       scale_fmt=SCALE_FLOAT, workspace=None, stream=None):
+    """As fp8_moe_decode with MXFP4 experts: w13 uint8 (E, 2I, H/2), w13_scale
+    uint8 (E, 2I, H/32); w2 uint8 (E, H, I/2), w2_scale uint8 (E, H, I/32)."""
+    _moe_decode("fp8_fp4_moe_decode", xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y,
+                2 * w2.shape[2], addend, scale_fmt, workspace, stream)

@@ -67,6 +67,9 @@ typedef enum { BSFP8_SCALE_FLOAT = 0, BSFP8_SCALE_UE8M0 = 1 } bsfp8_scale_fmt;
    and do not depend on the scheme. */
 typedef enum { BSFP8_ACT_DYNAMIC = 0, BSFP8_ACT_STATIC = 1 } bsfp8_act_scheme;
 
+/* Scores of moe_route_topk. */
+typedef enum { BSFP8_SCORE_SOFTMAX = 0, BSFP8_SCORE_SIGMOID = 1 } bsfp8_score;
+
 /* Operation ids for bsfp8_workspace_size. */
 typedef enum {
   BSFP8_OP_BLOCK_GEMM = 0,
@@ -75,7 +78,8 @@ typedef enum {
   BSFP8_OP_FP4_QUANT = 3,
   BSFP8_OP_FP4_GEMM = 4,
   BSFP8_OP_FP8_FP4_GEMM = 5,
-  BSFP8_OP_LINEAR_B32 = 6      /* fp8_linear with (32, 32) weight blocks */
+  BSFP8_OP_LINEAR_B32 = 6,     /* fp8_linear with (32, 32) weight blocks */
+  BSFP8_OP_MOE_DECODE = 7      /* fp8_moe_decode and fp8_fp4_moe_decode  */
 } bsfp8_op;
 
 /* Kernels fp8_block_gemm / fp8_linear choose between (bsfp8_gemm_kernel). */
@@ -127,6 +131,77 @@ BSFP8_API const char* bsfp8_status_string(int32_t status);
 BSFP8_API int32_t fp8_quant_act(const void* x, int64_t M, int64_t K, int64_t ldx,
                       int32_t group_k, int32_t act_scheme, int32_t scale_fmt,
                       void* xq, void* x_scale, void* stream);
+
+/*
+ * fp8_add_rmsnorm_quant -- the step before a layer's linears: the residual's
+ * addition, RMS norm and the activation quantization, in one pass.
+ *
+ *   h  = bf16(x + residual)          (h = x when residual is NULL)
+ *   y  = fl32(h * weight / sqrt(mean_k(h^2) + eps))
+ *   codes, scales = those of fp8_quant_act's codec (per group_k group, or
+ *   the static scale) applied to the fp32 row y, which is not rounded to
+ *   bf16 in between.
+ * The mean is held in 64 bits and y is correctly rounded (one fp32 rounding
+ * of the exact product), so the results do not depend on the row's length
+ * or on how it is dealt to the hardware.
+ *
+ *   x            bf16 [M][ldx], read-only; K % 16 == 0, ldx >= K, ldx % 8 == 0.
+ *   residual     bf16 [M][ldr] or NULL; residual_out bf16 [M][ldr], out: h.
+ *                Both or neither; residual_out may be residual itself (the
+ *                row is updated in place).  ldr is ignored when NULL.
+ *   weight       bf16 [K].
+ *   eps          finite, > 0.
+ *   group_k, act_scheme, scale_fmt   as for fp8_quant_act.
+ *   act_scale    STATIC: the calibrated scale (device; fp32 s > 0, 4-byte
+ *                aligned, or the E8M0 byte); every entry of x_scale is set
+ *                to it.  DYNAMIC: ignored, may be NULL.
+ *   y            out, bf16 [M][K] (the norm rounded to bf16, e.g. for a
+ *                router), or NULL.
+ *   xq, x_scale  out, as fp8_quant_act; both NULL for the norm alone (then
+ *                y is required and the quantization arguments are only
+ *                checked).
+ * Outputs must not overlap inputs or each other, except residual_out =
+ * residual.  NaN and Inf are outside the contract, as for fp8_quant_act.
+ * Errors: EINVAL (null pointers, sizes, strides, eps, enums, misalignment);
+ * ENOTSUP (group_k other than 128 or 32, or 32 with STATIC).
+ */
+BSFP8_API int32_t fp8_add_rmsnorm_quant(const void* x, int64_t ldx, const void* residual,
+                                        void* residual_out, int64_t ldr, const void* weight,
+                                        float eps, int64_t M, int64_t K, int32_t group_k,
+                                        int32_t act_scheme, int32_t scale_fmt,
+                                        const void* act_scale, void* y, void* xq,
+                                        void* x_scale, void* stream);
+
+/*
+ * moe_route_topk -- a router's scores to each token's k experts and weights,
+ * as fp8_moe_decode reads them.  For every row l of the logits:
+ *
+ *   s   = softmax(l)  or  sigmoid(l)
+ *   key = l when bias is NULL and n_group == 1 (both scores rise with l),
+ *         else s + bias (bias 0 when NULL), held in 64 bits
+ *   n_group > 1: the E experts form n_group groups of E / n_group
+ *         neighbours; a group's score is the sum of its two largest keys,
+ *         and only the topk_group best groups keep their experts
+ *   ids = the k experts with the largest keys, in descending order
+ *   weights = s[ids], divided by their sum when renorm is 1, times scale
+ * Ties go to the lower expert or group.  An expert whose logit is NaN or
+ * -inf, or whose key is, is never chosen (NaN and -inf logits count as
+ * score 0); a slot with no expert left gets id -1 and weight 0.
+ *
+ *   logits       [T][ldl], fp32 or (logits_bf16 = 1) bf16, ldl >= E, any
+ *                ldl; aligned to its type only.
+ *   bias         fp32 [E] or NULL: enters the choice, not the weights.
+ *   E, k         1 <= k <= E <= 1024, k <= 64.
+ *   n_group      divides E, <= 64; 1 <= topk_group <= n_group.
+ *   ids          out, int32 [T][k];  weights out, fp32 [T][k].
+ * Errors: EINVAL (sizes, null pointers, enums, alignment); ENOTSUP (k > 64,
+ * n_group > 64).
+ */
+BSFP8_API int32_t moe_route_topk(const void* logits, int64_t ldl, int32_t logits_bf16,
+                                 const float* bias, int64_t T, int32_t E, int32_t k,
+                                 int32_t score, int32_t renorm, float scale, int32_t n_group,
+                                 int32_t topk_group, int32_t* ids, float* weights,
+                                 void* stream);
 
 /*
  * fp8_quant_weight -- per 2D block weight quantization
@@ -288,6 +363,62 @@ BSFP8_API int32_t fp8_grouped_gemm_silu_mul_quant(const void* xq, const void* x_
                                         int64_t K, int32_t scale_fmt, void* stream);
 
 /*
+ * fp8_moe_decode -- a whole MoE layer for a few tokens, straight from the
+ * tokens' expert ids (no sorting, no segment offsets):
+ *
+ *   slot (t, j) with e = ids[t][j] in [0, E):
+ *     g = (X W13_e[0:I]^T)[t],  u = (X W13_e[I:2I]^T)[t]
+ *     (hq, hs) = the 1 x 128 activation quantization of bf16(silu(g) * u)
+ *     d(t, j)  = hq W2_e^T                                  (fp32)
+ *   y[t] = bf16_rne( addend[t] + sum_j weights[t][j] * d(t, j) )
+ *
+ * that is fp8_grouped_gemm_silu_mul_quant, fp8_grouped_gemm and the
+ * weighted sum, without rounding d to bf16.  Every expert that some token
+ * names is read once.  Deterministic: the same call gives the same bits.
+ *
+ *   xq, x_scale  as written by fp8_quant_act or fp8_add_rmsnorm_quant
+ *                (T rows of H, 1 x 128 groups).
+ *   ids          DEVICE int32 [T][k];  weights DEVICE fp32 [T][k].  A slot
+ *                whose id is outside [0, E) is skipped and its weight not
+ *                used: padding tokens, or experts that live on another
+ *                device.  A token may name an expert more than once.
+ *   w13          E4M3 [E][2I][H], gate rows then up rows; w13_scale
+ *                [E][2I/128][ceil(H/128)] (fp32 | UE8M0).
+ *   w2           E4M3 [E][H][I]; w2_scale [E][ceil(H/128)][I/128].
+ *   addend       bf16 [T][H] (a shared expert's output, or the residual)
+ *                or NULL; may be y itself.
+ *   y            out, bf16 [T][H]; a token with no slot left gets its
+ *                addend, or 0.
+ *   T <= 128, k <= 16 (ENOTSUP beyond: sort the rows and use
+ *   fp8_grouped_gemm); H % 16 == 0, I % 128 == 0, 1 <= E <= 1024.
+ *   workspace    >= bsfp8_workspace_size(BSFP8_OP_MOE_DECODE, T * k, H, I, 0).
+ * Errors: EINVAL (sizes, null pointers, enums, misalignment); ENOTSUP (T, k,
+ * H or I > 2^22, T k I >= 2^31); ENOSPC.
+ */
+BSFP8_API int32_t fp8_moe_decode(const void* xq, const void* x_scale, const int32_t* ids,
+                                 const float* weights, const void* w13, const void* w13_scale,
+                                 const void* w2, const void* w2_scale, const void* addend,
+                                 void* y, int64_t T, int32_t k, int64_t H, int64_t I, int32_t E,
+                                 int32_t scale_fmt, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * fp8_fp4_moe_decode -- fp8_moe_decode with MXFP4 expert weights (those of
+ * fp8_fp4_grouped_gemm):
+ *   w13          uint8 [E][2I][H/2], w13_scale E8M0 bytes [E][2I][H/32];
+ *   w2           uint8 [E][H][I/2],  w2_scale  E8M0 bytes [E][H][I/32]
+ * as mxfp4_quant_weight writes them per expert; H % 32 == 0.  scale_fmt is
+ * that of x_scale and of h's scales.  The rest as fp8_moe_decode.
+ */
+BSFP8_API int32_t fp8_fp4_moe_decode(const void* xq, const void* x_scale, const int32_t* ids,
+                                     const float* weights, const void* w13,
+                                     const void* w13_scale, const void* w2,
+                                     const void* w2_scale, const void* addend, void* y,
+                                     int64_t T, int32_t k, int64_t H, int64_t I, int32_t E,
+                                     int32_t scale_fmt, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * fp4_quant -- NVFP4-style quantization ([NVFP4]: 4-bit float weights and
  * input activations in 16-element groups, group_size 16): E2M1 codes with
  * an E4M3 scale per 16-element group and one fp32 scale per tensor.
@@ -422,8 +553,9 @@ BSFP8_API int32_t fp8_scale_to_ue8m0(const float* scale, int64_t n, void* out, v
 
 /*
  * Bytes of device workspace the given operation needs for this problem
- * (0 if none).  `op` is a bsfp8_op; M is T for the grouped GEMM and R for
- * fp4_quant; E is used by the grouped GEMM only.  Returns (size_t)-1 for an
+ * (0 if none).  `op` is a bsfp8_op; M is T for the grouped GEMM, R for
+ * fp4_quant and T * k for the MoE layer (N = H, K = I); E is used by the
+ * grouped GEMM only.  Returns (size_t)-1 for an
  * unknown op or negative sizes.
  */
 BSFP8_API size_t bsfp8_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K,
