@@ -283,6 +283,7 @@ struct RouteArgs {
 
 constexpr int kMoeMaxTokens = 128;   // tokens of one moe_decode call
 constexpr int kMoeMaxChoices = 16;   // experts per token
+constexpr int64_t kMoeMaxRowBytes = int64_t(1) << 30;   // codes of h (T k I)
 struct MoeArgs {
   const uint8_t* xq;         // [T][H] and its scales
   const void* xs;

@@ -171,7 +171,7 @@ static int32_t moe_decode_call(const void* xq, const void* xs, const int32_t* id
   if (T == 0) return BSFP8_OK;
   if (!ids || !wt || ((uintptr_t)ids & 3u) || ((uintptr_t)wt & 3u)) return BSFP8_EINVAL;
   // the rows of h are addressed with 32-bit offsets from one base
-  if (T * k * I > 0x7fffffffLL) return BSFP8_ENOTSUP;
+  if (T * k * I > kMoeMaxRowBytes) return BSFP8_ENOTSUP;
   const size_t need = moe_decode_workspace_bytes(T * k, I);
   if (workspace_bytes < need) return BSFP8_ENOSPC;
   if (!workspace || !al16(workspace)) return BSFP8_EINVAL;

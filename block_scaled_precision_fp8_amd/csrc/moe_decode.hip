@@ -8,18 +8,23 @@
 // Bound by HBM: every expert that a token chose is read once, 3 H I bytes
 // (half with MXFP4 weights); the tokens' own data is small and stays in L2.
 //
-//   moe_gate_up_kernel  one workgroup per (expert, 16 gate rows and the 16 up
-//                       rows beside them): its waves deal the K blocks, each
-//                       weight byte is read once for up to 64 of the expert's
-//                       slots, and the waves' partial tiles meet in LDS.
-//                       Also writes the slots sorted by expert.
-//   quant_act_kernel    h to codes and scales
-//   moe_down_kernel     one workgroup per 16 output features: its waves deal
-//                       the K blocks of all experts' rows, each adds its
-//                       weighted products to its own fp32 sums per token in
-//                       LDS, which are joined in a fixed order: no atomics,
-//                       the same bits on every run.
+//   moe_gate_up_kernel  one workgroup per CU; its tasks are (segment of an
+//                       expert's slots, 16 columns of h), dealt in equal
+//                       contiguous shares.  Writes h in bf16, and the slots
+//                       sorted by expert for the next launch.
+//   quant_act_kernel    h to codes and scales, where the down launch does not
+//                       do that itself
+//   moe_down_kernel     one workgroup per 16 output features; its tasks are
+//                       the segments.  Each wave adds its weighted products
+//                       to its own fp32 sums per token in LDS, which are
+//                       joined in a fixed order.
+//
+// In both a workgroup's waves take equal contiguous shares of its (task, K
+// block) pairs and stream the weights through a ring of registers across
+// tasks, with no barrier until the end.  No atomics: the same bits on every
+// run.
 #include <algorithm>
+#include <type_traits>
 
 #include "bsfp8.h"
 #include "bsfp8_internal.h"
@@ -31,336 +36,613 @@ constexpr int kMoeWaves = 8;
 constexpr int kMoeThreads = 64 * kMoeWaves;
 constexpr int kMoeMaxSlots = kMoeMaxTokens * kMoeMaxChoices;
 
+// A sorted slot as one word: slot, its token, and (down launch) which of its
+// token's rows in the expert's run it is.
+static_assert(kMoeMaxSlots <= 1 << 11 && kMoeMaxTokens <= 1 << 7, "slot word");
+__device__ __forceinline__ int slot_word(int slot, int k) { return slot | (slot / k) << 11; }
+__device__ __forceinline__ int slot_of(int w) { return w & 0x7ff; }
+__device__ __forceinline__ int token_of(int w) { return w >> 11 & 0x7f; }
+__device__ __forceinline__ int nth_of(int w) { return w >> 18; }      // -1 for w = -1
+
 // The slots in expert order, left by the gate/up launch for the down launch.
 struct MoePlan {
   int32_t total;                       // slots with an expert here
   int32_t pad[3];
   int32_t expert[kMoeMaxSlots];        // [total]
-  int32_t slot[kMoeMaxSlots];
+  int32_t slot[kMoeMaxSlots];          // slot words
 };
 
-// One K block's operands of a 16-row weight tile: 32 codes per lane (MXFP4:
-// 16 bytes and their scale byte).
-struct WFrag {
-  uint4 a, b;
-  int s;
-};
+// ---- operands ----------------------------------------------------------
+// The products run on the bf16 MFMA: every E4M3 and E2M1 value is a bf16
+// value, and the instruction keeps 24 bits below a group's largest product.
+// The FP8 MFMAs keep 13 (measured: 2^-16 of sum |a b| off for normal data,
+// 2^-13 with 50-fold outlier channels, against 2^-24 here), which moves
+// codes of h.  The conversions are free under the weight stream.
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+struct BFrag { bf8 v[4]; };            // 32 values of one row
 
 __device__ __forceinline__ uint4 ld_buf16(__amdgpu_buffer_rsrc_t r, uint32_t o) {
   const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0);
   return make_uint4(t.x, t.y, t.z, t.w);
 }
-// weights are read once: non-temporal
-__device__ __forceinline__ uint4 ld_buf16_nt(__amdgpu_buffer_rsrc_t r, uint32_t o) {
-  const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 2);
-  return make_uint4(t.x, t.y, t.z, t.w);
+
+__device__ __forceinline__ bf8 cvt_e4m3x8(uint32_t a, uint32_t b) {
+  const bf2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+  const bf2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+  const bf2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+  const bf2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+  return bf8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+__device__ __forceinline__ bf8 cvt_e2m1x8(uint32_t a, float s) {
+  const bf2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, s, 0);
+  const bf2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, s, 1);
+  const bf2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, s, 2);
+  const bf2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, s, 3);
+  return bf8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// 16 rows of one expert's weight (rows `row0`..) as buffers: codes, and with
-// MXFP4 their scale bytes.  Offsets past the tile's end read zeros.
+// A stored scale, as loaded: the fp32 value, or the E8M0 byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t ld_scale(__amdgpu_buffer_rsrc_t r, uint32_t i, bool ok) {
+  if (FMT == 0) return __builtin_amdgcn_raw_buffer_load_b32(r, ok ? i * 4 : kOOB, 0, 0);
+  return (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, ok ? i : kOOB, 0, 0);
+}
+template <int FMT>
+__device__ __forceinline__ float scale_value(uint32_t s) {
+  return FMT == 0 ? __uint_as_float(s) : e8m0_f32(s);
+}
+
+// One K block of a 16-row weight tile: a lane's 32 codes of row l16, with
+// MXFP4 their scale byte.  FP8: K 16 g4 .. + 15 and 64 + 16 g4 .. + 15 (the
+// order within a block is free while rows and weights agree; four lanes then
+// read 64 bytes in a piece).  MXFP4: the group K 32 g4 .. + 31.
+template <bool W4>
+struct WFrag {
+  uint4 c[W4 ? 1 : 2];
+  uint32_t s[W4 ? 1 : 0];
+  __device__ __forceinline__ BFrag bf16() const {
+    BFrag f;
+    if constexpr (W4) {
+      const float sc = __uint_as_float(s[0] << 23);  // the conversion reads the exponent field
+      f.v[0] = cvt_e2m1x8(c[0].x, sc); f.v[1] = cvt_e2m1x8(c[0].y, sc);
+      f.v[2] = cvt_e2m1x8(c[0].z, sc); f.v[3] = cvt_e2m1x8(c[0].w, sc);
+    } else {
+      f.v[0] = cvt_e4m3x8(c[0].x, c[0].y); f.v[1] = cvt_e4m3x8(c[0].z, c[0].w);
+      f.v[2] = cvt_e4m3x8(c[1].x, c[1].y); f.v[3] = cvt_e4m3x8(c[1].z, c[1].w);
+    }
+    return f;
+  }
+};
+template <bool W4>
+__device__ __forceinline__ uint32_t piece0(int g4) { return W4 ? 32 * g4 : 16 * g4; }
+template <bool W4>
+__device__ __forceinline__ uint32_t piece1(int g4) { return W4 ? 32 * g4 + 16 : 64 + 16 * g4; }
+
+// 16 rows of one expert's weight.  In a row's last, partial K block a lane
+// reads on into the next row: finite values, which meet zeros of the tokens'
+// rows.  Blocks from KB on give zeros and no traffic.
 template <bool W4>
 struct WTile {
   __amdgpu_buffer_rsrc_t codes, scales;
-  uint32_t lo, slo;
-  int64_t K;
-  __device__ __forceinline__ WTile(const uint8_t* w, const void* sc, int64_t row0, int rows,
-                                   int64_t K_, int l16)
-      : K(K_) {
+  uint32_t lo, slo, K;
+  int KB, g4;
+  __device__ __forceinline__ void init(int64_t K_, int lane) {
+    K = (uint32_t)K_;
+    KB = (int)((K_ + 127) / 128);
+    g4 = lane >> 4;
+    lo = (uint32_t)((lane & 15) * (W4 ? K_ / 2 : K_)) + g4 * 16;
+    slo = (uint32_t)((lane & 15) * (K_ / 32)) + g4;
+  }
+  __device__ __forceinline__ void aim(const uint8_t* w, const void* sc, int64_t row0) {
     const int64_t KW = W4 ? K / 2 : K;
-    codes = make_rsrc(w + row0 * KW, rows * KW);
-    lo = (uint32_t)(l16 * KW);
-    if (W4) {
-      scales = make_rsrc((const uint8_t*)sc + row0 * (K / 32), rows * (K / 32));
-      slo = (uint32_t)(l16 * (K / 32));
-    }
+    codes = make_rsrc(w + row0 * KW, 16 * KW);
+    if (W4) scales = make_rsrc((const uint8_t*)sc + row0 * (K / 32), 16 * (K / 32));
   }
-  __device__ __forceinline__ WFrag load(int kb, int g4) const {
-    WFrag f;
+  __device__ __forceinline__ WFrag<W4> load(int kb) const {
+    WFrag<W4> f;
+    const uint32_t o = lo + (kb < KB ? (uint32_t)kb * (W4 ? 64 : 128) : kOOB);
+    f.c[0] = ld_buf16(codes, o);
     if constexpr (W4) {
-      const int64_t k = (int64_t)kb * 64 + g4 * 16;
-      const bool in = k < K / 2;
-      f.a = ld_buf16_nt(codes, in ? lo + (uint32_t)k : kOOB);
-      f.b = make_uint4(0, 0, 0, 0);
-      f.s = __builtin_amdgcn_raw_buffer_load_b8(scales, in ? slo + (uint32_t)(kb * 4 + g4) : kOOB, 0, 0);
+      // the group itself may lie past the row: its scale is another row's
+      const bool in = (uint32_t)kb * 128 + g4 * 32 < K;
+      f.s[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, in ? slo + (uint32_t)kb * 4 : kOOB, 0, 0);
     } else {
-      const int64_t k = (int64_t)kb * 128 + g4 * 32;
-      f.a = ld_buf16_nt(codes, k < K ? lo + (uint32_t)k : kOOB);
-      f.b = ld_buf16_nt(codes, k + 16 < K ? lo + (uint32_t)k + 16 : kOOB);
-      f.s = 0;
+      f.c[1] = ld_buf16(codes, o + 64);
     }
     return f;
   }
 };
 
-// One K block of a row operand: 32 codes per lane and the group's scale
-// (fp32, or the E8M0 byte).
+// One K block of a token (or h) row: the 32 codes that meet a WFrag's.
 struct XFrag {
-  uint4 a, b;
-  float s;
-};
-template <int FMT>
-struct XRows {
-  __amdgpu_buffer_rsrc_t codes, scales;
-  int64_t K;
-  int KB;
-  __device__ __forceinline__ XRows(const uint8_t* x, const void* sc, int64_t rows, int64_t K_)
-      : K(K_), KB((int)((K_ + 127) / 128)) {
-    codes = make_rsrc(x, rows * K);
-    scales = make_rsrc(sc, rows * KB * (FMT == 0 ? 4 : 1));
-  }
-  // row < 0: no row, zeros
-  template <bool W4>
-  __device__ __forceinline__ XFrag load(int row, int kb, int g4) const {
-    XFrag f;
-    const int64_t k0 = (int64_t)kb * 128 + (W4 ? 16 * g4 : 32 * g4);
-    const int64_t k1 = k0 + (W4 ? 64 : 16);
-    const uint32_t o = (uint32_t)((int64_t)row * K);
-    f.a = ld_buf16(codes, row >= 0 && k0 < K ? o + (uint32_t)k0 : kOOB);
-    f.b = ld_buf16(codes, row >= 0 && k1 < K ? o + (uint32_t)k1 : kOOB);
-    const uint32_t so = row >= 0 ? (uint32_t)(row * KB + kb) * (FMT == 0 ? 4 : 1) : kOOB;
-    if (FMT == 0) f.s = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(scales, so, 0, 0));
-    else f.s = __int_as_float((int)__builtin_amdgcn_raw_buffer_load_b8(scales, so, 0, 0));
+  uint4 c[2];
+  __device__ __forceinline__ BFrag bf16() const {
+    BFrag f;
+    f.v[0] = cvt_e4m3x8(c[0].x, c[0].y); f.v[1] = cvt_e4m3x8(c[0].z, c[0].w);
+    f.v[2] = cvt_e4m3x8(c[1].x, c[1].y); f.v[3] = cvt_e4m3x8(c[1].z, c[1].w);
     return f;
   }
 };
 
-// sw: the weight block's scale (fp32, or the E8M0 byte; not used with MXFP4)
-template <int FMT, bool W4>
-__device__ __forceinline__ v4f moe_step(v4f acc, const WFrag& w, const XFrag& x, float sw) {
-  if constexpr (W4) return mfma_step_w4<FMT>(acc, join(w.a, w.b), join(x.a, x.b), x.s, w.s);
-  else return mfma_step<FMT>(acc, join(w.a, w.b), join(x.a, x.b), x.s, sw);
+// acc += (W X^T of one K block) * scale: output rows n (registers), slots m
+// (lanes).  c: the row group's scale, times the weight block's (FP8).
+__device__ __forceinline__ v4f moe_step(v4f acc, const BFrag& w, const BFrag& x, float c) {
+  v4f t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], t, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i], c, acc[i]);
+  return acc;
 }
 
 // ------------------------------------------------------------------------
-// RT: subtiles of 16 slots served by one reading of the weights; an expert
-// with more slots reads its rows again (from L2).
+// The slots sorted by expert (in slot order within one), in LDS, and their
+// segments: at most ROWS rows of one expert.
+struct SortedSlots {
+  int eid[kMoeMaxSlots];
+  int sl[kMoeMaxSlots];                // slot words
+  int seg[kMoeMaxSlots + 1];           // first row of every segment
+  int nsegs, total;
+};
+
+// by one wave, after eid
+template <int ROWS>
+__device__ __forceinline__ void find_segments(SortedSlots& p, int total, int lane) {
+  // a row starts a segment when its place in its run is a multiple of ROWS
+  int n = 0, start = 0;
+  for (int i0 = 0; i0 < total; i0 += 64) {
+    const int i = i0 + lane;
+    const bool run = i < total && (i == 0 || p.eid[i] != p.eid[i - 1]);
+    const unsigned long long b = __ballot(run) & (~0ull >> (63 - lane));
+    const int mine = b ? i0 + 63 - __clzll(b) : start;     // this row's run's start
+    const bool st = i < total && (i - mine) % ROWS == 0;
+    const unsigned long long sb = __ballot(st);
+    if (st) p.seg[n + __popcll(sb & ((1ull << lane) - 1))] = i;
+    n += __popcll(sb);
+    start = __shfl(mine, 63);
+  }
+  if (lane == 0) {
+    p.seg[n] = total;
+    p.nsegs = n;
+  }
+}
+
+// The sort, by the whole workgroup: a slot's place is the number of slots of
+// lower experts and of earlier slots of its own.  key: kMoeMaxSlots words.
+__device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32_t* ids, int S,
+                                           int k, int E) {
+  constexpr int kSkip = 0x7fffffff;                        // behind all others
+  const int S4 = (S + 3) & ~3;
+  for (int i = threadIdx.x; i < S4; i += kMoeThreads) {
+    const int e = i < S ? ids[i] : -1;
+    key[i] = e >= 0 && e < E ? e : kSkip;
+  }
+  if (threadIdx.x == 0) p.total = 0;
+  __syncthreads();
+  int valid = 0;
+  for (int i = threadIdx.x; i < S; i += kMoeThreads) {
+    const int e = key[i];
+    if (e == kSkip) continue;
+    int at = 0;
+    for (int j = 0; j < S4; j += 4) {
+      const int4 o = *(const int4*)(key + j);
+      at += (o.x < e || (o.x == e && j < i)) + (o.y < e || (o.y == e && j + 1 < i)) +
+            (o.z < e || (o.z == e && j + 2 < i)) + (o.w < e || (o.w == e && j + 3 < i));
+    }
+    p.eid[at] = e;
+    p.sl[at] = slot_word(i, k);
+    ++valid;
+  }
+  if (valid) atomicAdd(&p.total, valid);
+  __syncthreads();
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// ------------------------------------------------------------------------
 template <int FMT, bool W4, int RT>
 __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uint16_t* h,
-                                                                  MoePlan* plan, int by_slot) {
-  constexpr int DEPTH = 2;
-  __shared__ int list[kMoeMaxSlots];
-  __shared__ int head[2];              // slots of this expert, slots of lower experts
-  __shared__ v4f red[kMoeWaves][2 * RT][64];
+                                                                  MoePlan* plan) {
+  constexpr int D = RT == 1 ? 4 : RT == 2 ? 3 : 2;
+  constexpr int SB = FMT == 0 ? 4 : 1;
+  __shared__ SortedSlots p;
+  // partial products of tasks that begin or end inside a wave's share: [0]
+  // begun by an earlier wave, [1] begun here and left to the next
+  __shared__ v4f part[kMoeWaves][2][2 * RT][64];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = uniform(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int S = a.T * a.k;
-  const int e = by_slot ? __builtin_amdgcn_readfirstlane(a.ids[blockIdx.y]) : (int)blockIdx.y;
-  const bool first = blockIdx.x == 0 && blockIdx.y == 0;
-  const bool here = e >= 0 && e < a.E;
-  if (!here && !first) return;
-  // this expert's slots in slot order (wave 0), and how many lie before them
-  if (wave == 0) {
-    int n = 0, lower = 0, total = 0;
-    for (int s0 = 0; s0 < S; s0 += 64) {
-      const int s = s0 + lane;
-      const int v = s < S ? a.ids[s] : -1;
-      const bool ok = v >= 0 && v < a.E;
-      const unsigned long long mine = __ballot(ok && v == e);
-      if (ok && v == e) list[n + __popcll(mine & ((1ull << lane) - 1))] = s;
-      n += __popcll(mine);
-      lower += __popcll(__ballot(ok && v < e));
-      total += __popcll(__ballot(ok));
-    }
-    if (lane == 0) {
-      head[0] = here ? n : 0;
-      head[1] = lower;
-      if (first) plan->total = total;
-    }
-  }
-  __syncthreads();
-  const int n = __builtin_amdgcn_readfirstlane(head[0]);
-  if (n == 0 || (by_slot && list[0] != (int)blockIdx.y)) return;   // not the expert's first slot
+  sort_slots(p, (int*)part, a.ids, a.T * a.k, a.k, a.E);
+  const int total = uniform(p.total);
   if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < n; i += kMoeThreads) {
-      plan->expert[head[1] + i] = e;
-      plan->slot[head[1] + i] = list[i];
+    if (threadIdx.x == 0) plan->total = total;
+    for (int i = threadIdx.x; i < total; i += kMoeThreads) {
+      plan->expert[i] = p.eid[i];
+      plan->slot[i] = p.sl[i];
     }
   }
+  if (wave == 0) find_segments<16 * RT>(p, total, lane);
+  __syncthreads();
 
-  const int64_t K = a.H, I = a.I, n0 = (int64_t)blockIdx.x * 16;
-  const int KB = (int)((K + 127) / 128);
-  const WTile<W4> wg(a.w13, a.s13, (int64_t)e * 2 * I + n0, 16, K, l16);
-  const WTile<W4> wu(a.w13, a.s13, (int64_t)e * 2 * I + I + n0, 16, K, l16);
-  const int64_t sg = ((int64_t)e * 2 * I + n0) / 128 * KB, su = sg + I / 128 * KB;
-  const XRows<FMT> xr(a.xq, a.xs, a.T, K);
+  const int64_t K = a.H, I = a.I;
+  const int KB = (int)((K + 127) / 128), CT = (int)(I / 16);
+  const int64_t tasks = (int64_t)uniform(p.nsegs) * CT;
+  const int64_t t0 = tasks * blockIdx.x / gridDim.x, t1 = tasks * (blockIdx.x + 1) / gridDim.x;
+  const int64_t items = (t1 - t0) * KB;
+  auto share = [&](int w) { return items * w / kMoeWaves; };
+  const int64_t it0 = share(wave);
+  const int cnt = (int)(share(wave + 1) - it0);
 
-  for (int r0 = 0; r0 < n; r0 += 16 * RT) {
-    int row[RT];
+  // h of one task from its products: lane (l16, g4) has columns 4 g4 .. + 3
+  // of row l16
+  auto finish = [&](const v4f (&g)[RT], const v4f (&u)[RT], int seg, int ct) {
+    const int r0 = p.seg[seg], r1 = p.seg[seg + 1];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const int i = r0 + 16 * r + l16;
-      row[r] = i < n ? list[i] / a.k : -1;
+      uint32_t b[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        b[q] = f32_to_bf16(g[r][q] / (1.0f + expf(-g[r][q])) * u[r][q]);
+      if (i < r1)
+        *(uint2*)(h + (int64_t)slot_of(p.sl[i]) * I + ct * 16 + 4 * g4) =
+            make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
     }
+  };
+
+  if (cnt > 0) {
+    const __amdgpu_buffer_rsrc_t rows = make_rsrc(a.xq, a.T * K);
+    const __amdgpu_buffer_rsrc_t rscales = make_rsrc(a.xs, (int64_t)a.T * KB * SB);
+    // two cursors over the wave's items: loads, and products behind them
+    const int64_t task = t0 + it0 / KB;
+    int lseg = (int)(task / CT), lct = (int)(task - (int64_t)lseg * CT);
+    int lkb = (int)(it0 - it0 / KB * KB), left = cnt;
+    int pseg = lseg, pct = lct, pkb = lkb, begun = lkb;
+    const uint32_t k0 = piece0<W4>(g4), k1 = piece1<W4>(g4);
+    uint32_t xo[RT], so[RT];           // the segment's rows; no row: past the buffers
+    int e = 0;
+    WTile<W4> wg, wu;
+    __amdgpu_buffer_rsrc_t sg, su;
+    wg.init(K, lane);
+    wu.init(K, lane);
+    auto aim_rows = [&]() {
+      const int r0 = uniform(p.seg[lseg]), r1 = uniform(p.seg[lseg + 1]);
+      e = uniform(p.eid[r0]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int i = r0 + 16 * r + l16;
+        const uint32_t t = i < r1 ? token_of(p.sl[i]) : 0;
+        xo[r] = i < r1 ? t * (uint32_t)K : kOOB;
+        so[r] = i < r1 ? t * (uint32_t)KB * SB : kOOB;
+      }
+    };
+    auto aim = [&]() {
+      const int64_t row = (int64_t)e * 2 * I + lct * 16;
+      wg.aim(a.w13, a.s13, row);
+      wu.aim(a.w13, a.s13, row + I);
+      if (!W4) {
+        sg = make_rsrc((const uint8_t*)a.s13 + row / 128 * KB * SB, (int64_t)KB * SB);
+        su = make_rsrc((const uint8_t*)a.s13 + (row + I) / 128 * KB * SB, (int64_t)KB * SB);
+      }
+    };
+    struct Item {
+      WFrag<W4> g, u;
+      XFrag x[RT];
+      uint32_t sx[RT], sg, su;
+    } ring[D];
+    auto next = [&](Item& f) {
+      const bool in = left > 0;        // past the share: zeros, no traffic
+      const int kb = in ? lkb : KB;
+      f.g = wg.load(kb);
+      f.u = wu.load(kb);
+      const uint32_t k = (uint32_t)kb * 128, sk = in ? (uint32_t)kb * SB : 0x40000000u;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        f.x[r].c[0] = ld_buf16(rows, k + k0 < K ? xo[r] + k + k0 : kOOB);
+        f.x[r].c[1] = ld_buf16(rows, k + k1 < K ? xo[r] + k + k1 : kOOB);
+        if (FMT == 0) f.sx[r] = __builtin_amdgcn_raw_buffer_load_b32(rscales, so[r] + sk, 0, 0);
+        else f.sx[r] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rscales, so[r] + sk, 0, 0);
+      }
+      if constexpr (!W4) {
+        if (FMT == 0) {
+          f.sg = __builtin_amdgcn_raw_buffer_load_b32(sg, sk, 0, 0);
+          f.su = __builtin_amdgcn_raw_buffer_load_b32(su, sk, 0, 0);
+        } else {
+          f.sg = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sg, sk, 0, 0);
+          f.su = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(su, sk, 0, 0);
+        }
+      }
+      if (--left > 0 && ++lkb == KB) {
+        lkb = 0;
+        if (++lct == CT) {
+          lct = 0;
+          ++lseg;
+          aim_rows();
+        }
+        aim();
+      }
+    };
+    aim_rows();
+    aim();
+#pragma unroll
+    for (int d = 0; d < D; ++d) next(ring[d]);
     v4f ag[RT], au[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) ag[r] = au[r] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int kb0 = wave; kb0 < KB; kb0 += kMoeWaves * DEPTH) {
-      WFrag fg[DEPTH], fu[DEPTH];
-      XFrag fx[DEPTH][RT];
-      float cg[DEPTH], cu[DEPTH];
+    for (int i0 = 0; i0 < cnt; i0 += D) {
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        const int kb = kb0 + d * kMoeWaves;
-        const int kc = min(kb, KB - 1);          // past the end: multiplied by zeros
-        fg[d] = wg.load(kb, g4);
-        fu[d] = wu.load(kb, g4);
-        cg[d] = W4 ? 0.f : load_scale<FMT>(a.s13, sg + kc);
-        cu[d] = W4 ? 0.f : load_scale<FMT>(a.s13, su + kc);
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-          fx[d][r] = xr.template load<W4>(kb < KB ? row[r] : -1, kb, g4);
-      }
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d)
+      for (int d = 0; d < D; ++d) {
+        // items past the share are zeros times zeros
+        const BFrag bg = ring[d].g.bf16(), bu = ring[d].u.bf16();
+        const float cg = W4 ? 1.f : scale_value<FMT>(ring[d].sg);
+        const float cu = W4 ? 1.f : scale_value<FMT>(ring[d].su);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          ag[r] = moe_step<FMT, W4>(ag[r], fg[d], fx[d][r], cg[d]);
-          au[r] = moe_step<FMT, W4>(au[r], fu[d], fx[d][r], cu[d]);
+          const BFrag bx = ring[d].x[r].bf16();
+          const float sx = scale_value<FMT>(ring[d].sx[r]);
+          ag[r] = moe_step(ag[r], bg, bx, sx * cg);
+          au[r] = moe_step(au[r], bu, bx, sx * cu);
         }
-    }
-    if (r0 > 0) __syncthreads();                  // the last pass's sums were read
+        next(ring[d]);
+        const bool last = i0 + d + 1 == cnt;
+        if (i0 + d < cnt && (++pkb == KB || last)) {         // the task's end, here
+          if (pkb == KB && begun == 0) {
+            finish(ag, au, pseg, pct);
+          } else {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      red[wave][2 * r][lane] = ag[r];
-      red[wave][2 * r + 1][lane] = au[r];
+            for (int r = 0; r < RT; ++r) {
+              part[wave][begun == 0][2 * r][lane] = ag[r];
+              part[wave][begun == 0][2 * r + 1][lane] = au[r];
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < RT; ++r) ag[r] = au[r] = v4f{0.f, 0.f, 0.f, 0.f};
+          if (!last) {
+            begun = pkb = 0;
+            if (++pct == CT) {
+              pct = 0;
+              ++pseg;
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+    left = begun == 0 && pkb < KB;     // the last task: begun here, not ended
+    lseg = pseg;
+    lct = pct;
     __syncthreads();
-    for (int r = wave; r < RT; r += kMoeWaves) {
-      v4f g = red[0][2 * r][lane], u = red[0][2 * r + 1][lane];
+    if (left) {
+      v4f g[RT], u[RT];
 #pragma unroll
-      for (int w = 1; w < kMoeWaves; ++w) {
-        g += red[w][2 * r][lane];
-        u += red[w][2 * r + 1][lane];
+      for (int r = 0; r < RT; ++r) {
+        g[r] = part[wave][1][2 * r][lane];
+        u[r] = part[wave][1][2 * r + 1][lane];
       }
-      // lane: columns n0 + 4 g4 .. + 3 of slot l16
-      const int i = r0 + 16 * r + l16;
-      if (i < n) {
-        uint32_t b[4];
+      const int64_t end = (share(wave + 1) / KB + 1) * KB;
+      for (int w = wave + 1; w < kMoeWaves; ++w) {
+        if (share(w) == share(w + 1)) continue;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) b[q] = f32_to_bf16(g[q] / (1.0f + expf(-g[q])) * u[q]);
-        *(uint2*)(h + (int64_t)list[i] * I + n0 + 4 * g4) =
-            make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+        for (int r = 0; r < RT; ++r) {
+          g[r] += part[w][0][2 * r][lane];
+          u[r] += part[w][0][2 * r + 1][lane];
+        }
+        if (share(w + 1) >= end) break;
       }
+      finish(g, u, lseg, lct);
     }
+  } else {
+    __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------------
-template <int FMT, bool W4, int RT>
-__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const uint8_t* hq,
-                                                               const void* hs,
+// QUANT: h comes as bf16 and is quantized here, all rows into LDS, by every
+// workgroup (launches with few rows); else as codes and scales.
+template <int FMT, bool W4, int RT, bool QUANT>
+__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const uint16_t* h,
+                                                               const uint8_t* hq, const void* hs,
                                                                const MoePlan* plan) {
-  constexpr int DEPTH = 4;
-  extern __shared__ float sums[];      // [kMoeWaves][T][16]
-  __shared__ int eid[kMoeMaxSlots];    // the sorted slots' experts
-  __shared__ int sl[kMoeMaxSlots];     // slot | which of the token's rows in the run << 16
-  __shared__ int run[1024 + 1];        // first row of every expert's run
-  __shared__ int nruns;
+  constexpr int D = QUANT ? 6 : RT == 1 ? 4 : RT == 2 ? 3 : 2;
+  constexpr int SB = FMT == 0 ? 4 : 1;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // sums, codes and scales of h
+  __shared__ SortedSlots p;
+  __shared__ float swt[kMoeMaxSlots];  // the sorted slots' weights
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = uniform(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int T = a.T, k = a.k;
+  const int T = a.T;
   const int64_t N = a.H, K = a.I, n0 = (int64_t)blockIdx.x * 16;
   const int KB = (int)(K / 128);
-  const int total = __builtin_amdgcn_readfirstlane(plan->total);
-  float* mine = sums + (int64_t)wave * T * 16;
+  float* sums = (float*)lds;           // [waves][T][16]
+  const int stride = (int)K + 16;      // 16: rows start in different banks
+  uint8_t* xl = lds + kMoeWaves * T * 64;
+  float* xs = (float*)(xl + (QUANT ? (int64_t)T * a.k * stride : 0));
+
+  const int total = uniform(plan->total);
+  float* mine = sums + wave * T * 16;
   for (int i = lane * 4; i < T * 16; i += 256) *(float4*)(mine + i) = make_float4(0, 0, 0, 0);
   for (int i = threadIdx.x; i < total; i += kMoeThreads) {
-    eid[i] = plan->expert[i];
-    sl[i] = plan->slot[i];
+    p.eid[i] = plan->expert[i];
+    const int w = plan->slot[i];
+    p.sl[i] = w;
+    swt[i] = a.wt[slot_of(w)];
   }
   __syncthreads();
   if (wave == 0) {
-    int n = 0;
-    for (int i0 = 0; i0 < total; i0 += 64) {
-      const int i = i0 + lane;
-      const bool start = i < total && (i == 0 || eid[i] != eid[i - 1]);
-      const unsigned long long b = __ballot(start);
-      if (start) run[n + __popcll(b & ((1ull << lane) - 1))] = i;
-      n += __popcll(b);
-    }
-    if (lane == 0) {
-      run[n] = total;
-      nruns = n;
-    }
+    find_segments<16 * RT>(p, total, lane);
   } else if (wave == 1) {
     // a token that names an expert twice has neighbouring rows in its run:
     // number them, so that they add to the token's sum one after the other
     for (int i = lane; i < total; i += 64) {
       int nth = 0;
-      while (nth < i && nth < k && eid[i - nth - 1] == eid[i] &&
-             (sl[i - nth - 1] & 0xffff) / k == (sl[i] & 0xffff) / k)
+      while (nth < i && p.eid[i - nth - 1] == p.eid[i] &&
+             token_of(p.sl[i - nth - 1]) == token_of(p.sl[i]))
         ++nth;
-      if (nth) atomicOr(&sl[i], nth << 16);
+      if (nth) atomicOr(&p.sl[i], nth << 18);
     }
   }
   __syncthreads();
 
-  // (run, K block) pairs dealt to the waves in equal contiguous shares
-  const int64_t items = (int64_t)__builtin_amdgcn_readfirstlane(nruns) * KB;
-  int64_t it = items * wave / kMoeWaves;
-  const int64_t it1 = items * (wave + 1) / kMoeWaves;
-  const int rows = (int)min((int64_t)16, N - n0);
-  const XRows<FMT> xr(hq, hs, (int64_t)T * k, K);
+  const int64_t items = (int64_t)uniform(p.nsegs) * KB;
+  const int64_t it0 = items * wave / kMoeWaves;
+  const int cnt = (int)(items * (wave + 1) / kMoeWaves - it0);
   const int NB = (int)((N + 127) / 128);
-  while (it < it1) {
-    const int ri = (int)(it / KB), kb0 = (int)(it - (int64_t)ri * KB);
-    const int kb1 = (int)min((int64_t)KB, kb0 + (it1 - it));
-    it += kb1 - kb0;
-    const int r0 = __builtin_amdgcn_readfirstlane(run[ri]);
-    const int r1 = __builtin_amdgcn_readfirstlane(run[ri + 1]);
-    const int e = __builtin_amdgcn_readfirstlane(eid[r0]);
-    const WTile<W4> wt(a.w2, a.s2, (int64_t)e * N + n0, rows, K, l16);
-    const int64_t sb = ((int64_t)e * NB + n0 / 128) * KB;
-    for (int rb = r0; rb < r1; rb += 16 * RT) {
-      int row[RT], nth[RT];
-      float c[RT];
+  const __amdgpu_buffer_rsrc_t rows = make_rsrc(hq, (int64_t)T * a.k * K);
+  const __amdgpu_buffer_rsrc_t rscales = make_rsrc(hs, (int64_t)T * a.k * KB * SB);
+  // two cursors over the wave's items: loads, and products behind them
+  int lseg = (int)(it0 / KB), lkb = (int)(it0 - (int64_t)lseg * KB), left = cnt;
+  int pseg = lseg, pkb = lkb;
+  uint32_t xo[RT], so[RT];             // the segment's rows; no row: past the buffers
+  WTile<W4> wt;
+  __amdgpu_buffer_rsrc_t sw;
+  wt.init(K, lane);
+  auto aim = [&]() {
+    const int r0 = uniform(p.seg[lseg]), r1 = uniform(p.seg[lseg + 1]);
+    const int e = uniform(p.eid[r0]);
+    wt.aim(a.w2, a.s2, (int64_t)e * N + n0);
+    if (!W4)
+      sw = make_rsrc((const uint8_t*)a.s2 + ((int64_t)e * NB + n0 / 128) * KB * SB,
+                     (int64_t)KB * SB);
+    if (!QUANT) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const int i = rb + 16 * r + l16;
-        const int v = i < r1 ? sl[i] : -1;
-        row[r] = v < 0 ? -1 : v & 0xffff;
-        nth[r] = v < 0 ? -1 : v >> 16;
-        c[r] = v < 0 ? 0.f : a.wt[row[r]];
+        const int i = r0 + 16 * r + l16;
+        const uint32_t s = i < r1 ? slot_of(p.sl[i]) : 0;
+        xo[r] = i < r1 ? s * (uint32_t)K : kOOB;
+        so[r] = i < r1 ? s * (uint32_t)KB * SB : kOOB;
       }
-      v4f acc[RT];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
-      for (int kb = kb0; kb < kb1; kb += DEPTH) {
-        WFrag fw[DEPTH];
-        XFrag fx[DEPTH][RT];
-        float sw[DEPTH];
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-          const bool in = kb + d < kb1;
-          fw[d] = wt.load(in ? kb + d : KB, g4);        // KB: past the rows, zeros
-          sw[d] = W4 ? 0.f : load_scale<FMT>(a.s2, sb + min(kb + d, KB - 1));
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            fx[d][r] = xr.template load<W4>(in ? row[r] : -1, kb + d, g4);
-        }
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            acc[r] = moe_step<FMT, W4>(acc[r], fw[d], fx[d][r], sw[d]);
-      }
+    }
+  };
+  struct Item {
+    WFrag<W4> w;
+    XFrag x[QUANT ? 1 : RT];
+    uint32_t sx[RT], sw;
+  } ring[D];
+  auto next = [&](Item& f) {
+    // past the share: nothing (2^30 is past every buffer of rows)
+    const bool in = left > 0;
+    f.w = wt.load(in ? lkb : KB);
+    const uint32_t sk = in ? (uint32_t)lkb * SB : 0x40000000u;
+    if constexpr (!QUANT) {
+      const uint32_t k = in ? (uint32_t)lkb * 128 : 0x40000000u;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        // lane: outputs n0 + 4 g4 .. + 3 of row l16
-        float4* to = (float4*)(mine + (row[r] < 0 ? 0 : row[r] / k) * 16 + 4 * g4);
-        for (int p = 0; __ballot(nth[r] >= p) != 0; ++p) {
-          if (nth[r] == p) {
-            float4 v = *to;
-            v.x = fmaf(c[r], acc[r][0], v.x);
-            v.y = fmaf(c[r], acc[r][1], v.y);
-            v.z = fmaf(c[r], acc[r][2], v.z);
-            v.w = fmaf(c[r], acc[r][3], v.w);
-            *to = v;
+        f.x[r].c[0] = ld_buf16(rows, xo[r] + k + piece0<W4>(g4));
+        f.x[r].c[1] = ld_buf16(rows, xo[r] + k + piece1<W4>(g4));
+        if (FMT == 0) f.sx[r] = __builtin_amdgcn_raw_buffer_load_b32(rscales, so[r] + sk, 0, 0);
+        else f.sx[r] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rscales, so[r] + sk, 0, 0);
+      }
+    }
+    if constexpr (!W4) {
+      if (FMT == 0) f.sw = __builtin_amdgcn_raw_buffer_load_b32(sw, sk, 0, 0);
+      else f.sw = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sw, sk, 0, 0);
+    }
+    if (--left > 0 && ++lkb == KB) {
+      lkb = 0;
+      ++lseg;
+      aim();
+    }
+  };
+  if (cnt > 0) {
+    aim();
+#pragma unroll
+    for (int d = 0; d < D; ++d) next(ring[d]);
+  }
+  if constexpr (QUANT) {
+    // sixteen lanes hold a group, eight values each
+    const int C = KB * 16, all = total * C;      // 8-value chunks of the sorted rows
+    for (int q0 = threadIdx.x; q0 - (int)threadIdx.x < all; q0 += kMoeThreads) {
+      const int i = q0 / C, c = q0 - i * C;
+      const bool ok = q0 < all;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (ok) v = *(const uint4*)(h + (int64_t)slot_of(p.sl[i]) * K + c * 8);
+      const Unpacked f = unpack8(v);
+      float amax = amax8(f);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 16));
+      float s = 0.f;
+      int x = 0;
+      const uint2 codes = encode8<FMT>(f, amax, &s, &x);
+      if (ok) {
+        *(uint2*)(xl + i * stride + c * 8) = codes;
+        if ((c & 15) == 0) xs[i * KB + c / 16] = FMT == 0 ? s : e8m0_f32((uint32_t)(x + 127));
+      }
+    }
+    wait_vmcnt<0>();                   // nothing new: these loads came after the weights
+    __syncthreads();
+  }
+  if (cnt > 0) {
+    const uint8_t* px[RT];             // QUANT: the segment's rows in LDS
+    const float* ps[RT];
+    auto aim_products = [&]() {
+      const int r0 = p.seg[pseg], r1 = p.seg[pseg + 1];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int i = min(r0 + 16 * r + l16, r1 - 1);        // past the rows: not added
+        px[r] = xl + i * stride;
+        ps[r] = xs + i * KB;
+      }
+    };
+    if (QUANT) aim_products();
+    v4f acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < cnt; i0 += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        // items past the share are zeros times finite values
+        const BFrag bw = ring[d].w.bf16();
+        const float cw = W4 ? 1.f : scale_value<FMT>(ring[d].sw);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          XFrag x;
+          float sx;
+          if constexpr (QUANT) {
+            x.c[0] = *(const uint4*)(px[r] + pkb * 128 + piece0<W4>(g4));
+            x.c[1] = *(const uint4*)(px[r] + pkb * 128 + piece1<W4>(g4));
+            sx = ps[r][pkb];
+          } else {
+            x = ring[d].x[r];
+            sx = scale_value<FMT>(ring[d].sx[r]);
           }
-          __builtin_amdgcn_wave_barrier();
+          acc[r] = moe_step(acc[r], bw, x.bf16(), sx * cw);
         }
+        next(ring[d]);
+        const bool last = i0 + d + 1 == cnt;
+        if (i0 + d < cnt && (++pkb == KB || last)) {         // the segment's end, here
+          const int r0 = p.seg[pseg], r1 = p.seg[pseg + 1];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            // lane: outputs n0 + 4 g4 .. + 3 of row l16
+            const int at = r0 + 16 * r + l16;
+            const int v = at < r1 ? p.sl[at] : -1;
+            const float c = at < r1 ? swt[at] : 0.f;
+            const int nth = nth_of(v);
+            float4* to = (float4*)(mine + (v < 0 ? 0 : token_of(v)) * 16 + 4 * g4);
+            for (int q = 0; __ballot(nth >= q) != 0; ++q) {
+              if (nth == q) {
+                float4 o = *to;
+                o.x = fmaf(c, acc[r][0], o.x);
+                o.y = fmaf(c, acc[r][1], o.y);
+                o.z = fmaf(c, acc[r][2], o.z);
+                o.w = fmaf(c, acc[r][3], o.w);
+                *to = o;
+              }
+              __builtin_amdgcn_wave_barrier();
+            }
+            acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
+          }
+          if (!last) {
+            pkb = 0;
+            ++pseg;
+            if (QUANT) aim_products();
+          } else {
+            pkb = 0;                   // what is left of the ring reads row starts
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -368,11 +650,9 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
   for (int i = threadIdx.x; i < T * 4; i += kMoeThreads) {
     const int t = i >> 2;
     const int64_t n = n0 + 4 * (i & 3);
-    if (n >= N) continue;
     v4f v = *(const v4f*)(sums + t * 16 + 4 * (i & 3));
 #pragma unroll
-    for (int w = 1; w < kMoeWaves; ++w)
-      v += *(const v4f*)(sums + ((int64_t)w * T + t) * 16 + 4 * (i & 3));
+    for (int w = 1; w < kMoeWaves; ++w) v += *(const v4f*)(sums + (w * T + t) * 16 + 4 * (i & 3));
     const int64_t o = (int64_t)t * N + n;
     if (a.addend) {
       const uint2 d = *(const uint2*)(a.addend + o);
@@ -386,12 +666,11 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
 
 // workspace: [plan][h bf16 S x I][codes S x I][scales S x I/128 x 4]
 struct MoeWorkspace {
-  size_t plan, h, hq, hs, bytes;
+  size_t h, hq, hs, bytes;
 };
 inline MoeWorkspace moe_layout(int64_t S, int64_t I) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   MoeWorkspace w;
-  w.plan = 0;
   w.h = up(sizeof(MoePlan));
   w.hq = w.h + up((size_t)S * I * 2);
   w.hs = w.hq + up((size_t)S * I);
@@ -399,34 +678,43 @@ inline MoeWorkspace moe_layout(int64_t S, int64_t I) {
   return w;
 }
 
+constexpr int kMoeGateUpGroups = 256;      // one workgroup per CU
+constexpr int64_t kMoeQuantBytes = 49152;  // h in LDS, quantized by the down launch
+
 template <int FMT, bool W4, int RT>
 hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
-  const int S = a.T * a.k;
+  const int64_t S = (int64_t)a.T * a.k;
   const MoeWorkspace w = moe_layout(S, a.I);
   uint8_t* ws = (uint8_t*)a.workspace;
-  MoePlan* plan = (MoePlan*)(ws + w.plan);
+  MoePlan* plan = (MoePlan*)ws;
   uint16_t* h = (uint16_t*)(ws + w.h);
-  // one row of workgroups per expert, or per slot where those are fewer (a
-  // slot whose expert came before leaves at once)
-  const int by_slot = S < a.E;
-  hipLaunchKernelGGL((moe_gate_up_kernel<FMT, W4, RT>),
-                     dim3((unsigned)(a.I / 16), (unsigned)(by_slot ? S : a.E)), dim3(kMoeThreads),
-                     0, s, a, h, plan, by_slot);
+  hipLaunchKernelGGL((moe_gate_up_kernel<FMT, W4, RT>), dim3(kMoeGateUpGroups), dim3(kMoeThreads),
+                     0, s, a, h, plan);
   hipError_t r = hipGetLastError();
   if (r != hipSuccess) return r;
+  const dim3 grid((unsigned)(a.H / 16));
+  const size_t sums = (size_t)kMoeWaves * a.T * 64;
+  const int64_t codes = S * (a.I + 16 + a.I / 128 * 4);
+  if (codes <= kMoeQuantBytes) {
+    hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT, true>), grid, dim3(kMoeThreads),
+                       sums + (size_t)codes, s, a, h, nullptr, nullptr, plan);
+    return hipGetLastError();
+  }
   r = launch_quant_act(h, S, a.I, a.I, FMT, ws + w.hq, ws + w.hs, s);
   if (r != hipSuccess) return r;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT>), dim3((unsigned)((a.H + 15) / 16)),
-                     dim3(kMoeThreads), (size_t)kMoeWaves * a.T * 64, s, a, ws + w.hq, ws + w.hs,
-                     plan);
+  hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT, false>), grid, dim3(kMoeThreads), sums, s, a, h,
+                     ws + w.hq, ws + w.hs, plan);
   return hipGetLastError();
 }
 
 template <int FMT, bool W4>
 hipError_t launch_moe_rt(const MoeArgs& a, hipStream_t s) {
-  // the most slots one expert can expect: T tokens (each names it once)
-  if (a.T <= 16) return launch_moe<FMT, W4, 1>(a, s);
-  return launch_moe<FMT, W4, 2>(a, s);
+  // rows of a segment by the average expert's slots: an expert with more
+  // reads its weights again
+  const int64_t S = (int64_t)a.T * a.k;
+  if (a.T <= 16 || S <= (int64_t)a.E * 8) return launch_moe<FMT, W4, 1>(a, s);
+  if (a.T <= 32 || S <= (int64_t)a.E * 20) return launch_moe<FMT, W4, 2>(a, s);
+  return launch_moe<FMT, W4, 4>(a, s);
 }
 
 }  // namespace detail

@@ -393,7 +393,7 @@ BSFP8_API int32_t fp8_grouped_gemm_silu_mul_quant(const void* xq, const void* x_
  *   fp8_grouped_gemm); H % 16 == 0, I % 128 == 0, 1 <= E <= 1024.
  *   workspace    >= bsfp8_workspace_size(BSFP8_OP_MOE_DECODE, T * k, H, I, 0).
  * Errors: EINVAL (sizes, null pointers, enums, misalignment); ENOTSUP (T, k,
- * H or I > 2^22, T k I >= 2^31); ENOSPC.
+ * H or I > 2^22, T k I > 2^30); ENOSPC.
  */
 BSFP8_API int32_t fp8_moe_decode(const void* xq, const void* x_scale, const int32_t* ids,
                                  const float* weights, const void* w13, const void* w13_scale,
