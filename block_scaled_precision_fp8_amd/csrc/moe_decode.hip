@@ -119,7 +119,7 @@ __device__ __forceinline__ uint32_t piece0(int g4) { return W4 ? 32 * g4 : 16 * 
 template <bool W4>
 __device__ __forceinline__ uint32_t piece1(int g4) { return W4 ? 32 * g4 + 16 : 64 + 16 * g4; }
 
-// 16 rows of one expert's weight.  In a row's last, partial K block a lane
+// Up to 16 rows of one expert's weight.  In a row's last, partial K block a lane
 // reads on into the next row: finite values, which meet zeros of the tokens'
 // rows.  Blocks from KB on give zeros and no traffic.
 template <bool W4>
@@ -134,10 +134,11 @@ struct WTile {
     lo = (uint32_t)((lane & 15) * (W4 ? K_ / 2 : K_)) + g4 * 16;
     slo = (uint32_t)((lane & 15) * (K_ / 32)) + g4;
   }
-  __device__ __forceinline__ void aim(const uint8_t* w, const void* sc, int64_t row0) {
+  // n <= 16 rows from row0 on; the others give zeros
+  __device__ __forceinline__ void aim(const uint8_t* w, const void* sc, int64_t row0, int n) {
     const int64_t KW = W4 ? K / 2 : K;
-    codes = make_rsrc(w + row0 * KW, 16 * KW);
-    if (W4) scales = make_rsrc((const uint8_t*)sc + row0 * (K / 32), 16 * (K / 32));
+    codes = make_rsrc(w + row0 * KW, n * KW);
+    if (W4) scales = make_rsrc((const uint8_t*)sc + row0 * (K / 32), (int64_t)n * (K / 32));
   }
   __device__ __forceinline__ WFrag<W4> load(int kb) const {
     WFrag<W4> f;
@@ -244,7 +245,7 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 template <int FMT, bool W4, int RT>
 __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uint16_t* h,
                                                                   MoePlan* plan) {
-  constexpr int D = RT == 1 ? 4 : RT == 2 ? 3 : 2;
+  constexpr int D = W4 ? (RT == 1 ? 8 : RT == 2 ? 5 : 3) : (RT == 1 ? 5 : RT == 2 ? 4 : 2);
   constexpr int SB = FMT == 0 ? 4 : 1;
   __shared__ SortedSlots p;
   // partial products of tasks that begin or end inside a wave's share: [0]
@@ -319,8 +320,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
     };
     auto aim = [&]() {
       const int64_t row = (int64_t)e * 2 * I + lct * 16;
-      wg.aim(a.w13, a.s13, row);
-      wu.aim(a.w13, a.s13, row + I);
+      wg.aim(a.w13, a.s13, row, 16);
+      wu.aim(a.w13, a.s13, row + I, 16);
       if (!W4) {
         sg = make_rsrc((const uint8_t*)a.s13 + row / 128 * KB * SB, (int64_t)KB * SB);
         su = make_rsrc((const uint8_t*)a.s13 + (row + I) / 128 * KB * SB, (int64_t)KB * SB);
@@ -370,6 +371,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
     v4f ag[RT], au[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) ag[r] = au[r] = v4f{0.f, 0.f, 0.f, 0.f};
+    int prows = uniform(p.seg[pseg + 1] - p.seg[pseg]);
     for (int i0 = 0; i0 < cnt; i0 += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
@@ -379,6 +381,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
         const float cu = W4 ? 1.f : scale_value<FMT>(ring[d].su);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
+          if (r > 0 && prows <= 16 * r) break;
           const BFrag bx = ring[d].x[r].bf16();
           const float sx = scale_value<FMT>(ring[d].sx[r]);
           ag[r] = moe_step(ag[r], bg, bx, sx * cg);
@@ -403,6 +406,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
             if (++pct == CT) {
               pct = 0;
               ++pseg;
+              prows = uniform(p.seg[pseg + 1] - p.seg[pseg]);
             }
           }
         }
@@ -440,11 +444,14 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
 // ------------------------------------------------------------------------
 // QUANT: h comes as bf16 and is quantized here, all rows into LDS, by every
 // workgroup (launches with few rows); else as codes and scales.
-template <int FMT, bool W4, int RT, bool QUANT>
+// NT: 16-row weight tiles that make up the workgroup's R output features (R a
+// multiple of 4, the last tile partly empty), so that H / R workgroups can
+// match the CUs.
+template <int FMT, bool W4, int RT, bool QUANT, int NT>
 __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const uint16_t* h,
                                                                const uint8_t* hq, const void* hs,
-                                                               const MoePlan* plan) {
-  constexpr int D = QUANT ? 6 : RT == 1 ? 4 : RT == 2 ? 3 : 2;
+                                                               const MoePlan* plan, int R) {
+  constexpr int D = (QUANT ? 6 : RT == 1 ? 4 : RT == 2 ? 3 : 2) / (QUANT && NT == 2 ? 2 : 1) * (W4 && QUANT ? 2 : 1);
   constexpr int SB = FMT == 0 ? 4 : 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // sums, codes and scales of h
   __shared__ SortedSlots p;
@@ -453,16 +460,16 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
   const int wave = uniform(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
   const int T = a.T;
-  const int64_t N = a.H, K = a.I, n0 = (int64_t)blockIdx.x * 16;
+  const int64_t N = a.H, K = a.I, n0 = (int64_t)blockIdx.x * R;
   const int KB = (int)(K / 128);
-  float* sums = (float*)lds;           // [waves][T][16]
+  float* sums = (float*)lds;           // [waves][T][R]
   const int stride = (int)K + 16;      // 16: rows start in different banks
-  uint8_t* xl = lds + kMoeWaves * T * 64;
+  uint8_t* xl = lds + kMoeWaves * T * R * 4;
   float* xs = (float*)(xl + (QUANT ? (int64_t)T * a.k * stride : 0));
 
   const int total = uniform(plan->total);
-  float* mine = sums + wave * T * 16;
-  for (int i = lane * 4; i < T * 16; i += 256) *(float4*)(mine + i) = make_float4(0, 0, 0, 0);
+  float* mine = sums + wave * T * R;
+  for (int i = lane * 4; i < T * R; i += 256) *(float4*)(mine + i) = make_float4(0, 0, 0, 0);
   for (int i = threadIdx.x; i < total; i += kMoeThreads) {
     p.eid[i] = plan->expert[i];
     const int w = plan->slot[i];
@@ -488,23 +495,30 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
   const int64_t items = (int64_t)uniform(p.nsegs) * KB;
   const int64_t it0 = items * wave / kMoeWaves;
   const int cnt = (int)(items * (wave + 1) / kMoeWaves - it0);
-  const int NB = (int)((N + 127) / 128);
+  const int NB = (int)((N + 127) / 128), nrows = (int)min((int64_t)R, N - n0);
   const __amdgpu_buffer_rsrc_t rows = make_rsrc(hq, (int64_t)T * a.k * K);
   const __amdgpu_buffer_rsrc_t rscales = make_rsrc(hs, (int64_t)T * a.k * KB * SB);
   // two cursors over the wave's items: loads, and products behind them
   int lseg = (int)(it0 / KB), lkb = (int)(it0 - (int64_t)lseg * KB), left = cnt;
   int pseg = lseg, pkb = lkb;
   uint32_t xo[RT], so[RT];             // the segment's rows; no row: past the buffers
-  WTile<W4> wt;
+  WTile<W4> wt[NT];
   __amdgpu_buffer_rsrc_t sw;
-  wt.init(K, lane);
+  uint32_t swo[NT];                    // this lane's four outputs' row of block scales
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    wt[j].init(K, lane);
+    swo[j] = (uint32_t)(((n0 + 16 * j + 4 * g4) / 128 - n0 / 128) * KB) * SB;
+  }
   auto aim = [&]() {
     const int r0 = uniform(p.seg[lseg]), r1 = uniform(p.seg[lseg + 1]);
     const int e = uniform(p.eid[r0]);
-    wt.aim(a.w2, a.s2, (int64_t)e * N + n0);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      wt[j].aim(a.w2, a.s2, (int64_t)e * N + n0 + 16 * j, max(0, min(16, nrows - 16 * j)));
     if (!W4)
       sw = make_rsrc((const uint8_t*)a.s2 + ((int64_t)e * NB + n0 / 128) * KB * SB,
-                     (int64_t)KB * SB);
+                     min((int64_t)2, NB - n0 / 128) * KB * SB);
     if (!QUANT) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -516,14 +530,15 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
     }
   };
   struct Item {
-    WFrag<W4> w;
+    WFrag<W4> w[NT];
     XFrag x[QUANT ? 1 : RT];
-    uint32_t sx[RT], sw;
+    uint32_t sx[RT], sw[NT];
   } ring[D];
   auto next = [&](Item& f) {
     // past the share: nothing (2^30 is past every buffer of rows)
     const bool in = left > 0;
-    f.w = wt.load(in ? lkb : KB);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) f.w[j] = wt[j].load(in ? lkb : KB);
     const uint32_t sk = in ? (uint32_t)lkb * SB : 0x40000000u;
     if constexpr (!QUANT) {
       const uint32_t k = in ? (uint32_t)lkb * 128 : 0x40000000u;
@@ -536,8 +551,11 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
       }
     }
     if constexpr (!W4) {
-      if (FMT == 0) f.sw = __builtin_amdgcn_raw_buffer_load_b32(sw, sk, 0, 0);
-      else f.sw = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sw, sk, 0, 0);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (FMT == 0) f.sw[j] = __builtin_amdgcn_raw_buffer_load_b32(sw, swo[j] + sk, 0, 0);
+        else f.sw[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sw, swo[j] + sk, 0, 0);
+      }
     }
     if (--left > 0 && ++lkb == KB) {
       lkb = 0;
@@ -586,17 +604,26 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
       }
     };
     if (QUANT) aim_products();
-    v4f acc[RT];
+    v4f acc[RT][NT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    int prows = uniform(p.seg[pseg + 1] - p.seg[pseg]);
     for (int i0 = 0; i0 < cnt; i0 += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         // items past the share are zeros times finite values
-        const BFrag bw = ring[d].w.bf16();
-        const float cw = W4 ? 1.f : scale_value<FMT>(ring[d].sw);
+        BFrag bw[NT];
+        float cw[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          bw[j] = ring[d].w[j].bf16();
+          cw[j] = W4 ? 1.f : scale_value<FMT>(ring[d].sw[j]);
+        }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
+          if (r > 0 && prows <= 16 * r) break;
           XFrag x;
           float sx;
           if constexpr (QUANT) {
@@ -607,7 +634,9 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
             x = ring[d].x[r];
             sx = scale_value<FMT>(ring[d].sx[r]);
           }
-          acc[r] = moe_step(acc[r], bw, x.bf16(), sx * cw);
+          const BFrag bx = x.bf16();
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[r][j] = moe_step(acc[r][j], bw[j], bx, sx * cw[j]);
         }
         next(ring[d]);
         const bool last = i0 + d + 1 == cnt;
@@ -615,28 +644,31 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
           const int r0 = p.seg[pseg], r1 = p.seg[pseg + 1];
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            // lane: outputs n0 + 4 g4 .. + 3 of row l16
+            // lane: outputs n0 + 16 j + 4 g4 .. + 3 of row l16
             const int at = r0 + 16 * r + l16;
             const int v = at < r1 ? p.sl[at] : -1;
             const float c = at < r1 ? swt[at] : 0.f;
             const int nth = nth_of(v);
-            float4* to = (float4*)(mine + (v < 0 ? 0 : token_of(v)) * 16 + 4 * g4);
+            float* to = mine + (v < 0 ? 0 : token_of(v)) * R + 4 * g4;
             for (int q = 0; __ballot(nth >= q) != 0; ++q) {
-              if (nth == q) {
-                float4 o = *to;
-                o.x = fmaf(c, acc[r][0], o.x);
-                o.y = fmaf(c, acc[r][1], o.y);
-                o.z = fmaf(c, acc[r][2], o.z);
-                o.w = fmaf(c, acc[r][3], o.w);
-                *to = o;
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                if (nth == q && 16 * j + 4 * g4 < R) {
+                  v4f o = *(v4f*)(to + 16 * j);
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) o[x] = fmaf(c, acc[r][j][x], o[x]);
+                  *(v4f*)(to + 16 * j) = o;
+                }
               }
               __builtin_amdgcn_wave_barrier();
             }
-            acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
           }
           if (!last) {
             pkb = 0;
             ++pseg;
+            prows = uniform(p.seg[pseg + 1] - p.seg[pseg]);
             if (QUANT) aim_products();
           } else {
             pkb = 0;                   // what is left of the ring reads row starts
@@ -647,13 +679,14 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < T * 4; i += kMoeThreads) {
-    const int t = i >> 2;
-    const int64_t n = n0 + 4 * (i & 3);
-    v4f v = *(const v4f*)(sums + t * 16 + 4 * (i & 3));
+  const int Q = R / 4;
+  for (int i = threadIdx.x; i < T * Q; i += kMoeThreads) {
+    const int t = i / Q, c = 4 * (i - t * Q);
+    if (n0 + c >= N) continue;
+    v4f v = *(const v4f*)(sums + t * R + c);
 #pragma unroll
-    for (int w = 1; w < kMoeWaves; ++w) v += *(const v4f*)(sums + (w * T + t) * 16 + 4 * (i & 3));
-    const int64_t o = (int64_t)t * N + n;
+    for (int w = 1; w < kMoeWaves; ++w) v += *(const v4f*)(sums + (w * T + t) * R + c);
+    const int64_t o = (int64_t)t * N + n0 + c;
     if (a.addend) {
       const uint2 d = *(const uint2*)(a.addend + o);
       v[0] += bf16_lo(d.x); v[1] += bf16_hi(d.x);
@@ -681,6 +714,37 @@ inline MoeWorkspace moe_layout(int64_t S, int64_t I) {
 constexpr int kMoeGateUpGroups = 256;      // one workgroup per CU
 constexpr int64_t kMoeQuantBytes = 49152;  // h in LDS, quantized by the down launch
 
+// Output features of a down workgroup: a multiple of 4 from 8 to 32 (to 16
+// where the sums of more would not fit the LDS) with the least to do on the
+// busiest of 256 CUs, the larger where that is equal.
+inline int moe_down_rows(int64_t H, int T) {
+  int best = 0;
+  int64_t least = 0;
+  for (int r = T > 64 ? 16 : 32; r >= 8; r -= 4) {
+    const int64_t groups = (H + r - 1) / r, cost = (groups + 255) / 256 * r;
+    if (best == 0 || cost < least) {
+      best = r;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+template <int FMT, bool W4, int RT, bool QUANT>
+hipError_t launch_moe_down(const MoeArgs& a, const uint16_t* h, const uint8_t* hq, const void* hs,
+                           const MoePlan* plan, size_t lds, hipStream_t s) {
+  const int R = moe_down_rows(a.H, a.T);
+  const dim3 grid((unsigned)((a.H + R - 1) / R));
+  lds += (size_t)kMoeWaves * a.T * R * 4;
+  if (R <= 16)
+    hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT, QUANT, 1>), grid, dim3(kMoeThreads), lds, s, a,
+                       h, hq, hs, plan, R);
+  else
+    hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT, QUANT, 2>), grid, dim3(kMoeThreads), lds, s, a,
+                       h, hq, hs, plan, R);
+  return hipGetLastError();
+}
+
 template <int FMT, bool W4, int RT>
 hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
   const int64_t S = (int64_t)a.T * a.k;
@@ -692,19 +756,12 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
                      0, s, a, h, plan);
   hipError_t r = hipGetLastError();
   if (r != hipSuccess) return r;
-  const dim3 grid((unsigned)(a.H / 16));
-  const size_t sums = (size_t)kMoeWaves * a.T * 64;
   const int64_t codes = S * (a.I + 16 + a.I / 128 * 4);
-  if (codes <= kMoeQuantBytes) {
-    hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT, true>), grid, dim3(kMoeThreads),
-                       sums + (size_t)codes, s, a, h, nullptr, nullptr, plan);
-    return hipGetLastError();
-  }
+  if (codes <= kMoeQuantBytes)
+    return launch_moe_down<FMT, W4, RT, true>(a, h, nullptr, nullptr, plan, (size_t)codes, s);
   r = launch_quant_act(h, S, a.I, a.I, FMT, ws + w.hq, ws + w.hs, s);
   if (r != hipSuccess) return r;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT, false>), grid, dim3(kMoeThreads), sums, s, a, h,
-                     ws + w.hq, ws + w.hs, plan);
-  return hipGetLastError();
+  return launch_moe_down<FMT, W4, RT, false>(a, h, ws + w.hq, ws + w.hs, plan, 0, s);
 }
 
 template <int FMT, bool W4>
@@ -712,7 +769,7 @@ hipError_t launch_moe_rt(const MoeArgs& a, hipStream_t s) {
   // rows of a segment by the average expert's slots: an expert with more
   // reads its weights again
   const int64_t S = (int64_t)a.T * a.k;
-  if (a.T <= 16 || S <= (int64_t)a.E * 8) return launch_moe<FMT, W4, 1>(a, s);
+  if (a.T <= 16 || S <= (int64_t)a.E * 10) return launch_moe<FMT, W4, 1>(a, s);
   if (a.T <= 32 || S <= (int64_t)a.E * 20) return launch_moe<FMT, W4, 2>(a, s);
   return launch_moe<FMT, W4, 4>(a, s);
 }
