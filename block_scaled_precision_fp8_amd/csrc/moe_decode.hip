@@ -94,35 +94,25 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 }
 
 // One K block of a 16-row weight tile: a lane's 32 codes of row l16, with
-// MXFP4 their scale byte.  FP8: K 16 g4 .. + 15 and 64 + 16 g4 .. + 15 (the
+// MXFP4 the scales as loaded.  FP8: K 16 g4 .. + 15 and 64 + 16 g4 .. + 15 (the
 // order within a block is free while rows and weights agree; four lanes then
 // read 64 bytes in a piece).  MXFP4: the group K 32 g4 .. + 31.
 template <bool W4>
 struct WFrag {
   uint4 c[W4 ? 1 : 2];
   uint32_t s[W4 ? 1 : 0];
-  __device__ __forceinline__ BFrag bf16() const {
-    BFrag f;
-    if constexpr (W4) {
-      const float sc = __uint_as_float(s[0] << 23);  // the conversion reads the exponent field
-      f.v[0] = cvt_e2m1x8(c[0].x, sc); f.v[1] = cvt_e2m1x8(c[0].y, sc);
-      f.v[2] = cvt_e2m1x8(c[0].z, sc); f.v[3] = cvt_e2m1x8(c[0].w, sc);
-    } else {
-      f.v[0] = cvt_e4m3x8(c[0].x, c[0].y); f.v[1] = cvt_e4m3x8(c[0].z, c[0].w);
-      f.v[2] = cvt_e4m3x8(c[1].x, c[1].y); f.v[3] = cvt_e4m3x8(c[1].z, c[1].w);
-    }
-    return f;
-  }
 };
-template <bool W4>
-__device__ __forceinline__ uint32_t piece0(int g4) { return W4 ? 32 * g4 : 16 * g4; }
-template <bool W4>
-__device__ __forceinline__ uint32_t piece1(int g4) { return W4 ? 32 * g4 + 16 : 64 + 16 * g4; }
+// A value per row of a 16-row operand: loaded by the lanes of g4 = 0 only (a
+// load costs its lanes' addresses, not its bytes), spread to all four groups.
+__device__ __forceinline__ uint32_t spread16(uint32_t v, int l16) {
+  return (uint32_t)__builtin_amdgcn_ds_bpermute(l16 * 4, (int)v);
+}
 
-// Up to 16 rows of one expert's weight.  In a row's last, partial K block a lane
-// reads on into the next row: finite values, which meet zeros of the tokens'
-// rows.  Blocks from KB on give zeros and no traffic.
-template <bool W4>
+// Up to 16 rows of one expert's weight.  In a row's last, partial K block a
+// lane reads on into the next row: finite values, which meet zeros of the
+// tokens' rows.  Blocks from KB on give zeros and no traffic.
+// RAGGED (MXFP4): rows of scale bytes that do not begin at a dword.
+template <bool W4, bool RAGGED>
 struct WTile {
   __amdgpu_buffer_rsrc_t codes, scales;
   uint32_t lo, slo, K;
@@ -132,7 +122,7 @@ struct WTile {
     KB = (int)((K_ + 127) / 128);
     g4 = lane >> 4;
     lo = (uint32_t)((lane & 15) * (W4 ? K_ / 2 : K_)) + g4 * 16;
-    slo = (uint32_t)((lane & 15) * (K_ / 32)) + g4;
+    slo = (uint32_t)((lane & 15) * (K_ / 32)) + (RAGGED ? g4 : g4 == 0 ? 0 : kOOB);
   }
   // n <= 16 rows from row0 on; the others give zeros
   __device__ __forceinline__ void aim(const uint8_t* w, const void* sc, int64_t row0, int n) {
@@ -145,26 +135,62 @@ struct WTile {
     const uint32_t o = lo + (kb < KB ? (uint32_t)kb * (W4 ? 64 : 128) : kOOB);
     f.c[0] = ld_buf16(codes, o);
     if constexpr (W4) {
-      // the group itself may lie past the row: its scale is another row's
-      const bool in = (uint32_t)kb * 128 + g4 * 32 < K;
-      f.s[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, in ? slo + (uint32_t)kb * 4 : kOOB, 0, 0);
+      if constexpr (RAGGED) {
+        // the group itself may lie past the row: its scale is another row's
+        const bool in = (uint32_t)kb * 128 + g4 * 32 < K;
+        f.s[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, in ? slo + (uint32_t)kb * 4 : kOOB, 0, 0);
+      } else {
+        f.s[0] = __builtin_amdgcn_raw_buffer_load_b32(scales, slo + (kb < KB ? (uint32_t)kb * 4 : 0x40000000u), 0, 0);
+      }
     } else {
       f.c[1] = ld_buf16(codes, o + 64);
     }
     return f;
   }
-};
-
-// One K block of a token (or h) row: the 32 codes that meet a WFrag's.
-struct XFrag {
-  uint4 c[2];
-  __device__ __forceinline__ BFrag bf16() const {
+  // the codes as bf16, with MXFP4 times their group's scale
+  __device__ __forceinline__ BFrag bf16(const WFrag<W4>& w, int l16) const {
     BFrag f;
-    f.v[0] = cvt_e4m3x8(c[0].x, c[0].y); f.v[1] = cvt_e4m3x8(c[0].z, c[0].w);
-    f.v[2] = cvt_e4m3x8(c[1].x, c[1].y); f.v[3] = cvt_e4m3x8(c[1].z, c[1].w);
+    if constexpr (W4) {
+      const uint32_t b = RAGGED ? w.s[0] : spread16(w.s[0], l16) >> (8 * g4) & 0xff;
+      const float sc = __uint_as_float(b << 23);     // the conversion reads the exponent field
+      f.v[0] = cvt_e2m1x8(w.c[0].x, sc); f.v[1] = cvt_e2m1x8(w.c[0].y, sc);
+      f.v[2] = cvt_e2m1x8(w.c[0].z, sc); f.v[3] = cvt_e2m1x8(w.c[0].w, sc);
+    } else {
+      f.v[0] = cvt_e4m3x8(w.c[0].x, w.c[0].y); f.v[1] = cvt_e4m3x8(w.c[0].z, w.c[0].w);
+      f.v[2] = cvt_e4m3x8(w.c[1].x, w.c[1].y); f.v[3] = cvt_e4m3x8(w.c[1].z, w.c[1].w);
+    }
     return f;
   }
 };
+
+// One K block of 16 token (or h) rows.  Loaded eight lanes to a row, whole
+// 128-byte pieces, and turned into the MFMA's layout through 2 KB of the
+// wave's own LDS: read in that layout (a lane per row) the rows would take
+// as many address cycles as the weights.
+struct XFrag {
+  uint4 c[2];                          // rows lane / 8 and 8 + lane / 8
+};
+__device__ __forceinline__ int xpiece(int row, int piece) {      // LDS offset, banks spread
+  return row * 128 + ((piece ^ (row >> 1 & 7)) * 16);
+}
+__device__ __forceinline__ void x_to_lds(uint8_t* lds, const XFrag& x, int lane) {
+  *(uint4*)(lds + xpiece(lane >> 3, lane & 7)) = x.c[0];
+  *(uint4*)(lds + xpiece(8 + (lane >> 3), lane & 7)) = x.c[1];
+}
+__device__ __forceinline__ BFrag x_bf16(uint4 a, uint4 b) {
+  BFrag f;
+  f.v[0] = cvt_e4m3x8(a.x, a.y); f.v[1] = cvt_e4m3x8(a.z, a.w);
+  f.v[2] = cvt_e4m3x8(b.x, b.y); f.v[3] = cvt_e4m3x8(b.z, b.w);
+  return f;
+}
+// the 32 codes that meet a weight lane's: pieces g4 and 4 + g4, with MXFP4
+// 2 g4 and 2 g4 + 1
+template <bool W4>
+__device__ __forceinline__ BFrag x_from_lds(const uint8_t* lds, int lane) {
+  const int l16 = lane & 15, g4 = lane >> 4;
+  return x_bf16(*(const uint4*)(lds + xpiece(l16, W4 ? 2 * g4 : g4)),
+                *(const uint4*)(lds + xpiece(l16, W4 ? 2 * g4 + 1 : 4 + g4)));
+}
 
 // acc += (W X^T of one K block) * scale: output rows n (registers), slots m
 // (lanes).  c: the row group's scale, times the weight block's (FP8).
@@ -183,30 +209,40 @@ __device__ __forceinline__ v4f moe_step(v4f acc, const BFrag& w, const BFrag& x,
 struct SortedSlots {
   int eid[kMoeMaxSlots];
   int sl[kMoeMaxSlots];                // slot words
-  int seg[kMoeMaxSlots + 1];           // first row of every segment
-  int nsegs, total;
+  uint16_t seg[kMoeMaxSlots + 1];      // first row of every segment
+  int nruns, nsegs, total;
 };
 
-// by one wave, after eid
-template <int ROWS>
-__device__ __forceinline__ void find_segments(SortedSlots& p, int total, int lane) {
-  // a row starts a segment when its place in its run is a multiple of ROWS
-  int n = 0, start = 0;
+// by one wave, after eid: segments of `rows` (a power of two), or just the
+// number of runs (rows 0)
+__device__ __forceinline__ void find_segments(SortedSlots& p, int total, int lane, int rows) {
+  // a row starts a segment when its place in its run is a multiple of rows
+  int n = 0, runs = 0, start = 0;
   for (int i0 = 0; i0 < total; i0 += 64) {
     const int i = i0 + lane;
     const bool run = i < total && (i == 0 || p.eid[i] != p.eid[i - 1]);
-    const unsigned long long b = __ballot(run) & (~0ull >> (63 - lane));
+    const unsigned long long rb = __ballot(run);
+    runs += __popcll(rb);
+    if (rows == 0) continue;
+    const unsigned long long b = rb & (~0ull >> (63 - lane));
     const int mine = b ? i0 + 63 - __clzll(b) : start;     // this row's run's start
-    const bool st = i < total && (i - mine) % ROWS == 0;
+    const bool st = i < total && ((i - mine) & (rows - 1)) == 0;
     const unsigned long long sb = __ballot(st);
-    if (st) p.seg[n + __popcll(sb & ((1ull << lane) - 1))] = i;
+    if (st) p.seg[n + __popcll(sb & ((1ull << lane) - 1))] = (uint16_t)i;
     n += __popcll(sb);
     start = __shfl(mine, 63);
   }
   if (lane == 0) {
-    p.seg[n] = total;
+    p.seg[n] = (uint16_t)total;
     p.nsegs = n;
+    p.nruns = runs;
   }
+}
+
+// Subtiles of 16 rows per segment, by the average run: a run of more rows
+// reads its weights again, a subtile costs registers and a shorter ring.
+__device__ __forceinline__ int subtiles(int total, int runs) {
+  return total <= 10 * runs ? 1 : total <= 20 * runs ? 2 : 4;
 }
 
 // The sort, by the whole workgroup: a slot's place is the number of slots of
@@ -242,30 +278,12 @@ __device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // ------------------------------------------------------------------------
-template <int FMT, bool W4, int RT>
-__global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uint16_t* h,
-                                                                  MoePlan* plan) {
+template <int FMT, bool W4, bool RAGGED, int RT>
+__device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const SortedSlots& p,
+                                        v4f* part, int lane, int wave) {
   constexpr int D = W4 ? (RT == 1 ? 8 : RT == 2 ? 5 : 3) : (RT == 1 ? 5 : RT == 2 ? 4 : 2);
   constexpr int SB = FMT == 0 ? 4 : 1;
-  __shared__ SortedSlots p;
-  // partial products of tasks that begin or end inside a wave's share: [0]
-  // begun by an earlier wave, [1] begun here and left to the next
-  __shared__ v4f part[kMoeWaves][2][2 * RT][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = uniform(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
-  sort_slots(p, (int*)part, a.ids, a.T * a.k, a.k, a.E);
-  const int total = uniform(p.total);
-  if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) plan->total = total;
-    for (int i = threadIdx.x; i < total; i += kMoeThreads) {
-      plan->expert[i] = p.eid[i];
-      plan->slot[i] = p.sl[i];
-    }
-  }
-  if (wave == 0) find_segments<16 * RT>(p, total, lane);
-  __syncthreads();
-
   const int64_t K = a.H, I = a.I;
   const int KB = (int)((K + 127) / 128), CT = (int)(I / 16);
   const int64_t tasks = (int64_t)uniform(p.nsegs) * CT;
@@ -275,6 +293,11 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
   const int64_t it0 = share(wave);
   const int cnt = (int)(share(wave + 1) - it0);
 
+  // partial products of tasks that begin or end inside a wave's share: 0
+  // begun by an earlier wave, 1 begun here and left to the next
+  auto piece = [&](int w, int which, int i) -> v4f& {
+    return part[((w * 2 + which) * 2 * RT + i) * 64 + lane];
+  };
   // h of one task from its products: lane (l16, g4) has columns 4 g4 .. + 3
   // of row l16
   auto finish = [&](const v4f (&g)[RT], const v4f (&u)[RT], int seg, int ct) {
@@ -293,6 +316,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
   };
 
   if (cnt > 0) {
+    uint8_t* xbuf = (uint8_t*)&part[(wave * 2 + 1) * 2 * RT * 64];   // free until the last task
     const __amdgpu_buffer_rsrc_t rows = make_rsrc(a.xq, a.T * K);
     const __amdgpu_buffer_rsrc_t rscales = make_rsrc(a.xs, (int64_t)a.T * KB * SB);
     // two cursors over the wave's items: loads, and products behind them
@@ -300,10 +324,10 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
     int lseg = (int)(task / CT), lct = (int)(task - (int64_t)lseg * CT);
     int lkb = (int)(it0 - it0 / KB * KB), left = cnt;
     int pseg = lseg, pct = lct, pkb = lkb, begun = lkb;
-    const uint32_t k0 = piece0<W4>(g4), k1 = piece1<W4>(g4);
-    uint32_t xo[RT], so[RT];           // the segment's rows; no row: past the buffers
+    const uint32_t xk = (lane & 7) * 16;
+    uint32_t xo[2 * RT], so[RT];       // the segment's rows; no row: past the buffers
     int e = 0;
-    WTile<W4> wg, wu;
+    WTile<W4, RAGGED> wg, wu;
     __amdgpu_buffer_rsrc_t sg, su;
     wg.init(K, lane);
     wu.init(K, lane);
@@ -311,11 +335,14 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
       const int r0 = uniform(p.seg[lseg]), r1 = uniform(p.seg[lseg + 1]);
       e = uniform(p.eid[r0]);
 #pragma unroll
+      for (int r = 0; r < 2 * RT; ++r) {
+        const int i = r0 + 8 * r + (lane >> 3);
+        xo[r] = i < r1 ? token_of(p.sl[i]) * (uint32_t)K + xk : kOOB;
+      }
+#pragma unroll
       for (int r = 0; r < RT; ++r) {
         const int i = r0 + 16 * r + l16;
-        const uint32_t t = i < r1 ? token_of(p.sl[i]) : 0;
-        xo[r] = i < r1 ? t * (uint32_t)K : kOOB;
-        so[r] = i < r1 ? t * (uint32_t)KB * SB : kOOB;
+        so[r] = g4 == 0 && i < r1 ? token_of(p.sl[i]) * (uint32_t)KB * SB : kOOB;
       }
     };
     auto aim = [&]() {
@@ -340,8 +367,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
       const uint32_t k = (uint32_t)kb * 128, sk = in ? (uint32_t)kb * SB : 0x40000000u;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        f.x[r].c[0] = ld_buf16(rows, k + k0 < K ? xo[r] + k + k0 : kOOB);
-        f.x[r].c[1] = ld_buf16(rows, k + k1 < K ? xo[r] + k + k1 : kOOB);
+        f.x[r].c[0] = ld_buf16(rows, k + xk < (uint32_t)K ? xo[2 * r] + k : kOOB);
+        f.x[r].c[1] = ld_buf16(rows, k + xk < (uint32_t)K ? xo[2 * r + 1] + k : kOOB);
         if (FMT == 0) f.sx[r] = __builtin_amdgcn_raw_buffer_load_b32(rscales, so[r] + sk, 0, 0);
         else f.sx[r] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rscales, so[r] + sk, 0, 0);
       }
@@ -375,17 +402,20 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
     for (int i0 = 0; i0 < cnt; i0 += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        // items past the share are zeros times zeros
-        const BFrag bg = ring[d].g.bf16(), bu = ring[d].u.bf16();
-        const float cg = W4 ? 1.f : scale_value<FMT>(ring[d].sg);
-        const float cu = W4 ? 1.f : scale_value<FMT>(ring[d].su);
+        if (i0 + d < cnt) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          if (r > 0 && prows <= 16 * r) break;
-          const BFrag bx = ring[d].x[r].bf16();
-          const float sx = scale_value<FMT>(ring[d].sx[r]);
-          ag[r] = moe_step(ag[r], bg, bx, sx * cg);
-          au[r] = moe_step(au[r], bu, bx, sx * cu);
+          for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[r], lane);
+          const BFrag bg = wg.bf16(ring[d].g, l16), bu = wu.bf16(ring[d].u, l16);
+          const float cg = W4 ? 1.f : scale_value<FMT>(ring[d].sg);
+          const float cu = W4 ? 1.f : scale_value<FMT>(ring[d].su);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            if (r > 0 && prows <= 16 * r) break;
+            const BFrag bx = x_from_lds<W4>(xbuf + r * 2048, lane);
+            const float sx = scale_value<FMT>(spread16(ring[d].sx[r], l16));
+            ag[r] = moe_step(ag[r], bg, bx, sx * cg);
+            au[r] = moe_step(au[r], bu, bx, sx * cu);
+          }
         }
         next(ring[d]);
         const bool last = i0 + d + 1 == cnt;
@@ -395,8 +425,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
           } else {
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-              part[wave][begun == 0][2 * r][lane] = ag[r];
-              part[wave][begun == 0][2 * r + 1][lane] = au[r];
+              piece(wave, begun == 0, 2 * r) = ag[r];
+              piece(wave, begun == 0, 2 * r + 1) = au[r];
             }
           }
 #pragma unroll
@@ -421,16 +451,16 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
       v4f g[RT], u[RT];
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        g[r] = part[wave][1][2 * r][lane];
-        u[r] = part[wave][1][2 * r + 1][lane];
+        g[r] = piece(wave, 1, 2 * r);
+        u[r] = piece(wave, 1, 2 * r + 1);
       }
       const int64_t end = (share(wave + 1) / KB + 1) * KB;
       for (int w = wave + 1; w < kMoeWaves; ++w) {
         if (share(w) == share(w + 1)) continue;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          g[r] += part[w][0][2 * r][lane];
-          u[r] += part[w][0][2 * r + 1][lane];
+          g[r] += piece(w, 0, 2 * r);
+          u[r] += piece(w, 0, 2 * r + 1);
         }
         if (share(w + 1) >= end) break;
       }
@@ -441,6 +471,36 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
   }
 }
 
+// MANY: more than 16 tokens, so that an expert can have more than 16 slots.
+template <int FMT, bool W4, bool RAGGED, bool MANY>
+__global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uint16_t* h,
+                                                                  MoePlan* plan) {
+  __shared__ SortedSlots p;
+  __shared__ v4f part[kMoeWaves * 2 * 2 * (MANY ? 4 : 1) * 64];
+  const int lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
+  sort_slots(p, (int*)part, a.ids, a.T * a.k, a.k, a.E);
+  const int total = uniform(p.total);
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) plan->total = total;
+    for (int i = threadIdx.x; i < total; i += kMoeThreads) {
+      plan->expert[i] = p.eid[i];
+      plan->slot[i] = p.sl[i];
+    }
+  }
+  if (wave == 0) {
+    find_segments(p, total, lane, MANY ? 0 : 16);
+    if (MANY) find_segments(p, total, lane, 16 * subtiles(total, uniform(p.nruns)));
+  }
+  __syncthreads();
+  const int rt = MANY ? subtiles(total, uniform(p.nruns)) : 1;
+  if (rt == 1) gate_up<FMT, W4, RAGGED, 1>(a, h, p, part, lane, wave);
+  if constexpr (MANY) {
+    if (rt == 2) gate_up<FMT, W4, RAGGED, 2>(a, h, p, part, lane, wave);
+    if (rt == 4) gate_up<FMT, W4, RAGGED, 4>(a, h, p, part, lane, wave);
+  }
+}
+
 // ------------------------------------------------------------------------
 // QUANT: h comes as bf16 and is quantized here, all rows into LDS, by every
 // workgroup (launches with few rows); else as codes and scales.
@@ -448,49 +508,20 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
 // multiple of 4, the last tile partly empty), so that H / R workgroups can
 // match the CUs.
 template <int FMT, bool W4, int RT, bool QUANT, int NT>
-__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const uint16_t* h,
-                                                               const uint8_t* hq, const void* hs,
-                                                               const MoePlan* plan, int R) {
+__device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const uint8_t* hq,
+                                     const void* hs, const SortedSlots& p, const float* swt,
+                                     float* mine, uint8_t* xl, int total, int R, int lane,
+                                     int wave) {
   constexpr int D = (QUANT ? 6 : RT == 1 ? 4 : RT == 2 ? 3 : 2) / (QUANT && NT == 2 ? 2 : 1) * (W4 && QUANT ? 2 : 1);
   constexpr int SB = FMT == 0 ? 4 : 1;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // sums, codes and scales of h
-  __shared__ SortedSlots p;
-  __shared__ float swt[kMoeMaxSlots];  // the sorted slots' weights
-  const int lane = threadIdx.x & 63;
-  const int wave = uniform(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
   const int T = a.T;
   const int64_t N = a.H, K = a.I, n0 = (int64_t)blockIdx.x * R;
   const int KB = (int)(K / 128);
-  float* sums = (float*)lds;           // [waves][T][R]
+  // QUANT: codes of the sorted rows, then their scales; else 2 KB RT a wave
   const int stride = (int)K + 16;      // 16: rows start in different banks
-  uint8_t* xl = lds + kMoeWaves * T * R * 4;
   float* xs = (float*)(xl + (QUANT ? (int64_t)T * a.k * stride : 0));
-
-  const int total = uniform(plan->total);
-  float* mine = sums + wave * T * R;
-  for (int i = lane * 4; i < T * R; i += 256) *(float4*)(mine + i) = make_float4(0, 0, 0, 0);
-  for (int i = threadIdx.x; i < total; i += kMoeThreads) {
-    p.eid[i] = plan->expert[i];
-    const int w = plan->slot[i];
-    p.sl[i] = w;
-    swt[i] = a.wt[slot_of(w)];
-  }
-  __syncthreads();
-  if (wave == 0) {
-    find_segments<16 * RT>(p, total, lane);
-  } else if (wave == 1) {
-    // a token that names an expert twice has neighbouring rows in its run:
-    // number them, so that they add to the token's sum one after the other
-    for (int i = lane; i < total; i += 64) {
-      int nth = 0;
-      while (nth < i && p.eid[i - nth - 1] == p.eid[i] &&
-             token_of(p.sl[i - nth - 1]) == token_of(p.sl[i]))
-        ++nth;
-      if (nth) atomicOr(&p.sl[i], nth << 18);
-    }
-  }
-  __syncthreads();
+  uint8_t* xbuf = xl + wave * 2048 * RT;
 
   const int64_t items = (int64_t)uniform(p.nsegs) * KB;
   const int64_t it0 = items * wave / kMoeWaves;
@@ -501,8 +532,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
   // two cursors over the wave's items: loads, and products behind them
   int lseg = (int)(it0 / KB), lkb = (int)(it0 - (int64_t)lseg * KB), left = cnt;
   int pseg = lseg, pkb = lkb;
-  uint32_t xo[RT], so[RT];             // the segment's rows; no row: past the buffers
-  WTile<W4> wt[NT];
+  uint32_t xo[2 * RT], so[RT];         // the segment's rows; no row: past the buffers
+  WTile<W4, false> wt[NT];
   __amdgpu_buffer_rsrc_t sw;
   uint32_t swo[NT];                    // this lane's four outputs' row of block scales
 #pragma unroll
@@ -521,11 +552,14 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
                      min((int64_t)2, NB - n0 / 128) * KB * SB);
     if (!QUANT) {
 #pragma unroll
+      for (int r = 0; r < 2 * RT; ++r) {
+        const int i = r0 + 8 * r + (lane >> 3);
+        xo[r] = i < r1 ? slot_of(p.sl[i]) * (uint32_t)K + (lane & 7) * 16 : kOOB;
+      }
+#pragma unroll
       for (int r = 0; r < RT; ++r) {
         const int i = r0 + 16 * r + l16;
-        const uint32_t s = i < r1 ? slot_of(p.sl[i]) : 0;
-        xo[r] = i < r1 ? s * (uint32_t)K : kOOB;
-        so[r] = i < r1 ? s * (uint32_t)KB * SB : kOOB;
+        so[r] = g4 == 0 && i < r1 ? slot_of(p.sl[i]) * (uint32_t)KB * SB : kOOB;
       }
     }
   };
@@ -544,8 +578,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
       const uint32_t k = in ? (uint32_t)lkb * 128 : 0x40000000u;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        f.x[r].c[0] = ld_buf16(rows, xo[r] + k + piece0<W4>(g4));
-        f.x[r].c[1] = ld_buf16(rows, xo[r] + k + piece1<W4>(g4));
+        f.x[r].c[0] = ld_buf16(rows, xo[2 * r] + k);
+        f.x[r].c[1] = ld_buf16(rows, xo[2 * r + 1] + k);
         if (FMT == 0) f.sx[r] = __builtin_amdgcn_raw_buffer_load_b32(rscales, so[r] + sk, 0, 0);
         else f.sx[r] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rscales, so[r] + sk, 0, 0);
       }
@@ -613,30 +647,34 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
     for (int i0 = 0; i0 < cnt; i0 += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        // items past the share are zeros times finite values
+        if (i0 + d < cnt) {
+        if constexpr (!QUANT) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[r], lane);
+        }
         BFrag bw[NT];
         float cw[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          bw[j] = ring[d].w[j].bf16();
+          bw[j] = wt[j].bf16(ring[d].w[j], l16);
           cw[j] = W4 ? 1.f : scale_value<FMT>(ring[d].sw[j]);
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           if (r > 0 && prows <= 16 * r) break;
-          XFrag x;
+          BFrag bx;
           float sx;
           if constexpr (QUANT) {
-            x.c[0] = *(const uint4*)(px[r] + pkb * 128 + piece0<W4>(g4));
-            x.c[1] = *(const uint4*)(px[r] + pkb * 128 + piece1<W4>(g4));
+            bx = x_bf16(*(const uint4*)(px[r] + pkb * 128 + (W4 ? 32 * g4 : 16 * g4)),
+                        *(const uint4*)(px[r] + pkb * 128 + (W4 ? 32 * g4 + 16 : 64 + 16 * g4)));
             sx = ps[r][pkb];
           } else {
-            x = ring[d].x[r];
-            sx = scale_value<FMT>(ring[d].sx[r]);
+            bx = x_from_lds<W4>(xbuf + r * 2048, lane);
+            sx = scale_value<FMT>(spread16(ring[d].sx[r], l16));
           }
-          const BFrag bx = x.bf16();
 #pragma unroll
           for (int j = 0; j < NT; ++j) acc[r][j] = moe_step(acc[r][j], bw[j], bx, sx * cw[j]);
+        }
         }
         next(ring[d]);
         const bool last = i0 + d + 1 == cnt;
@@ -670,13 +708,58 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
             ++pseg;
             prows = uniform(p.seg[pseg + 1] - p.seg[pseg]);
             if (QUANT) aim_products();
-          } else {
-            pkb = 0;                   // what is left of the ring reads row starts
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+  }
+}
+
+template <int FMT, bool W4, bool QUANT, int NT, bool MANY>
+__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const uint16_t* h,
+                                                               const uint8_t* hq, const void* hs,
+                                                               const MoePlan* plan, int R) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // sums, then the rows of h
+  __shared__ SortedSlots p;
+  __shared__ float swt[kMoeMaxSlots];  // the sorted slots' weights
+  const int lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int T = a.T;
+  const int64_t N = a.H, n0 = (int64_t)blockIdx.x * R;
+  float* sums = (float*)lds;           // [waves][T][R]
+  uint8_t* xl = lds + kMoeWaves * T * R * 4;
+
+  const int total = uniform(plan->total);
+  float* mine = sums + wave * T * R;
+  for (int i = lane * 4; i < T * R; i += 256) *(float4*)(mine + i) = make_float4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < total; i += kMoeThreads) {
+    p.eid[i] = plan->expert[i];
+    const int w = plan->slot[i];
+    p.sl[i] = w;
+    swt[i] = a.wt[slot_of(w)];
+  }
+  __syncthreads();
+  if (wave == 0) {
+    find_segments(p, total, lane, MANY ? 0 : 16);
+    if (MANY) find_segments(p, total, lane, 16 * subtiles(total, uniform(p.nruns)));
+  } else if (wave == 1) {
+    // a token that names an expert twice has neighbouring rows in its run:
+    // number them, so that they add to the token's sum one after the other
+    for (int i = lane; i < total; i += 64) {
+      int nth = 0;
+      while (nth < i && p.eid[i - nth - 1] == p.eid[i] &&
+             token_of(p.sl[i - nth - 1]) == token_of(p.sl[i]))
+        ++nth;
+      if (nth) atomicOr(&p.sl[i], nth << 18);
+    }
+  }
+  __syncthreads();
+  const int rt = MANY ? subtiles(total, uniform(p.nruns)) : 1;
+  if (rt == 1) down<FMT, W4, 1, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, total, R, lane, wave);
+  if constexpr (MANY) {
+    if (rt == 2) down<FMT, W4, 2, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, total, R, lane, wave);
+    if (rt == 4) down<FMT, W4, 4, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, total, R, lane, wave);
   }
   __syncthreads();
   const int Q = R / 4;
@@ -730,48 +813,48 @@ inline int moe_down_rows(int64_t H, int T) {
   return best;
 }
 
-template <int FMT, bool W4, int RT, bool QUANT>
+template <int FMT, bool W4, bool QUANT, bool MANY>
 hipError_t launch_moe_down(const MoeArgs& a, const uint16_t* h, const uint8_t* hq, const void* hs,
                            const MoePlan* plan, size_t lds, hipStream_t s) {
   const int R = moe_down_rows(a.H, a.T);
   const dim3 grid((unsigned)((a.H + R - 1) / R));
   lds += (size_t)kMoeWaves * a.T * R * 4;
   if (R <= 16)
-    hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT, QUANT, 1>), grid, dim3(kMoeThreads), lds, s, a,
-                       h, hq, hs, plan, R);
+    hipLaunchKernelGGL((moe_down_kernel<FMT, W4, QUANT, 1, MANY>), grid, dim3(kMoeThreads), lds, s,
+                       a, h, hq, hs, plan, R);
   else
-    hipLaunchKernelGGL((moe_down_kernel<FMT, W4, RT, QUANT, 2>), grid, dim3(kMoeThreads), lds, s, a,
-                       h, hq, hs, plan, R);
+    hipLaunchKernelGGL((moe_down_kernel<FMT, W4, QUANT, 2, MANY>), grid, dim3(kMoeThreads), lds, s,
+                       a, h, hq, hs, plan, R);
   return hipGetLastError();
 }
 
-template <int FMT, bool W4, int RT>
+template <int FMT, bool W4, bool MANY>
 hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
   const int64_t S = (int64_t)a.T * a.k;
   const MoeWorkspace w = moe_layout(S, a.I);
   uint8_t* ws = (uint8_t*)a.workspace;
   MoePlan* plan = (MoePlan*)ws;
   uint16_t* h = (uint16_t*)(ws + w.h);
-  hipLaunchKernelGGL((moe_gate_up_kernel<FMT, W4, RT>), dim3(kMoeGateUpGroups), dim3(kMoeThreads),
-                     0, s, a, h, plan);
+  if (W4 && a.H % 128 != 0)
+    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, W4, W4, MANY>), dim3(kMoeGateUpGroups),
+                       dim3(kMoeThreads), 0, s, a, h, plan);
+  else
+    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, W4, false, MANY>), dim3(kMoeGateUpGroups),
+                       dim3(kMoeThreads), 0, s, a, h, plan);
   hipError_t r = hipGetLastError();
   if (r != hipSuccess) return r;
   const int64_t codes = S * (a.I + 16 + a.I / 128 * 4);
   if (codes <= kMoeQuantBytes)
-    return launch_moe_down<FMT, W4, RT, true>(a, h, nullptr, nullptr, plan, (size_t)codes, s);
+    return launch_moe_down<FMT, W4, true, MANY>(a, h, nullptr, nullptr, plan, (size_t)codes, s);
   r = launch_quant_act(h, S, a.I, a.I, FMT, ws + w.hq, ws + w.hs, s);
   if (r != hipSuccess) return r;
-  return launch_moe_down<FMT, W4, RT, false>(a, h, ws + w.hq, ws + w.hs, plan, 0, s);
+  return launch_moe_down<FMT, W4, false, MANY>(a, h, ws + w.hq, ws + w.hs, plan,
+                                               (size_t)kMoeWaves * 2048 * (MANY ? 4 : 1), s);
 }
 
 template <int FMT, bool W4>
-hipError_t launch_moe_rt(const MoeArgs& a, hipStream_t s) {
-  // rows of a segment by the average expert's slots: an expert with more
-  // reads its weights again
-  const int64_t S = (int64_t)a.T * a.k;
-  if (a.T <= 16 || S <= (int64_t)a.E * 10) return launch_moe<FMT, W4, 1>(a, s);
-  if (a.T <= 32 || S <= (int64_t)a.E * 20) return launch_moe<FMT, W4, 2>(a, s);
-  return launch_moe<FMT, W4, 4>(a, s);
+hipError_t launch_moe_many(const MoeArgs& a, hipStream_t s) {
+  return a.T > 16 ? launch_moe<FMT, W4, true>(a, s) : launch_moe<FMT, W4, false>(a, s);
 }
 
 }  // namespace detail
@@ -780,8 +863,8 @@ using namespace detail;
 size_t moe_decode_workspace_bytes(int64_t S, int64_t I) { return moe_layout(S, I).bytes; }
 
 hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t s) {
-  if (a.w4) return a.fmt == 0 ? launch_moe_rt<0, true>(a, s) : launch_moe_rt<1, true>(a, s);
-  return a.fmt == 0 ? launch_moe_rt<0, false>(a, s) : launch_moe_rt<1, false>(a, s);
+  if (a.w4) return a.fmt == 0 ? launch_moe_many<0, true>(a, s) : launch_moe_many<1, true>(a, s);
+  return a.fmt == 0 ? launch_moe_many<0, false>(a, s) : launch_moe_many<1, false>(a, s);
 }
 
 }  // namespace bsfp8
