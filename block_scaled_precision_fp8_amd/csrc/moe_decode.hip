@@ -100,7 +100,7 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 template <bool W4>
 struct WFrag {
   uint4 c[W4 ? 1 : 2];
-  uint32_t s[W4 ? 1 : 0];
+  uint32_t s[W4 ? 1 : 0];              // not with ScaleChunk
 };
 // A value per row of a 16-row operand: loaded by the lanes of g4 = 0 only (a
 // load costs its lanes' addresses, not its bytes), spread to all four groups.
@@ -108,11 +108,18 @@ __device__ __forceinline__ uint32_t spread16(uint32_t v, int l16) {
   return (uint32_t)__builtin_amdgcn_ds_bpermute(l16 * 4, (int)v);
 }
 
+// How MXFP4 scale bytes reach a weight lane: a byte per lane and block (rows
+// of scales that do not begin at a dword), a dword per row and block, or
+// through LDS, 32 blocks of 16 rows at a time (ScaleChunk).  A row's scales
+// for 32 blocks share one cache line, which has left the L1 before the next
+// block: the first two fetch it again for every block, as many bytes as four
+// times the weights.
+enum ScaleMode { kScaleByte, kScaleDword, kScaleChunk };
+
 // Up to 16 rows of one expert's weight.  In a row's last, partial K block a
 // lane reads on into the next row: finite values, which meet zeros of the
 // tokens' rows.  Blocks from KB on give zeros and no traffic.
-// RAGGED (MXFP4): rows of scale bytes that do not begin at a dword.
-template <bool W4, bool RAGGED>
+template <bool W4, ScaleMode SM>
 struct WTile {
   __amdgpu_buffer_rsrc_t codes, scales;
   uint32_t lo, slo, K;
@@ -122,24 +129,25 @@ struct WTile {
     KB = (int)((K_ + 127) / 128);
     g4 = lane >> 4;
     lo = (uint32_t)((lane & 15) * (W4 ? K_ / 2 : K_)) + g4 * 16;
-    slo = (uint32_t)((lane & 15) * (K_ / 32)) + (RAGGED ? g4 : g4 == 0 ? 0 : kOOB);
+    slo = (uint32_t)((lane & 15) * (K_ / 32)) + (SM == kScaleByte ? g4 : g4 == 0 ? 0 : kOOB);
   }
   // n <= 16 rows from row0 on; the others give zeros
   __device__ __forceinline__ void aim(const uint8_t* w, const void* sc, int64_t row0, int n) {
     const int64_t KW = W4 ? K / 2 : K;
     codes = make_rsrc(w + row0 * KW, n * KW);
-    if (W4) scales = make_rsrc((const uint8_t*)sc + row0 * (K / 32), (int64_t)n * (K / 32));
+    if (W4 && SM != kScaleChunk)
+      scales = make_rsrc((const uint8_t*)sc + row0 * (K / 32), (int64_t)n * (K / 32));
   }
   __device__ __forceinline__ WFrag<W4> load(int kb) const {
     WFrag<W4> f;
     const uint32_t o = lo + (kb < KB ? (uint32_t)kb * (W4 ? 64 : 128) : kOOB);
     f.c[0] = ld_buf16(codes, o);
     if constexpr (W4) {
-      if constexpr (RAGGED) {
+      if constexpr (SM == kScaleByte) {
         // the group itself may lie past the row: its scale is another row's
         const bool in = (uint32_t)kb * 128 + g4 * 32 < K;
         f.s[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, in ? slo + (uint32_t)kb * 4 : kOOB, 0, 0);
-      } else {
+      } else if constexpr (SM == kScaleDword) {
         f.s[0] = __builtin_amdgcn_raw_buffer_load_b32(scales, slo + (kb < KB ? (uint32_t)kb * 4 : 0x40000000u), 0, 0);
       }
     } else {
@@ -147,11 +155,15 @@ struct WTile {
     }
     return f;
   }
-  // the codes as bf16, with MXFP4 times their group's scale
-  __device__ __forceinline__ BFrag bf16(const WFrag<W4>& w, int l16) const {
+  // the codes as bf16, with MXFP4 times their group's scale; chunk: the
+  // block's column of this row's dwords in LDS
+  __device__ __forceinline__ BFrag bf16(const WFrag<W4>& w, int l16, const uint32_t* chunk) const {
     BFrag f;
     if constexpr (W4) {
-      const uint32_t b = RAGGED ? w.s[0] : spread16(w.s[0], l16) >> (8 * g4) & 0xff;
+      uint32_t b;
+      if (SM == kScaleByte) b = w.s[0];
+      else if (SM == kScaleDword) b = spread16(w.s[0], l16) >> (8 * g4) & 0xff;
+      else b = *chunk >> (8 * g4) & 0xff;
       const float sc = __uint_as_float(b << 23);     // the conversion reads the exponent field
       f.v[0] = cvt_e2m1x8(w.c[0].x, sc); f.v[1] = cvt_e2m1x8(w.c[0].y, sc);
       f.v[2] = cvt_e2m1x8(w.c[0].z, sc); f.v[3] = cvt_e2m1x8(w.c[0].w, sc);
@@ -160,6 +172,28 @@ struct WTile {
       f.v[2] = cvt_e4m3x8(w.c[1].x, w.c[1].y); f.v[3] = cvt_e4m3x8(w.c[1].z, w.c[1].w);
     }
     return f;
+  }
+};
+
+// The scale dwords (four groups, one K block) of 16 rows and 32 blocks:
+// loaded into registers a chunk ahead, then kept in the wave's own LDS.
+constexpr int kChunk = 32, kChunkRow = kChunk + 1;         // + 1: rows in different banks
+constexpr int kChunkDwords = 16 * kChunkRow;
+struct ScaleChunk {
+  uint32_t v[8];
+  // K % 128 == 0
+  __device__ __forceinline__ void load(const void* sc, int64_t row0, int n, int64_t K, int kb0,
+                                       int lane) {
+    const uint32_t row = (uint32_t)(K / 32), kb = kb0 + (lane & 31);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc((const uint8_t*)sc + row0 * row, (int64_t)n * row);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      v[q] = __builtin_amdgcn_raw_buffer_load_b32(
+          r, kb * 4 < row ? (2 * q + (lane >> 5)) * row + kb * 4 : kOOB, 0, 0);
+  }
+  __device__ __forceinline__ void store(uint32_t* lds, int lane) const {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) lds[(2 * q + (lane >> 5)) * kChunkRow + (lane & 31)] = v[q];
   }
 };
 
@@ -281,6 +315,8 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 template <int FMT, bool W4, bool RAGGED, int RT>
 __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const SortedSlots& p,
                                         v4f* part, int lane, int wave) {
+  constexpr ScaleMode SM = RAGGED ? kScaleByte : RT == 4 ? kScaleDword : kScaleChunk;
+  constexpr bool CHUNK = W4 && SM == kScaleChunk;
   constexpr int D = W4 ? (RT == 1 ? 8 : RT == 2 ? 5 : 3) : (RT == 1 ? 5 : RT == 2 ? 4 : 2);
   constexpr int SB = FMT == 0 ? 4 : 1;
   const int l16 = lane & 15, g4 = lane >> 4;
@@ -317,6 +353,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
 
   if (cnt > 0) {
     uint8_t* xbuf = (uint8_t*)&part[(wave * 2 + 1) * 2 * RT * 64];   // free until the last task
+    uint32_t* chunks = (uint32_t*)&part[kMoeWaves * 4 * RT * 64] + wave * 2 * kChunkDwords;
     const __amdgpu_buffer_rsrc_t rows = make_rsrc(a.xq, a.T * K);
     const __amdgpu_buffer_rsrc_t rscales = make_rsrc(a.xs, (int64_t)a.T * KB * SB);
     // two cursors over the wave's items: loads, and products behind them
@@ -327,7 +364,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
     const uint32_t xk = (lane & 7) * 16;
     uint32_t xo[2 * RT], so[RT];       // the segment's rows; no row: past the buffers
     int e = 0;
-    WTile<W4, RAGGED> wg, wu;
+    WTile<W4, SM> wg, wu;
     __amdgpu_buffer_rsrc_t sg, su;
     wg.init(K, lane);
     wu.init(K, lane);
@@ -391,10 +428,30 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
         aim();
       }
     };
+    // scale chunks: loaded one ahead of the products
+    ScaleChunk cg4, cu4;
+    int cseg = pseg, cct = pct, ckb = pkb & ~(kChunk - 1), cleft = cnt + (pkb - ckb);
+    auto next_chunk = [&]() {
+      if (cleft <= 0) return;
+      const int64_t row = (int64_t)uniform(p.eid[uniform(p.seg[cseg])]) * 2 * I + cct * 16;
+      cg4.load(a.s13, row, 16, K, ckb, lane);
+      cu4.load(a.s13, row + I, 16, K, ckb, lane);
+      cleft -= min(kChunk, KB - ckb);
+      ckb += kChunk;
+      if (ckb >= KB) {
+        ckb = 0;
+        if (++cct == CT) {
+          cct = 0;
+          ++cseg;
+        }
+      }
+    };
+    if (CHUNK) next_chunk();
     aim_rows();
     aim();
 #pragma unroll
     for (int d = 0; d < D; ++d) next(ring[d]);
+    bool fresh = true;                 // the products enter a chunk
     v4f ag[RT], au[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) ag[r] = au[r] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -405,7 +462,13 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
         if (i0 + d < cnt) {
 #pragma unroll
           for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[r], lane);
-          const BFrag bg = wg.bf16(ring[d].g, l16), bu = wu.bf16(ring[d].u, l16);
+          if (CHUNK && fresh) {
+            cg4.store(chunks, lane);
+            cu4.store(chunks + kChunkDwords, lane);
+            next_chunk();
+          }
+          const uint32_t* ch = chunks + l16 * kChunkRow + (pkb & (kChunk - 1));
+          const BFrag bg = wg.bf16(ring[d].g, l16, ch), bu = wu.bf16(ring[d].u, l16, ch + kChunkDwords);
           const float cg = W4 ? 1.f : scale_value<FMT>(ring[d].sg);
           const float cu = W4 ? 1.f : scale_value<FMT>(ring[d].su);
 #pragma unroll
@@ -440,6 +503,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
             }
           }
         }
+        fresh = (pkb & (kChunk - 1)) == 0;
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -476,7 +540,10 @@ template <int FMT, bool W4, bool RAGGED, bool MANY>
 __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uint16_t* h,
                                                                   MoePlan* plan) {
   __shared__ SortedSlots p;
-  __shared__ v4f part[kMoeWaves * 2 * 2 * (MANY ? 4 : 1) * 64];
+  // partial products of 1, 2 or 4 subtiles, up to 2 with the scale chunks behind
+  constexpr int kPart = kMoeWaves * 4 * 64, kChunks = W4 ? kMoeWaves * 2 * kChunkDwords / 4 : 0;
+  __shared__ v4f part[MANY ? (4 * kPart > 2 * kPart + kChunks ? 4 * kPart : 2 * kPart + kChunks)
+                           : kPart + kChunks];
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   sort_slots(p, (int*)part, a.ids, a.T * a.k, a.k, a.E);
@@ -518,7 +585,12 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
   const int T = a.T;
   const int64_t N = a.H, K = a.I, n0 = (int64_t)blockIdx.x * R;
   const int KB = (int)(K / 128);
-  // QUANT: codes of the sorted rows, then their scales; else 2 KB RT a wave
+  constexpr ScaleMode SM = RT == 4 && !QUANT ? kScaleDword : kScaleChunk;
+  constexpr bool CHUNK = W4 && SM == kScaleChunk;
+  // scale chunks; QUANT: codes of the sorted rows, then their scales; else 2
+  // KB RT a wave
+  uint32_t* chunks = (uint32_t*)xl + wave * NT * kChunkDwords;
+  if (CHUNK) xl += kMoeWaves * NT * kChunkDwords * 4;
   const int stride = (int)K + 16;      // 16: rows start in different banks
   float* xs = (float*)(xl + (QUANT ? (int64_t)T * a.k * stride : 0));
   uint8_t* xbuf = xl + wave * 2048 * RT;
@@ -533,7 +605,7 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
   int lseg = (int)(it0 / KB), lkb = (int)(it0 - (int64_t)lseg * KB), left = cnt;
   int pseg = lseg, pkb = lkb;
   uint32_t xo[2 * RT], so[RT];         // the segment's rows; no row: past the buffers
-  WTile<W4, false> wt[NT];
+  WTile<W4, SM> wt[NT];
   __amdgpu_buffer_rsrc_t sw;
   uint32_t swo[NT];                    // this lane's four outputs' row of block scales
 #pragma unroll
@@ -597,7 +669,24 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
       aim();
     }
   };
+  // scale chunks: loaded one ahead of the products
+  ScaleChunk c4[NT];
+  int cseg = pseg, ckb = pkb & ~(kChunk - 1), cleft = cnt + (pkb - ckb);
+  auto next_chunk = [&]() {
+    if (cleft <= 0) return;
+    const int64_t row = (int64_t)uniform(p.eid[uniform(p.seg[cseg])]) * N + n0;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      c4[j].load(a.s2, row + 16 * j, max(0, min(16, nrows - 16 * j)), K, ckb, lane);
+    cleft -= min(kChunk, KB - ckb);
+    ckb += kChunk;
+    if (ckb >= KB) {
+      ckb = 0;
+      ++cseg;
+    }
+  };
   if (cnt > 0) {
+    if (CHUNK) next_chunk();
     aim();
 #pragma unroll
     for (int d = 0; d < D; ++d) next(ring[d]);
@@ -644,6 +733,7 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
     int prows = uniform(p.seg[pseg + 1] - p.seg[pseg]);
+    bool fresh = true;                 // the products enter a chunk
     for (int i0 = 0; i0 < cnt; i0 += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
@@ -652,11 +742,17 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
 #pragma unroll
           for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[r], lane);
         }
+        if (CHUNK && fresh) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) c4[j].store(chunks + j * kChunkDwords, lane);
+          next_chunk();
+        }
+        const uint32_t* ch = chunks + l16 * kChunkRow + (pkb & (kChunk - 1));
         BFrag bw[NT];
         float cw[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          bw[j] = wt[j].bf16(ring[d].w[j], l16);
+          bw[j] = wt[j].bf16(ring[d].w[j], l16, ch + j * kChunkDwords);
           cw[j] = W4 ? 1.f : scale_value<FMT>(ring[d].sw[j]);
         }
 #pragma unroll
@@ -710,6 +806,7 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
             if (QUANT) aim_products();
           }
         }
+        fresh = (pkb & (kChunk - 1)) == 0;
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -796,6 +893,7 @@ inline MoeWorkspace moe_layout(int64_t S, int64_t I) {
 
 constexpr int kMoeGateUpGroups = 256;      // one workgroup per CU
 constexpr int64_t kMoeQuantBytes = 49152;  // h in LDS, quantized by the down launch
+constexpr size_t kMoeDownBytes = 163840 - sizeof(SortedSlots) - kMoeMaxSlots * 4;
 
 // Output features of a down workgroup: a multiple of 4 from 8 to 32 (to 16
 // where the sums of more would not fit the LDS) with the least to do on the
@@ -813,12 +911,20 @@ inline int moe_down_rows(int64_t H, int T) {
   return best;
 }
 
+// LDS of a down workgroup: the sums, and the scale chunks of MXFP4 weights
+inline size_t moe_sums_bytes(const MoeArgs& a) {
+  return (size_t)kMoeWaves * a.T * moe_down_rows(a.H, a.T) * 4;
+}
+inline size_t moe_chunk_bytes(const MoeArgs& a) {
+  return a.w4 ? (size_t)kMoeWaves * (moe_down_rows(a.H, a.T) > 16 ? 2 : 1) * kChunkDwords * 4 : 0;
+}
+
 template <int FMT, bool W4, bool QUANT, bool MANY>
 hipError_t launch_moe_down(const MoeArgs& a, const uint16_t* h, const uint8_t* hq, const void* hs,
                            const MoePlan* plan, size_t lds, hipStream_t s) {
   const int R = moe_down_rows(a.H, a.T);
   const dim3 grid((unsigned)((a.H + R - 1) / R));
-  lds += (size_t)kMoeWaves * a.T * R * 4;
+  lds += moe_sums_bytes(a);
   if (R <= 16)
     hipLaunchKernelGGL((moe_down_kernel<FMT, W4, QUANT, 1, MANY>), grid, dim3(kMoeThreads), lds, s,
                        a, h, hq, hs, plan, R);
@@ -844,12 +950,16 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
   hipError_t r = hipGetLastError();
   if (r != hipSuccess) return r;
   const int64_t codes = S * (a.I + 16 + a.I / 128 * 4);
-  if (codes <= kMoeQuantBytes)
-    return launch_moe_down<FMT, W4, true, MANY>(a, h, nullptr, nullptr, plan, (size_t)codes, s);
+  const size_t chunks = moe_chunk_bytes(a);
+  if (codes <= kMoeQuantBytes && (size_t)codes + chunks + moe_sums_bytes(a) <= kMoeDownBytes)
+    return launch_moe_down<FMT, W4, true, MANY>(a, h, nullptr, nullptr, plan, codes + chunks, s);
   r = launch_quant_act(h, S, a.I, a.I, FMT, ws + w.hq, ws + w.hs, s);
   if (r != hipSuccess) return r;
   return launch_moe_down<FMT, W4, false, MANY>(a, h, ws + w.hq, ws + w.hs, plan,
-                                               (size_t)kMoeWaves * 2048 * (MANY ? 4 : 1), s);
+                                               // 4 subtiles, or up to 2 beside the scale chunks
+                                               MANY ? std::max((size_t)kMoeWaves * 8192,
+                                                               chunks + kMoeWaves * 4096)
+                                                    : chunks + kMoeWaves * 2048, s);
 }
 
 template <int FMT, bool W4>
