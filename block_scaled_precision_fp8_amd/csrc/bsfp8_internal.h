@@ -264,6 +264,7 @@ struct NormArgs {
   void* xs;
   const void* xstat;         // the static scheme's scale, or null
   float eps;
+  double inv_k;              // 1 / K
   int64_t M, K;
   int fmt, group_k;
 };
@@ -277,6 +278,8 @@ struct RouteArgs {
   int E, k, score, renorm;
   float scale;
   int n_group, topk_group;
+  int group_lanes;           // set by the launcher: lanes that scan a group,
+  uint32_t group_rcp;        // 2^20 / (experts of a group), rounded up
   int32_t* ids;              // [T][k]
   float* weights;            // [T][k]
 };

@@ -283,7 +283,8 @@ int32_t fp8_add_rmsnorm_quant(const void* x, int64_t ldx, const void* residual,
   a.res = (const uint16_t*)residual; a.res_out = (uint16_t*)residual_out; a.ldr = ldr;
   a.w = (const uint16_t*)weight; a.y = (uint16_t*)y; a.xq = (uint8_t*)xq; a.xs = x_scale;
   a.xstat = stat ? act_scale : nullptr;
-  a.eps = eps; a.M = M; a.K = K; a.fmt = scale_fmt; a.group_k = group_k;
+  a.eps = eps; a.inv_k = 1.0 / (double)K; a.M = M; a.K = K; a.fmt = scale_fmt;
+  a.group_k = group_k;
   return hip_status(launch_add_rmsnorm_quant(a, (hipStream_t)stream));
 }
 

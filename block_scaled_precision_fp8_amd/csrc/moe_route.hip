@@ -12,6 +12,8 @@
 // One wave per token: lane i holds the experts i, i + 64, ...; each of the k
 // rounds takes the wave's largest (key, lowest id).  Bound by latency (one
 // round of loads, k wave reductions) until some thousands of tokens.
+#include <type_traits>
+
 #include "bsfp8_internal.h"
 
 namespace bsfp8 {
@@ -35,13 +37,60 @@ __device__ __forceinline__ double unordered64(u64 k) {
   return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
 }
 
+// Wave maxima on the vector ALU: exchanges inside rows of 16 lanes, then the
+// four rows' results (an exchange through LDS takes ten times as long).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp<kXor1>(v));
+  v = max(v, dpp<kXor2>(v));
+  v = max(v, dpp<kMirror8>(v));
+  v = max(v, dpp<kMirror16>(v));
+  return max(max(lane_u32(v, 0), lane_u32(v, 16)), max(lane_u32(v, 32), lane_u32(v, 48)));
+}
 __device__ __forceinline__ u64 wave_max(u64 v) {
+  const uint32_t hi = wave_max((uint32_t)(v >> 32));
+  return (u64)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, __uint_as_float(dpp<kXor1>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp<kXor2>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp<kMirror8>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp<kMirror16>(__float_as_uint(v))));
+  const uint32_t u = __float_as_uint(v);
+  return fmaxf(fmaxf(__uint_as_float(lane_u32(u, 0)), __uint_as_float(lane_u32(u, 16))),
+               fmaxf(__uint_as_float(lane_u32(u, 32)), __uint_as_float(lane_u32(u, 48))));
+}
+template <int CTRL>
+__device__ __forceinline__ u64 dpp64(u64 v) {
+  return (u64)dpp<CTRL>((uint32_t)(v >> 32)) << 32 | dpp<CTRL>((uint32_t)v);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += __longlong_as_double((long long)dpp64<kXor1>((u64)__double_as_longlong(v)));
+  v += __longlong_as_double((long long)dpp64<kXor2>((u64)__double_as_longlong(v)));
+  v += __longlong_as_double((long long)dpp64<kMirror8>((u64)__double_as_longlong(v)));
+  v += __longlong_as_double((long long)dpp64<kMirror16>((u64)__double_as_longlong(v)));
+  double s = 0.0;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const u64 t = __shfl_xor(v, o, 64);
-    v = t > v ? t : v;
+  for (int r = 0; r < 64; r += 16) {
+    const u64 u = (u64)__double_as_longlong(v);
+    s += __longlong_as_double((long long)((u64)lane_u32((uint32_t)(u >> 32), r) << 32 | lane_u32((uint32_t)u, r)));
   }
-  return v;
+  return s;
+}
+
+// The two largest of two such pairs.
+__device__ __forceinline__ void merge2(u64& a0, u64& a1, u64 b0, u64 b1) {
+  const u64 lo = a0 < b0 ? a0 : b0, hi = a0 < b0 ? b0 : a0;
+  const u64 m = a1 < b1 ? b1 : a1;
+  a0 = hi;
+  a1 = lo < m ? m : lo;
 }
 
 template <bool BF16, bool K64, int NE>
@@ -66,8 +115,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
     }
     top = fmaxf(top, l[i]);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if (a.score == 0) top = wave_max(top);
 
   // softmax denominators: needed for the scores as such, not where the
   // chosen ones are divided by their own sum
@@ -83,21 +131,21 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       if (l[i] > ninf) Z += K64 ? expo(l[i]) : l[i] == top ? 1.0 : (double)expf(l[i] - top);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) Z += __shfl_xor(Z, o, 64);
+    Z = wave_sum(Z);
   }
 
-  u64 key[NE];
+  typedef typename std::conditional<K64, u64, uint32_t>::type Key;
+  Key key[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    key[i] = kNever;
+    key[i] = 0;
     const int e = lane + 64 * i;
     if (l[i] > ninf) {
       if constexpr (K64) {
         const double v = score(l[i]) + (a.bias ? (double)a.bias[e] : 0.0);
         if (v > -(double)__builtin_inff()) key[i] = ordered64(v);
       } else {
-        key[i] = ((u64)ordered32(l[i]) << 32) | (uint32_t)~e;
+        key[i] = ordered32(l[i]);
       }
     }
   }
@@ -109,27 +157,31 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
         if (lane + 64 * i < E) gk[lane + 64 * i] = key[i];
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      const int gs = E / a.n_group;
+      // L lanes (a power of two) scan each group, lanes g L .. + L - 1 group g
+      const int gs = E / a.n_group, L = a.group_lanes;
+      const int g = lane / L;
+      u64 b0 = kNever, b1 = kNever;    // the group's two largest keys
+      if (g < a.n_group)
+        for (int j = lane & (L - 1); j < gs; j += L) merge2(b0, b1, gk[g * gs + j], kNever);
+      if (L > 1) merge2(b0, b1, dpp64<kXor1>(b0), dpp64<kXor1>(b1));
+      if (L > 2) merge2(b0, b1, dpp64<kXor2>(b0), dpp64<kXor2>(b1));
+      if (L > 4) merge2(b0, b1, dpp64<kMirror8>(b0), dpp64<kMirror8>(b1));
+      if (L > 8) merge2(b0, b1, dpp64<kMirror16>(b0), dpp64<kMirror16>(b1));
+      if (L > 16) merge2(b0, b1, __shfl_xor(b0, 16, 64), __shfl_xor(b1, 16, 64));
       u64 gscore = kNever;
-      if (lane < a.n_group) {
-        u64 b0 = kNever, b1 = kNever;   // the group's two largest keys
-        for (int j = 0; j < gs; ++j) {
-          const u64 v = gk[lane * gs + j];
-          if (v > b0) { b1 = b0; b0 = v; } else if (v > b1) { b1 = v; }
-        }
-        if (b0 != kNever)
-          gscore = ordered64(unordered64(b0) + (b1 != kNever ? unordered64(b1) : 0.0));
-      }
+      if (b0 != kNever)
+        gscore = ordered64(unordered64(b0) + (b1 != kNever ? unordered64(b1) : 0.0));
       int better = 0;
-      for (int g = 0; g < a.n_group; ++g) {
-        const u64 v = __shfl(gscore, g, 64);
-        better += (v > gscore || (v == gscore && g < lane)) ? 1 : 0;
+      for (int o = 0; o < a.n_group; ++o) {
+        const u64 v = (u64)lane_u32((uint32_t)(gscore >> 32), o * L) << 32 | lane_u32((uint32_t)gscore, o * L);
+        better += (v > gscore || (v == gscore && o < g)) ? 1 : 0;
       }
-      const u64 kept = __ballot(lane < a.n_group && better < a.topk_group);
+      const u64 kept = __ballot(g < a.n_group && better < a.topk_group);
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
-        if (e < E && !((kept >> (e / gs)) & 1)) key[i] = kNever;
+        // e / gs by its reciprocal: exact below e gs = 2^20
+        if (e < E && !((kept >> (((uint32_t)e * a.group_rcp >> 20) * L)) & 1)) key[i] = kNever;
       }
     }
   }
@@ -137,25 +189,22 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
   // k rounds; lane j keeps the j-th choice
   int mine = -1;
   for (int j = 0; j < a.k; ++j) {
-    u64 best = kNever;
-    int at = 0x7fffffff;
+    Key best = 0;
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (key[i] > best) { best = key[i]; at = lane + 64 * i; }
-    const u64 all = wave_max(best);
-    if (all == kNever) break;
-    int e;
-    if constexpr (K64) {
-      e = best == all ? at : 0x7fffffff;
+    for (int i = 0; i < NE; ++i) best = key[i] > best ? key[i] : best;
+    best = wave_max(best);
+    if (best == 0) break;
+    // the lowest of the experts with that key
+    int e = 0;
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) e = min(e, __shfl_xor(e, o, 64));
-    } else {
-      e = (int)~(uint32_t)all;
+    for (int i = NE - 1; i >= 0; --i) {
+      const u64 b = __ballot(key[i] == best);
+      if (b) e = 64 * i + __builtin_ctzll(b);
     }
     if (lane == j) mine = e;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-      if (lane + 64 * i == e) key[i] = kNever;
+      if (lane + 64 * i == e) key[i] = 0;
   }
   // the chosen experts' logits, from their lanes
   float lv = ninf;
@@ -166,9 +215,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
   }
   double w = mine >= 0 ? score(lv) : 0.0;
   if (a.renorm) {
-    double sum = w;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    const double sum = wave_sum(w);
     w = sum > 0.0 ? w / sum : 0.0;
   }
   if (lane < a.k) {
@@ -178,7 +225,11 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
 }
 
 template <bool BF16, bool K64>
-hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+hipError_t launch_route(RouteArgs a, hipStream_t s) {
+  a.group_lanes = 1;
+  while (a.group_lanes * 2 * a.n_group <= 64) a.group_lanes *= 2;
+  a.group_rcp = ((1u << 20) + a.E / a.n_group - 1) / (a.E / a.n_group);
+
   const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
   const size_t lds = K64 && a.n_group > 1 ? (size_t)kRouteWaves * a.E * 8 : 0;
 #define BSFP8_ROUTE(NE)                                                                       \

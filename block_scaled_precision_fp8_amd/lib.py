@@ -121,11 +121,20 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream():
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:                 # a torch without these entry points
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
     if stream is not None:
         return ctypes.c_void_p(stream)
-    import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current device's current stream, without the Stream object that
+    # torch.cuda.current_stream() makes (0.2 against 3 us of host time a call)
+    return ctypes.c_void_p(_raw_stream())
 
 
 def workspace_size(op, M, N, K, E=0):
