@@ -12,8 +12,6 @@
 // One wave per token: lane i holds the experts i, i + 64, ...; each of the k
 // rounds takes the wave's largest (key, lowest id).  Bound by latency (one
 // round of loads, k wave reductions) until some thousands of tokens.
-#include <type_traits>
-
 #include "bsfp8_internal.h"
 
 namespace bsfp8 {
@@ -54,10 +52,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = max(v, dpp<kMirror16>(v));
   return max(max(lane_u32(v, 0), lane_u32(v, 16)), max(lane_u32(v, 32), lane_u32(v, 48)));
 }
-__device__ __forceinline__ u64 wave_max(u64 v) {
-  const uint32_t hi = wave_max((uint32_t)(v >> 32));
-  return (u64)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-}
 __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, __uint_as_float(dpp<kXor1>(__float_as_uint(v))));
   v = fmaxf(v, __uint_as_float(dpp<kXor2>(__float_as_uint(v))));
@@ -93,60 +87,55 @@ __device__ __forceinline__ void merge2(u64& a0, u64& a1, u64 b0, u64 b1) {
   a1 = lo < m ? m : lo;
 }
 
-template <bool BF16, bool K64, int NE>
+// SOFT: softmax scores, else sigmoid.  Keys are held as two words; with K64
+// false the low one is not there.
+template <bool BF16, bool SOFT, bool K64, int NE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs a) {
-  extern __shared__ u64 gkeys[];       // K64 with groups: E keys per wave
+  extern __shared__ u64 gkeys[];       // with groups: E keys per wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
   if (t >= a.T) return;                // whole waves; no workgroup barrier below
   const int E = a.E;
   const float ninf = -__builtin_inff();
-  float l[NE];
+  float l[NE], bias[NE];
   float top = ninf;
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = ninf;
-    if (e < E) {
-      const int64_t at = t * a.ldl + e;
-      const float v = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)a.logits)[at] << 16)
-                           : ((const float*)a.logits)[at];
-      if (v > ninf) l[i] = v;          // NaN and -inf: never chosen
-    }
+    const int e = min(lane + 64 * i, E - 1);
+    const int64_t at = t * a.ldl + e;
+    const float v = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)a.logits)[at] << 16)
+                         : ((const float*)a.logits)[at];
+    if (K64) bias[i] = a.bias ? a.bias[e] : 0.0f;
+    l[i] = lane + 64 * i < E && v > ninf ? v : ninf;       // NaN and -inf: never chosen
     top = fmaxf(top, l[i]);
   }
-  if (a.score == 0) top = wave_max(top);
+  if (SOFT) top = wave_max(top);
 
+  // in 64 bits: scores that fp32 cannot hold still have a ratio.  At the top
+  // 1, +inf included; -inf gives 0
+  auto expo = [&](float v) -> double { return v == top ? 1.0 : exp((double)v - (double)top); };
   // softmax denominators: needed for the scores as such, not where the
   // chosen ones are divided by their own sum
   double Z = 1.0;
-  const bool soft = a.score == 0;
-  auto expo = [&](float v) -> double {   // e^(v - top); 1 at the top, +inf included
-    return v == top ? 1.0 : exp((double)v - (double)top);
-  };
-  // in 64 bits: scores that fp32 cannot hold still have a ratio
-  auto score = [&](float v) -> double { return soft ? expo(v) / Z : 1.0 / (1.0 + exp(-(double)v)); };
-  if (soft && (K64 || !a.renorm)) {
+  if (SOFT && (K64 || !a.renorm)) {
     Z = 0.0;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-      if (l[i] > ninf) Z += K64 ? expo(l[i]) : l[i] == top ? 1.0 : (double)expf(l[i] - top);
+      Z += l[i] == ninf ? 0.0 : K64 ? expo(l[i]) : l[i] == top ? 1.0 : (double)expf(l[i] - top);
     Z = wave_sum(Z);
   }
+  auto score = [&](float v) -> double { return SOFT ? expo(v) / Z : 1.0 / (1.0 + exp(-(double)v)); };
 
-  typedef typename std::conditional<K64, u64, uint32_t>::type Key;
-  Key key[NE];
+  uint32_t hi[NE], lo[K64 ? NE : 1];   // 0, 0: never chosen
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    key[i] = 0;
-    const int e = lane + 64 * i;
-    if (l[i] > ninf) {
-      if constexpr (K64) {
-        const double v = score(l[i]) + (a.bias ? (double)a.bias[e] : 0.0);
-        if (v > -(double)__builtin_inff()) key[i] = ordered64(v);
-      } else {
-        key[i] = ordered32(l[i]);
-      }
+    if constexpr (K64) {
+      const double v = score(l[i]) + (double)bias[i];
+      const u64 k = l[i] > ninf && v > -(double)__builtin_inff() ? ordered64(v) : kNever;
+      hi[i] = (uint32_t)(k >> 32);
+      lo[i] = (uint32_t)k;
+    } else {
+      hi[i] = l[i] > ninf ? ordered32(l[i]) : 0u;
     }
   }
   if constexpr (K64) {
@@ -154,7 +143,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
       u64* gk = gkeys + (int64_t)wave * E;
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (lane + 64 * i < E) gk[lane + 64 * i] = key[i];
+        if (lane + 64 * i < E) gk[lane + 64 * i] = (u64)hi[i] << 32 | lo[i];
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       // L lanes (a power of two) scan each group, lanes g L .. + L - 1 group g
@@ -179,9 +168,11 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
       const u64 kept = __ballot(g < a.n_group && better < a.topk_group);
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        const int e = lane + 64 * i;
         // e / gs by its reciprocal: exact below e gs = 2^20
-        if (e < E && !((kept >> (((uint32_t)e * a.group_rcp >> 20) * L)) & 1)) key[i] = kNever;
+        const uint32_t e = lane + 64 * i;
+        const bool in = kept >> ((e * a.group_rcp >> 20) * L & 63) & 1;
+        hi[i] = in ? hi[i] : 0u;
+        lo[i] = in ? lo[i] : 0u;
       }
     }
   }
@@ -189,22 +180,37 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
   // k rounds; lane j keeps the j-th choice
   int mine = -1;
   for (int j = 0; j < a.k; ++j) {
-    Key best = 0;
+    uint32_t best = hi[0];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) best = key[i] > best ? key[i] : best;
+    for (int i = 1; i < NE; ++i) best = max(best, hi[i]);
     best = wave_max(best);
     if (best == 0) break;
-    // the lowest of the experts with that key
+    // the experts with that high word; of several (rare) those with the
+    // largest low word; of these the lowest
+    u64 has[NE];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      has[i] = __ballot(hi[i] == best);
+      n += __popcll(has[i]);
+    }
+    if constexpr (K64) {
+      if (n > 1) {
+        uint32_t low = 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) low = max(low, hi[i] == best ? lo[i] : 0u);
+        low = wave_max(low);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) has[i] = __ballot(hi[i] == best && lo[i] == low);
+      }
+    }
     int e = 0;
 #pragma unroll
-    for (int i = NE - 1; i >= 0; --i) {
-      const u64 b = __ballot(key[i] == best);
-      if (b) e = 64 * i + __builtin_ctzll(b);
-    }
+    for (int i = NE - 1; i >= 0; --i)
+      if (has[i]) e = 64 * i + __builtin_ctzll(has[i]);
     if (lane == j) mine = e;
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (lane + 64 * i == e) key[i] = 0;
+    for (int i = 0; i < NE; ++i) hi[i] = lane + 64 * i == e ? 0u : hi[i];
   }
   // the chosen experts' logits, from their lanes
   float lv = ninf;
@@ -224,16 +230,15 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
   }
 }
 
-template <bool BF16, bool K64>
+template <bool BF16, bool SOFT, bool K64>
 hipError_t launch_route(RouteArgs a, hipStream_t s) {
   a.group_lanes = 1;
   while (a.group_lanes * 2 * a.n_group <= 64) a.group_lanes *= 2;
   a.group_rcp = ((1u << 20) + a.E / a.n_group - 1) / (a.E / a.n_group);
-
   const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
   const size_t lds = K64 && a.n_group > 1 ? (size_t)kRouteWaves * a.E * 8 : 0;
 #define BSFP8_ROUTE(NE)                                                                       \
-  hipLaunchKernelGGL((route_topk_kernel<BF16, K64, NE>), grid, block, lds, s, a)
+  hipLaunchKernelGGL((route_topk_kernel<BF16, SOFT, K64, NE>), grid, block, lds, s, a)
   if (a.E <= 64) BSFP8_ROUTE(1);
   else if (a.E <= 128) BSFP8_ROUTE(2);
   else if (a.E <= 256) BSFP8_ROUTE(4);
@@ -243,13 +248,18 @@ hipError_t launch_route(RouteArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool BF16, bool SOFT>
+hipError_t launch_route_key(const RouteArgs& a, hipStream_t s) {
+  if (a.bias || a.n_group > 1) return launch_route<BF16, SOFT, true>(a, s);
+  return launch_route<BF16, SOFT, false>(a, s);
+}
+
 }  // namespace detail
 using namespace detail;
 
 hipError_t launch_route_topk(const RouteArgs& a, hipStream_t s) {
-  const bool k64 = a.bias || a.n_group > 1;
-  if (a.bf16) return k64 ? launch_route<true, true>(a, s) : launch_route<true, false>(a, s);
-  return k64 ? launch_route<false, true>(a, s) : launch_route<false, false>(a, s);
+  if (a.bf16) return a.score == 0 ? launch_route_key<true, true>(a, s) : launch_route_key<true, false>(a, s);
+  return a.score == 0 ? launch_route_key<false, true>(a, s) : launch_route_key<false, false>(a, s);
 }
 
 }  // namespace bsfp8
