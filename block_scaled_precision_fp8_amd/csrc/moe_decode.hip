@@ -44,12 +44,14 @@ __device__ __forceinline__ int slot_of(int w) { return w & 0x7ff; }
 __device__ __forceinline__ int token_of(int w) { return w >> 11 & 0x7f; }
 __device__ __forceinline__ int nth_of(int w) { return w >> 18; }      // -1 for w = -1
 
-// The slots in expert order, left by the gate/up launch for the down launch.
+// The sorted slots and their segments, left by the gate/up launch for the
+// down launch (which loads all arrays before it knows the counts).
 struct MoePlan {
-  int32_t total;                       // slots with an expert here
-  int32_t pad[3];
-  int32_t expert[kMoeMaxSlots];        // [total]
+  int32_t total, nsegs, subtiles, pad;
+  uint16_t seg[kMoeMaxSlots + 8];      // first row of every segment, and total
+  int32_t expert[kMoeMaxSlots];
   int32_t slot[kMoeMaxSlots];          // slot words
+  float weight[kMoeMaxSlots];
 };
 
 // ---- operands ----------------------------------------------------------
@@ -244,23 +246,32 @@ struct SortedSlots {
   int eid[kMoeMaxSlots];
   int sl[kMoeMaxSlots];                // slot words
   uint16_t seg[kMoeMaxSlots + 1];      // first row of every segment
-  int nruns, nsegs, total;
+  int nsegs, total, rt;                // rt: subtiles of a segment
 };
 
-// by one wave, after eid: segments of `rows` (a power of two), or just the
-// number of runs (rows 0)
-__device__ __forceinline__ void find_segments(SortedSlots& p, int total, int lane, int rows) {
-  // a row starts a segment when its place in its run is a multiple of rows
-  int n = 0, runs = 0, start = 0;
+// Subtiles of 16 rows per segment, by the average run: a run of more rows
+// reads its weights again, a subtile costs registers and a shorter ring.
+__device__ __forceinline__ int subtiles(int total, int runs) {
+  return total <= 10 * runs ? 1 : total <= 20 * runs ? 2 : 4;
+}
+
+// By one wave, after eid.  MANY: a run can have more than 16 rows.
+template <bool MANY>
+__device__ __forceinline__ void find_segments(SortedSlots& p, int total, int lane) {
+  auto starts_run = [&](int i) { return i < total && (i == 0 || p.eid[i] != p.eid[i - 1]); };
+  int rt = 1;
+  if (MANY) {
+    int runs = 0;
+    for (int i0 = 0; i0 < total; i0 += 64) runs += __popcll(__ballot(starts_run(i0 + lane)));
+    rt = subtiles(total, runs);
+  }
+  // a row starts a segment when its place in its run is a multiple of 16 rt
+  int n = 0, start = 0;
   for (int i0 = 0; i0 < total; i0 += 64) {
     const int i = i0 + lane;
-    const bool run = i < total && (i == 0 || p.eid[i] != p.eid[i - 1]);
-    const unsigned long long rb = __ballot(run);
-    runs += __popcll(rb);
-    if (rows == 0) continue;
-    const unsigned long long b = rb & (~0ull >> (63 - lane));
+    const unsigned long long b = __ballot(starts_run(i)) & (~0ull >> (63 - lane));
     const int mine = b ? i0 + 63 - __clzll(b) : start;     // this row's run's start
-    const bool st = i < total && ((i - mine) & (rows - 1)) == 0;
+    const bool st = i < total && ((i - mine) & (16 * rt - 1)) == 0;
     const unsigned long long sb = __ballot(st);
     if (st) p.seg[n + __popcll(sb & ((1ull << lane) - 1))] = (uint16_t)i;
     n += __popcll(sb);
@@ -269,21 +280,37 @@ __device__ __forceinline__ void find_segments(SortedSlots& p, int total, int lan
   if (lane == 0) {
     p.seg[n] = (uint16_t)total;
     p.nsegs = n;
-    p.nruns = runs;
+    p.total = total;
+    p.rt = rt;
   }
 }
 
-// Subtiles of 16 rows per segment, by the average run: a run of more rows
-// reads its weights again, a subtile costs registers and a shorter ring.
-__device__ __forceinline__ int subtiles(int total, int runs) {
-  return total <= 10 * runs ? 1 : total <= 20 * runs ? 2 : 4;
-}
-
-// The sort, by the whole workgroup: a slot's place is the number of slots of
-// lower experts and of earlier slots of its own.  key: kMoeMaxSlots words.
+// The sort and the segments, by the whole workgroup: a slot's place is the
+// number of slots of lower experts and of earlier slots of its own.  key:
+// kMoeMaxSlots words.
+template <bool MANY>
 __device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32_t* ids, int S,
-                                           int k, int E) {
+                                           int k, int E, int lane, int wave) {
   constexpr int kSkip = 0x7fffffff;                        // behind all others
+  if (S <= 64) {
+    // one wave, in registers
+    if (wave == 0) {
+      int e = lane < S ? ids[lane] : -1;
+      if (e < 0 || e >= E) e = kSkip;
+      int at = 0;
+      for (int j = 0; j < S; ++j) {
+        const int o = __builtin_amdgcn_readlane(e, j);
+        at += o < e || (o == e && j < lane);
+      }
+      if (e != kSkip) {
+        p.eid[at] = e;
+        p.sl[at] = slot_word(lane, k);
+      }
+      find_segments<MANY>(p, __popcll(__ballot(e != kSkip)), lane);
+    }
+    __syncthreads();
+    return;
+  }
   const int S4 = (S + 3) & ~3;
   for (int i = threadIdx.x; i < S4; i += kMoeThreads) {
     const int e = i < S ? ids[i] : -1;
@@ -306,6 +333,8 @@ __device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32
     ++valid;
   }
   if (valid) atomicAdd(&p.total, valid);
+  __syncthreads();
+  if (wave == 0) find_segments<MANY>(p, __builtin_amdgcn_readfirstlane(p.total), lane);
   __syncthreads();
 }
 
@@ -546,38 +575,47 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
                            : kPart + kChunks];
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
-  sort_slots(p, (int*)part, a.ids, a.T * a.k, a.k, a.E);
-  const int total = uniform(p.total);
-  if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) plan->total = total;
-    for (int i = threadIdx.x; i < total; i += kMoeThreads) {
-      plan->expert[i] = p.eid[i];
-      plan->slot[i] = p.sl[i];
-    }
-  }
-  if (wave == 0) {
-    find_segments(p, total, lane, MANY ? 0 : 16);
-    if (MANY) find_segments(p, total, lane, 16 * subtiles(total, uniform(p.nruns)));
-  }
-  __syncthreads();
-  const int rt = MANY ? subtiles(total, uniform(p.nruns)) : 1;
+  sort_slots<MANY>(p, (int*)part, a.ids, a.T * a.k, a.k, a.E, lane, wave);
+  const int rt = MANY ? uniform(p.rt) : 1;
   if (rt == 1) gate_up<FMT, W4, RAGGED, 1>(a, h, p, part, lane, wave);
   if constexpr (MANY) {
     if (rt == 2) gate_up<FMT, W4, RAGGED, 2>(a, h, p, part, lane, wave);
     if (rt == 4) gate_up<FMT, W4, RAGGED, 4>(a, h, p, part, lane, wave);
   }
+  if (blockIdx.x == 0) {
+    const int total = uniform(p.total), nsegs = uniform(p.nsegs);
+    if (threadIdx.x == 0) {
+      plan->total = total;
+      plan->nsegs = nsegs;
+      plan->subtiles = rt;
+    }
+    for (int i = threadIdx.x; i <= nsegs; i += kMoeThreads) plan->seg[i] = p.seg[i];
+    for (int i = threadIdx.x; i < total; i += kMoeThreads) {
+      const int e = p.eid[i], w = p.sl[i];
+      // a token that names an expert twice has neighbouring rows in its run:
+      // numbered, so that they add to the token's sum one after the other
+      int nth = 0;
+      while (nth < i && p.eid[i - nth - 1] == e && token_of(p.sl[i - nth - 1]) == token_of(w)) ++nth;
+      plan->expert[i] = e;
+      plan->slot[i] = w | nth << 18;
+      plan->weight[i] = a.wt[slot_of(w)];
+    }
+  }
 }
 
 // ------------------------------------------------------------------------
 // QUANT: h comes as bf16 and is quantized here, all rows into LDS, by every
-// workgroup (launches with few rows); else as codes and scales.
+// workgroup (launches with few rows; skipped slots' rows, never written, are
+// not read back); else as codes and scales.
+constexpr int kAhead = 4;
+
 // NT: 16-row weight tiles that make up the workgroup's R output features (R a
 // multiple of 4, the last tile partly empty), so that H / R workgroups can
 // match the CUs.
 template <int FMT, bool W4, int RT, bool QUANT, int NT>
 __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const uint8_t* hq,
                                      const void* hs, const SortedSlots& p, const float* swt,
-                                     float* mine, uint8_t* xl, int total, int R, int lane,
+                                     float* mine, uint8_t* xl, const uint4* hv, int R, int lane,
                                      int wave) {
   constexpr int D = (QUANT ? 6 : RT == 1 ? 4 : RT == 2 ? 3 : 2) / (QUANT && NT == 2 ? 2 : 1) * (W4 && QUANT ? 2 : 1);
   constexpr int SB = FMT == 0 ? 4 : 1;
@@ -693,12 +731,13 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
   }
   if constexpr (QUANT) {
     // sixteen lanes hold a group, eight values each
-    const int C = KB * 16, all = total * C;      // 8-value chunks of the sorted rows
-    for (int q0 = threadIdx.x; q0 - (int)threadIdx.x < all; q0 += kMoeThreads) {
+    const int C = KB * 16, all = T * a.k * C;    // 8-value chunks of all slots' rows
+    for (int q0 = threadIdx.x, u = 0; q0 - (int)threadIdx.x < all; q0 += kMoeThreads, ++u) {
       const int i = q0 / C, c = q0 - i * C;
       const bool ok = q0 < all;
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (ok) v = *(const uint4*)(h + (int64_t)slot_of(p.sl[i]) * K + c * 8);
+      if (u < kAhead) v = u == 0 ? hv[0] : u == 1 ? hv[1] : u == 2 ? hv[2] : hv[3];
+      else if (ok) v = *(const uint4*)(h + (int64_t)q0 * 8);
       const Unpacked f = unpack8(v);
       float amax = amax8(f);
 #pragma unroll
@@ -721,7 +760,7 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
       const int r0 = p.seg[pseg], r1 = p.seg[pseg + 1];
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const int i = min(r0 + 16 * r + l16, r1 - 1);        // past the rows: not added
+        const int i = slot_of(p.sl[min(r0 + 16 * r + l16, r1 - 1)]);   // past the rows: not added
         px[r] = xl + i * stride;
         ps[r] = xs + i * KB;
       }
@@ -827,36 +866,39 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
   float* sums = (float*)lds;           // [waves][T][R]
   uint8_t* xl = lds + kMoeWaves * T * R * 4;
 
-  const int total = uniform(plan->total);
-  float* mine = sums + wave * T * R;
-  for (int i = lane * 4; i < T * R; i += 256) *(float4*)(mine + i) = make_float4(0, 0, 0, 0);
-  for (int i = threadIdx.x; i < total; i += kMoeThreads) {
-    p.eid[i] = plan->expert[i];
-    const int w = plan->slot[i];
-    p.sl[i] = w;
-    swt[i] = a.wt[slot_of(w)];
-  }
-  __syncthreads();
-  if (wave == 0) {
-    find_segments(p, total, lane, MANY ? 0 : 16);
-    if (MANY) find_segments(p, total, lane, 16 * subtiles(total, uniform(p.nruns)));
-  } else if (wave == 1) {
-    // a token that names an expert twice has neighbouring rows in its run:
-    // number them, so that they add to the token's sum one after the other
-    for (int i = lane; i < total; i += 64) {
-      int nth = 0;
-      while (nth < i && p.eid[i - nth - 1] == p.eid[i] &&
-             token_of(p.sl[i - nth - 1]) == token_of(p.sl[i]))
-        ++nth;
-      if (nth) atomicOr(&p.sl[i], nth << 18);
+  // everything that does not wait for the counts goes out at once
+  const int S = T * a.k;
+  uint4 hv[kAhead];                    // QUANT: this lane's first chunks of h
+  if constexpr (QUANT) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t q = threadIdx.x + u * kMoeThreads;
+      hv[u] = q < S * (a.I / 8) ? *(const uint4*)(h + q * 8) : make_uint4(0, 0, 0, 0);
     }
   }
+  const int nsegs = plan->nsegs, subs = plan->subtiles;
+  float* mine = sums + wave * T * R;
+  for (int i = lane * 4; i < T * R; i += 256) *(float4*)(mine + i) = make_float4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < S; i += kMoeThreads) {
+    const int e = plan->expert[i], w = plan->slot[i];
+    const float c = plan->weight[i];
+    const uint16_t g = plan->seg[i];
+    p.eid[i] = e;
+    p.sl[i] = w;
+    swt[i] = c;
+    p.seg[i] = g;
+  }
+  if (threadIdx.x == 0) {
+    p.seg[S] = plan->seg[S];
+    p.nsegs = nsegs;
+    p.rt = subs;
+  }
   __syncthreads();
-  const int rt = MANY ? subtiles(total, uniform(p.nruns)) : 1;
-  if (rt == 1) down<FMT, W4, 1, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, total, R, lane, wave);
+  const int rt = MANY ? uniform(p.rt) : 1;
+  if (rt == 1) down<FMT, W4, 1, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, hv, R, lane, wave);
   if constexpr (MANY) {
-    if (rt == 2) down<FMT, W4, 2, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, total, R, lane, wave);
-    if (rt == 4) down<FMT, W4, 4, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, total, R, lane, wave);
+    if (rt == 2) down<FMT, W4, 2, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, hv, R, lane, wave);
+    if (rt == 4) down<FMT, W4, 4, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, hv, R, lane, wave);
   }
   __syncthreads();
   const int Q = R / 4;
