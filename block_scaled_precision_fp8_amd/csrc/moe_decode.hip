@@ -346,14 +346,17 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
                                         v4f* part, int lane, int wave) {
   constexpr ScaleMode SM = RAGGED ? kScaleByte : RT == 4 ? kScaleDword : kScaleChunk;
   constexpr bool CHUNK = W4 && SM == kScaleChunk;
-  constexpr int D = W4 ? (RT == 1 ? 8 : RT == 2 ? 5 : 3) : (RT == 1 ? 5 : RT == 2 ? 4 : 2);
+  // an item: U K blocks, 128 bytes of a weight row (MXFP4: both halves of a
+  // cache line in one go)
+  constexpr int U = W4 && RT < 4 ? 2 : 1;
+  constexpr int D = W4 ? (RT == 1 ? 4 : RT == 2 ? 2 : 3) : (RT == 1 ? 5 : RT == 2 ? 4 : 2);
   constexpr int SB = FMT == 0 ? 4 : 1;
   const int l16 = lane & 15, g4 = lane >> 4;
   const int64_t K = a.H, I = a.I;
-  const int KB = (int)((K + 127) / 128), CT = (int)(I / 16);
+  const int KB = (int)((K + 127) / 128), KI = (KB + U - 1) / U, CT = (int)(I / 16);
   const int64_t tasks = (int64_t)uniform(p.nsegs) * CT;
   const int64_t t0 = tasks * blockIdx.x / gridDim.x, t1 = tasks * (blockIdx.x + 1) / gridDim.x;
-  const int64_t items = (t1 - t0) * KB;
+  const int64_t items = (t1 - t0) * KI;
   auto share = [&](int w) { return items * w / kMoeWaves; };
   const int64_t it0 = share(wave);
   const int cnt = (int)(share(wave + 1) - it0);
@@ -386,10 +389,10 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
     const __amdgpu_buffer_rsrc_t rows = make_rsrc(a.xq, a.T * K);
     const __amdgpu_buffer_rsrc_t rscales = make_rsrc(a.xs, (int64_t)a.T * KB * SB);
     // two cursors over the wave's items: loads, and products behind them
-    const int64_t task = t0 + it0 / KB;
+    const int64_t task = t0 + it0 / KI;
     int lseg = (int)(task / CT), lct = (int)(task - (int64_t)lseg * CT);
-    int lkb = (int)(it0 - it0 / KB * KB), left = cnt;
-    int pseg = lseg, pct = lct, pkb = lkb, begun = lkb;
+    int lki = (int)(it0 - it0 / KI * KI), left = cnt;
+    int pseg = lseg, pct = lct, pki = lki, begun = lki;
     const uint32_t xk = (lane & 7) * 16;
     uint32_t xo[2 * RT], so[RT];       // the segment's rows; no row: past the buffers
     int e = 0;
@@ -421,22 +424,29 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
       }
     };
     struct Item {
-      WFrag<W4> g, u;
-      XFrag x[RT];
-      uint32_t sx[RT], sg, su;
+      WFrag<W4> g[U], u[U];
+      XFrag x[U][RT];
+      uint32_t sx[U][RT], sg, su;
     } ring[D];
     auto next = [&](Item& f) {
       const bool in = left > 0;        // past the share: zeros, no traffic
-      const int kb = in ? lkb : KB;
-      f.g = wg.load(kb);
-      f.u = wu.load(kb);
-      const uint32_t k = (uint32_t)kb * 128, sk = in ? (uint32_t)kb * SB : 0x40000000u;
+      const int kb = in ? lki * U : KB;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        f.x[r].c[0] = ld_buf16(rows, k + xk < (uint32_t)K ? xo[2 * r] + k : kOOB);
-        f.x[r].c[1] = ld_buf16(rows, k + xk < (uint32_t)K ? xo[2 * r + 1] + k : kOOB);
-        if (FMT == 0) f.sx[r] = __builtin_amdgcn_raw_buffer_load_b32(rscales, so[r] + sk, 0, 0);
-        else f.sx[r] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rscales, so[r] + sk, 0, 0);
+      for (int q = 0; q < U; ++q) f.g[q] = wg.load(kb + q);
+#pragma unroll
+      for (int q = 0; q < U; ++q) f.u[q] = wu.load(kb + q);
+      const uint32_t sk = in ? (uint32_t)kb * SB : 0x40000000u;
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const uint32_t k = (uint32_t)(kb + q) * 128;
+        const uint32_t sq = kb + q < KB ? (uint32_t)(kb + q) * SB : 0x40000000u;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          f.x[q][r].c[0] = ld_buf16(rows, k + xk < (uint32_t)K ? xo[2 * r] + k : kOOB);
+          f.x[q][r].c[1] = ld_buf16(rows, k + xk < (uint32_t)K ? xo[2 * r + 1] + k : kOOB);
+          if (FMT == 0) f.sx[q][r] = __builtin_amdgcn_raw_buffer_load_b32(rscales, so[r] + sq, 0, 0);
+          else f.sx[q][r] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rscales, so[r] + sq, 0, 0);
+        }
       }
       if constexpr (!W4) {
         if (FMT == 0) {
@@ -447,8 +457,8 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
           f.su = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(su, sk, 0, 0);
         }
       }
-      if (--left > 0 && ++lkb == KB) {
-        lkb = 0;
+      if (--left > 0 && ++lki == KI) {
+        lki = 0;
         if (++lct == CT) {
           lct = 0;
           ++lseg;
@@ -459,13 +469,13 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
     };
     // scale chunks: loaded one ahead of the products
     ScaleChunk cg4, cu4;
-    int cseg = pseg, cct = pct, ckb = pkb & ~(kChunk - 1), cleft = cnt + (pkb - ckb);
+    int cseg = pseg, cct = pct, ckb = pki * U & ~(kChunk - 1), cleft = (cnt + pki) * U - ckb;
     auto next_chunk = [&]() {
       if (cleft <= 0) return;
       const int64_t row = (int64_t)uniform(p.eid[uniform(p.seg[cseg])]) * 2 * I + cct * 16;
       cg4.load(a.s13, row, 16, K, ckb, lane);
       cu4.load(a.s13, row + I, 16, K, ckb, lane);
-      cleft -= min(kChunk, KB - ckb);
+      cleft -= min(kChunk, KI * U - ckb);
       ckb += kChunk;
       if (ckb >= KB) {
         ckb = 0;
@@ -489,30 +499,34 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (i0 + d < cnt) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[r], lane);
           if (CHUNK && fresh) {
             cg4.store(chunks, lane);
             cu4.store(chunks + kChunkDwords, lane);
             next_chunk();
           }
-          const uint32_t* ch = chunks + l16 * kChunkRow + (pkb & (kChunk - 1));
-          const BFrag bg = wg.bf16(ring[d].g, l16, ch), bu = wu.bf16(ring[d].u, l16, ch + kChunkDwords);
           const float cg = W4 ? 1.f : scale_value<FMT>(ring[d].sg);
           const float cu = W4 ? 1.f : scale_value<FMT>(ring[d].su);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            if (r > 0 && prows <= 16 * r) break;
-            const BFrag bx = x_from_lds<W4>(xbuf + r * 2048, lane);
-            const float sx = scale_value<FMT>(spread16(ring[d].sx[r], l16));
-            ag[r] = moe_step(ag[r], bg, bx, sx * cg);
-            au[r] = moe_step(au[r], bu, bx, sx * cu);
+          for (int q = 0; q < U; ++q) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[q][r], lane);
+            const uint32_t* ch = chunks + l16 * kChunkRow + (pki * U & (kChunk - 1)) + q;
+            const BFrag bg = wg.bf16(ring[d].g[q], l16, ch);
+            const BFrag bu = wu.bf16(ring[d].u[q], l16, ch + kChunkDwords);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              if (r > 0 && prows <= 16 * r) break;
+              const BFrag bx = x_from_lds<W4>(xbuf + r * 2048, lane);
+              const float sx = scale_value<FMT>(spread16(ring[d].sx[q][r], l16));
+              ag[r] = moe_step(ag[r], bg, bx, sx * cg);
+              au[r] = moe_step(au[r], bu, bx, sx * cu);
+            }
           }
         }
         next(ring[d]);
         const bool last = i0 + d + 1 == cnt;
-        if (i0 + d < cnt && (++pkb == KB || last)) {         // the task's end, here
-          if (pkb == KB && begun == 0) {
+        if (i0 + d < cnt && (++pki == KI || last)) {         // the task's end, here
+          if (pki == KI && begun == 0) {
             finish(ag, au, pseg, pct);
           } else {
 #pragma unroll
@@ -524,7 +538,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
 #pragma unroll
           for (int r = 0; r < RT; ++r) ag[r] = au[r] = v4f{0.f, 0.f, 0.f, 0.f};
           if (!last) {
-            begun = pkb = 0;
+            begun = pki = 0;
             if (++pct == CT) {
               pct = 0;
               ++pseg;
@@ -532,11 +546,11 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
             }
           }
         }
-        fresh = (pkb & (kChunk - 1)) == 0;
+        fresh = (pki * U & (kChunk - 1)) == 0;
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    left = begun == 0 && pkb < KB;     // the last task: begun here, not ended
+    left = begun == 0 && pki < KI;     // the last task: begun here, not ended
     lseg = pseg;
     lct = pct;
     __syncthreads();
@@ -547,7 +561,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
         g[r] = piece(wave, 1, 2 * r);
         u[r] = piece(wave, 1, 2 * r + 1);
       }
-      const int64_t end = (share(wave + 1) / KB + 1) * KB;
+      const int64_t end = (share(wave + 1) / KI + 1) * KI;
       for (int w = wave + 1; w < kMoeWaves; ++w) {
         if (share(w) == share(w + 1)) continue;
 #pragma unroll
@@ -617,12 +631,13 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
                                      const void* hs, const SortedSlots& p, const float* swt,
                                      float* mine, uint8_t* xl, const uint4* hv, int R, int lane,
                                      int wave) {
-  constexpr int D = (QUANT ? 6 : RT == 1 ? 4 : RT == 2 ? 3 : 2) / (QUANT && NT == 2 ? 2 : 1) * (W4 && QUANT ? 2 : 1);
+  constexpr int U = W4 && (RT < 4 || QUANT) ? 2 : 1;   // K blocks of an item, as above
+  constexpr int D = QUANT ? (NT == 2 ? 3 : 6) : RT == 1 ? 4 : RT == 2 && !W4 ? 3 : 2;
   constexpr int SB = FMT == 0 ? 4 : 1;
   const int l16 = lane & 15, g4 = lane >> 4;
   const int T = a.T;
   const int64_t N = a.H, K = a.I, n0 = (int64_t)blockIdx.x * R;
-  const int KB = (int)(K / 128);
+  const int KB = (int)(K / 128), KI = (KB + U - 1) / U;
   constexpr ScaleMode SM = RT == 4 && !QUANT ? kScaleDword : kScaleChunk;
   constexpr bool CHUNK = W4 && SM == kScaleChunk;
   // scale chunks; QUANT: codes of the sorted rows, then their scales; else 2
@@ -633,15 +648,15 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
   float* xs = (float*)(xl + (QUANT ? (int64_t)T * a.k * stride : 0));
   uint8_t* xbuf = xl + wave * 2048 * RT;
 
-  const int64_t items = (int64_t)uniform(p.nsegs) * KB;
+  const int64_t items = (int64_t)uniform(p.nsegs) * KI;
   const int64_t it0 = items * wave / kMoeWaves;
   const int cnt = (int)(items * (wave + 1) / kMoeWaves - it0);
   const int NB = (int)((N + 127) / 128), nrows = (int)min((int64_t)R, N - n0);
   const __amdgpu_buffer_rsrc_t rows = make_rsrc(hq, (int64_t)T * a.k * K);
   const __amdgpu_buffer_rsrc_t rscales = make_rsrc(hs, (int64_t)T * a.k * KB * SB);
   // two cursors over the wave's items: loads, and products behind them
-  int lseg = (int)(it0 / KB), lkb = (int)(it0 - (int64_t)lseg * KB), left = cnt;
-  int pseg = lseg, pkb = lkb;
+  int lseg = (int)(it0 / KI), lki = (int)(it0 - (int64_t)lseg * KI), left = cnt;
+  int pseg = lseg, pki = lki;
   uint32_t xo[2 * RT], so[RT];         // the segment's rows; no row: past the buffers
   WTile<W4, SM> wt[NT];
   __amdgpu_buffer_rsrc_t sw;
@@ -674,49 +689,56 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
     }
   };
   struct Item {
-    WFrag<W4> w[NT];
-    XFrag x[QUANT ? 1 : RT];
-    uint32_t sx[RT], sw[NT];
+    WFrag<W4> w[NT][U];
+    XFrag x[QUANT ? 1 : U][QUANT ? 1 : RT];
+    uint32_t sx[U][RT], sw[NT];
   } ring[D];
   auto next = [&](Item& f) {
-    // past the share: nothing (2^30 is past every buffer of rows)
+    // past the share, or the row: nothing (2^30 is past every buffer of rows)
     const bool in = left > 0;
+    const int kb = in ? lki * U : KB;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) f.w[j] = wt[j].load(in ? lkb : KB);
-    const uint32_t sk = in ? (uint32_t)lkb * SB : 0x40000000u;
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < U; ++q) f.w[j][q] = wt[j].load(kb + q);
     if constexpr (!QUANT) {
-      const uint32_t k = in ? (uint32_t)lkb * 128 : 0x40000000u;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        f.x[r].c[0] = ld_buf16(rows, xo[2 * r] + k);
-        f.x[r].c[1] = ld_buf16(rows, xo[2 * r + 1] + k);
-        if (FMT == 0) f.sx[r] = __builtin_amdgcn_raw_buffer_load_b32(rscales, so[r] + sk, 0, 0);
-        else f.sx[r] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rscales, so[r] + sk, 0, 0);
+      for (int q = 0; q < U; ++q) {
+        const uint32_t k = kb + q < KB ? (uint32_t)(kb + q) * 128 : 0x40000000u;
+        const uint32_t sq = kb + q < KB ? (uint32_t)(kb + q) * SB : 0x40000000u;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          f.x[q][r].c[0] = ld_buf16(rows, xo[2 * r] + k);
+          f.x[q][r].c[1] = ld_buf16(rows, xo[2 * r + 1] + k);
+          if (FMT == 0) f.sx[q][r] = __builtin_amdgcn_raw_buffer_load_b32(rscales, so[r] + sq, 0, 0);
+          else f.sx[q][r] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rscales, so[r] + sq, 0, 0);
+        }
       }
     }
     if constexpr (!W4) {
+      const uint32_t sk = in ? (uint32_t)kb * SB : 0x40000000u;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (FMT == 0) f.sw[j] = __builtin_amdgcn_raw_buffer_load_b32(sw, swo[j] + sk, 0, 0);
         else f.sw[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sw, swo[j] + sk, 0, 0);
       }
     }
-    if (--left > 0 && ++lkb == KB) {
-      lkb = 0;
+    if (--left > 0 && ++lki == KI) {
+      lki = 0;
       ++lseg;
       aim();
     }
   };
   // scale chunks: loaded one ahead of the products
   ScaleChunk c4[NT];
-  int cseg = pseg, ckb = pkb & ~(kChunk - 1), cleft = cnt + (pkb - ckb);
+  int cseg = pseg, ckb = pki * U & ~(kChunk - 1), cleft = (cnt + pki) * U - ckb;
   auto next_chunk = [&]() {
     if (cleft <= 0) return;
     const int64_t row = (int64_t)uniform(p.eid[uniform(p.seg[cseg])]) * N + n0;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       c4[j].load(a.s2, row + 16 * j, max(0, min(16, nrows - 16 * j)), K, ckb, lane);
-    cleft -= min(kChunk, KB - ckb);
+    cleft -= min(kChunk, KI * U - ckb);
     ckb += kChunk;
     if (ckb >= KB) {
       ckb = 0;
@@ -777,43 +799,47 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (i0 + d < cnt) {
-        if constexpr (!QUANT) {
+          if (CHUNK && fresh) {
 #pragma unroll
-          for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[r], lane);
-        }
-        if (CHUNK && fresh) {
-#pragma unroll
-          for (int j = 0; j < NT; ++j) c4[j].store(chunks + j * kChunkDwords, lane);
-          next_chunk();
-        }
-        const uint32_t* ch = chunks + l16 * kChunkRow + (pkb & (kChunk - 1));
-        BFrag bw[NT];
-        float cw[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          bw[j] = wt[j].bf16(ring[d].w[j], l16, ch + j * kChunkDwords);
-          cw[j] = W4 ? 1.f : scale_value<FMT>(ring[d].sw[j]);
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          if (r > 0 && prows <= 16 * r) break;
-          BFrag bx;
-          float sx;
-          if constexpr (QUANT) {
-            bx = x_bf16(*(const uint4*)(px[r] + pkb * 128 + (W4 ? 32 * g4 : 16 * g4)),
-                        *(const uint4*)(px[r] + pkb * 128 + (W4 ? 32 * g4 + 16 : 64 + 16 * g4)));
-            sx = ps[r][pkb];
-          } else {
-            bx = x_from_lds<W4>(xbuf + r * 2048, lane);
-            sx = scale_value<FMT>(spread16(ring[d].sx[r], l16));
+            for (int j = 0; j < NT; ++j) c4[j].store(chunks + j * kChunkDwords, lane);
+            next_chunk();
           }
+          float cw[NT];
 #pragma unroll
-          for (int j = 0; j < NT; ++j) acc[r][j] = moe_step(acc[r][j], bw[j], bx, sx * cw[j]);
-        }
+          for (int j = 0; j < NT; ++j) cw[j] = W4 ? 1.f : scale_value<FMT>(ring[d].sw[j]);
+#pragma unroll
+          for (int q = 0; q < U; ++q) {
+            if constexpr (!QUANT) {
+#pragma unroll
+              for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[q][r], lane);
+            }
+            const uint32_t* ch = chunks + l16 * kChunkRow + (pki * U & (kChunk - 1)) + q;
+            BFrag bw[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) bw[j] = wt[j].bf16(ring[d].w[j][q], l16, ch + j * kChunkDwords);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              if (r > 0 && prows <= 16 * r) break;
+              BFrag bx;
+              float sx;
+              if constexpr (QUANT) {
+                const int kb = min(pki * U + q, KB - 1);     // past the row: times zeros
+                const uint8_t* x = px[r] + kb * 128;
+                bx = x_bf16(*(const uint4*)(x + (W4 ? 32 * g4 : 16 * g4)),
+                            *(const uint4*)(x + (W4 ? 32 * g4 + 16 : 64 + 16 * g4)));
+                sx = ps[r][kb];
+              } else {
+                bx = x_from_lds<W4>(xbuf + r * 2048, lane);
+                sx = scale_value<FMT>(spread16(ring[d].sx[q][r], l16));
+              }
+#pragma unroll
+              for (int j = 0; j < NT; ++j) acc[r][j] = moe_step(acc[r][j], bw[j], bx, sx * cw[j]);
+            }
+          }
         }
         next(ring[d]);
         const bool last = i0 + d + 1 == cnt;
-        if (i0 + d < cnt && (++pkb == KB || last)) {         // the segment's end, here
+        if (i0 + d < cnt && (++pki == KI || last)) {         // the segment's end, here
           const int r0 = p.seg[pseg], r1 = p.seg[pseg + 1];
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
@@ -839,13 +865,13 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
             for (int j = 0; j < NT; ++j) acc[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
           }
           if (!last) {
-            pkb = 0;
+            pki = 0;
             ++pseg;
             prows = uniform(p.seg[pseg + 1] - p.seg[pseg]);
             if (QUANT) aim_products();
           }
         }
-        fresh = (pkb & (kChunk - 1)) == 0;
+        fresh = (pki * U & (kChunk - 1)) == 0;
         __builtin_amdgcn_sched_barrier(0);
       }
     }

@@ -441,3 +441,15 @@ def test_norm_route_moe_chain(fmt):
     # and the whole chain as one float64 layer, up to steps of h in doubt
     ref = Y.moe_layer(rq, rs, rid, rw, *wts, fmt, False, Y.bf16_bits(h))
     assert rel_fro(F.bf16_decode(bf16_bits(out)), ref) <= 2e-2
+
+
+@pytest.mark.parametrize("w4", [False, True])
+@pytest.mark.parametrize("T,k,H,I,E", [(1, 2, 7168, 128, 4), (3, 1, 5136, 256, 2), (40, 2, 4736, 384, 3),
+                                       (3, 2, 256, 4480, 2), (40, 1, 4480, 4480, 2), (70, 2, 6144, 128, 2),
+                                       (128, 3, 4352, 128, 24)])
+def test_moe_wide(T, k, H, I, E, w4):
+    """Output rows dealt in uneven groups over 128-row scale blocks, more K
+    blocks than one chunk of MXFP4 scales, h quantized in both launches."""
+    if w4:
+        H = H // 32 * 32
+    case(T, k, H, I, E, T % 2, w4, add=True, seed=T)
