@@ -122,6 +122,10 @@ __device__ __forceinline__ uint32_t act_encode4_rcp(float a, float b, float c, f
   return e4m3x4(ldexpf(a, -e), ldexpf(b, -e), ldexpf(c, -e), ldexpf(d, -e));
 }
 
+__device__ __forceinline__ int64_t grid_row() {
+  return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
+
 // Buffer resource over [base, base + bytes): loads past the end return 0,
 // which handles ragged M, N and K edges without branches.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
@@ -251,6 +255,13 @@ __device__ __forceinline__ v4f mfma_step_w4(v4f acc, const v8i& a, const v8i& b,
 }  // namespace detail
 
 // ---------------------------------------------------------------- host
+
+// A grid of n workgroups that may exceed what one dimension's lanes can count
+// (2^32): rows of 2^20 workgroups; a kernel's number is grid_row().
+inline dim3 row_grid(int64_t n) {
+  const int64_t x = n < (1 << 20) ? n : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
 
 struct NormArgs {
   const uint16_t* x;

@@ -93,7 +93,7 @@ template <bool BF16, bool SOFT, bool K64, int NE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs a) {
   extern __shared__ u64 gkeys[];       // with groups: E keys per wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
+  const int64_t t = grid_row() * kRouteWaves + wave;
   if (t >= a.T) return;                // whole waves; no workgroup barrier below
   const int E = a.E;
   const float ninf = -__builtin_inff();
@@ -235,7 +235,7 @@ hipError_t launch_route(RouteArgs a, hipStream_t s) {
   a.group_lanes = 1;
   while (a.group_lanes * 2 * a.n_group <= 64) a.group_lanes *= 2;
   a.group_rcp = ((1u << 20) + a.E / a.n_group - 1) / (a.E / a.n_group);
-  const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
+  const dim3 grid = row_grid((a.T + kRouteWaves - 1) / kRouteWaves), block(64 * kRouteWaves);
   const size_t lds = K64 && a.n_group > 1 ? (size_t)kRouteWaves * a.E * 8 : 0;
 #define BSFP8_ROUTE(NE)                                                                       \
   hipLaunchKernelGGL((route_topk_kernel<BF16, SOFT, K64, NE>), grid, block, lds, s, a)

@@ -135,7 +135,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_quant_kernel(NormA
   constexpr int WPR = TPR / 64;                    // waves per row
   __shared__ double red[WPR > 1 ? WPR : 1];
   const int tr = threadIdx.x % TPR;
-  const int64_t m = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
+  const int64_t m = grid_row() * RPW + threadIdx.x / TPR;
   if (m >= a.M) return;                            // whole waves: RPW > 1 has one wave per row
   const int C = (int)(a.K / 8);
   const uint16_t* xr = a.x + m * a.ldx;
@@ -207,9 +207,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_quant_kernel(NormA
 
 template <int FMT, int MODE>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-#define BSFP8_NORM(TPR, NC)                                                                  \
-  hipLaunchKernelGGL((norm_quant_kernel<FMT, MODE, TPR, NC>),                                \
-                     dim3((unsigned)(TPR < 256 ? (a.M + 256 / TPR - 1) / (256 / TPR) : a.M)), \
+#define BSFP8_NORM(TPR, NC)                                                     \
+  hipLaunchKernelGGL((norm_quant_kernel<FMT, MODE, TPR, NC>),                   \
+                     row_grid(TPR < 256 ? (a.M + 256 / TPR - 1) / (256 / TPR) : a.M), \
                      dim3(TPR < 256 ? 256 : TPR), 0, s, a)
   // One chunk per lane where a workgroup has the lanes: the fewest registers
   // and the most rows in flight (8192 x 4096: 512 lanes 50 us, 256 lanes of two

@@ -118,7 +118,7 @@ def _check(fn, s):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _raw_stream():
@@ -131,10 +131,10 @@ def _raw_stream():
 
 def _stream(stream):
     if stream is not None:
-        return ctypes.c_void_p(stream)
+        return stream
     # the current device's current stream, without the Stream object that
     # torch.cuda.current_stream() makes (0.2 against 3 us of host time a call)
-    return ctypes.c_void_p(_raw_stream())
+    return _raw_stream()
 
 
 def workspace_size(op, M, N, K, E=0):

@@ -142,3 +142,26 @@ def test_route_streams_and_graph():
         rid, rw = Y.route_topk(h, k, None, True, True, 1.0, 8, 4)
         assert np.array_equal(ids.cpu().numpy(), rid)
         assert np.allclose(w.cpu().numpy(), rw, rtol=2 * 110 * 2.0 ** -24, atol=0)
+
+
+def test_route_more_tokens_than_one_grid_dimension():
+    import torch
+    from block_scaled_precision_fp8_amd import lib as L
+    T, E, k = (4 << 20) + 777, 4, 2
+    say(f"route T={T}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    l = torch.randn((T, E), generator=g, device="cuda")
+    ids = torch.full((T + 1, k), -77, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, k), -77.0, device="cuda")
+    L.moe_route_topk(l, ids[:T], w[:T])
+    torch.cuda.synchronize()
+    assert (ids[T] == -77).all() and (w[T] == -77.0).all()
+    best = torch.topk(l, k, dim=1)                # distinct fp32 draws: no ties to order
+    for lo in range(0, T, 1 << 20):
+        v = torch.gather(l[lo:lo + (1 << 20)], 1, ids[lo:min(lo + (1 << 20), T)].long())
+        assert torch.equal(v, best.values[lo:lo + (1 << 20)])
+    rows = [0, (4 << 20) - 1, 4 << 20, T - 1]
+    rid, rw = Y.route_topk(l[rows].cpu().numpy(), k)
+    assert np.array_equal(ids[rows].cpu().numpy(), rid)
+    assert np.allclose(w[rows].cpu().numpy(), rw, rtol=2 * 110 * 2.0 ** -24, atol=0)

@@ -200,3 +200,30 @@ def test_norm_feeds_block_gemm():
     L.fp8_block_gemm(to_dev(q), to_dev(s), to_dev(wq), to_dev(ws), y, scale_fmt=1)
     torch.cuda.synchronize()
     assert rel_fro(F.bf16_decode(bf16_bits(y)), G.block_gemm(q, s, wq, ws, fmt=1)) <= 2e-3
+
+
+def test_norm_more_rows_than_one_grid_dimension():
+    """More workgroups than the grid's first dimension: every row as in a
+    short call, and one past the last left alone."""
+    import torch
+    from block_scaled_precision_fp8_amd import lib as L
+    M, K = (4 << 20) + 1001, 16
+    say(f"norm M={M}")
+    x = synth.device_normal_bf16((M, K), 1.0, "single", "x")
+    w = synth.device_normal_bf16((K,), 1.0, "single", "w")
+
+    def call(rows):
+        n = rows.shape[0]
+        q = torch.full((n + 1, K), 0xA5, dtype=torch.uint8, device="cuda")
+        s = torch.full((n + 1, 1), 7.0, device="cuda")
+        L.fp8_add_rmsnorm_quant(rows, w, q[:n], s[:n])
+        torch.cuda.synchronize()
+        assert (q[n] == 0xA5).all() and s[n] == 7.0
+        return q[:n], s[:n]
+
+    q, s = call(x)
+    for lo, hi in ((0, 100), (M // 2, M // 2 + 100), ((4 << 20) - 50, (4 << 20) + 50), (M - 100, M)):
+        a, b = call(x[lo:hi])
+        assert torch.equal(a, q[lo:hi]) and torch.equal(b, s[lo:hi])
+    rq, rs = Y.quant_rows(Y.add_rmsnorm(bf16_bits(x[M - 100:]), bf16_bits(w), 1e-6)[1])
+    assert np.array_equal(u8(q[M - 100:]), rq) and np.array_equal(s[M - 100:].cpu().numpy(), rs)
