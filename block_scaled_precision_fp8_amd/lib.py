@@ -97,7 +97,10 @@ def load(path=None):
     # and kernels run on the runtime that owns torch's streams and memory.
     # Opened before torch, the library would load the system runtime and
     # torch a second one beside it.
-    import torch  # noqa: F401
+    import torch
+    global _device, _raw_stream
+    _device = getattr(torch._C, "_cuda_getDevice", _device)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
     lib = ctypes.CDLL(p)
     for name, (res, args) in _SIGS.items():
         fn = getattr(lib, name)
@@ -121,20 +124,20 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream():
+# Replaced by load() with the functions below them, which make no objects (a
+# call's stream: 0.2 against 3 us of host time).
+def _device():
     import torch
-    try:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    except AttributeError:                 # a torch without these entry points
-        return torch.cuda.current_stream().cuda_stream
+    return torch.cuda.current_device()
+
+
+def _raw_stream(device):
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _stream(stream):
-    if stream is not None:
-        return stream
-    # the current device's current stream, without the Stream object that
-    # torch.cuda.current_stream() makes (0.2 against 3 us of host time a call)
-    return _raw_stream()
+    return _raw_stream(_device()) if stream is None else stream
 
 
 def workspace_size(op, M, N, K, E=0):
@@ -146,6 +149,12 @@ def gemm_kernel(M, N, K):
     sp = ctypes.c_int32(0)
     kind = int(load().bsfp8_gemm_kernel(M, N, K, ctypes.byref(sp)))
     return kind, int(sp.value)
+
+
+def _on_current_device(t):
+    d = t.get_device()
+    if d >= 0 and d != _device():          # -1: not on a GPU
+        raise ValueError("tensors must be on the current device")
 
 
 def _workspace(op, M, N, K, E, ws, device):
@@ -292,12 +301,24 @@ def fp8_add_rmsnorm_quant(x, weight, xq, x_scale, residual=None, residual_out=No
     residual_out bf16 (M, K) with one row stride; y bf16 (M, K) out or None;
     xq uint8 (M, K) and x_scale (M, G) out, or both None; act_scale as for
     fp8_linear."""
-    M, K = x.shape
-    ldr = K if residual is None else residual.stride(0)
-    if residual is not None and residual_out is not None and residual_out.stride(0) != ldr and M > 1:
-        raise ValueError("residual and residual_out need the same row stride")
-    _check("fp8_add_rmsnorm_quant", load().fp8_add_rmsnorm_quant(
-        _ptr(x), x.stride(0), _ptr(residual), _ptr(residual_out), ldr, _ptr(weight), eps, M, K,
+    lib = load()
+    _on_current_device(x)
+    shape, (ldx, one), ldr = x.shape, x.stride(), 0
+    M, K = shape
+    if residual is not None and residual_out is not None:
+        if residual.shape != shape or residual_out.shape != shape:
+            raise ValueError("residual and residual_out need the shape of x")
+        ldr, inner = residual.stride()
+        one = one if inner == 1 else 0
+        if residual_out is not residual:
+            ldo, inner = residual_out.stride()
+            one = one if inner == 1 else 0
+            if ldo != ldr and M > 1:
+                raise ValueError("residual and residual_out need the same row stride")
+    if one != 1:
+        raise ValueError("rows must be contiguous")
+    _check("fp8_add_rmsnorm_quant", lib.fp8_add_rmsnorm_quant(
+        _ptr(x), ldx, _ptr(residual), _ptr(residual_out), ldr, _ptr(weight), eps, M, K,
         group_k, act_scheme, scale_fmt, _ptr(act_scale), _ptr(y), _ptr(xq), _ptr(x_scale),
         _stream(stream)))
 
@@ -306,21 +327,50 @@ def moe_route_topk(logits, ids, weights, bias=None, score=SCORE_SOFTMAX, renorm=
                    n_group=1, topk_group=1, stream=None):
     """logits: fp32 or bf16 (T, E) with row stride ldl; bias fp32 (E,) or
     None; ids int32 (T, k) out; weights fp32 (T, k) out."""
-    T, E = logits.shape
-    _check("moe_route_topk", load().moe_route_topk(
-        _ptr(logits), logits.stride(0), int(logits.element_size() == 2), _ptr(bias), T, E,
-        ids.shape[1], score, int(renorm), scale, n_group, topk_group, _ptr(ids), _ptr(weights),
+    import torch
+    lib = load()
+    _on_current_device(logits)
+    (T, E), (ldl, one), shape = logits.shape, logits.stride(), ids.shape
+    bf16 = logits.dtype is torch.bfloat16
+    if not (bf16 or logits.dtype is torch.float32) or ids.dtype is not torch.int32 or \
+            weights.dtype is not torch.float32:
+        raise ValueError("logits must be fp32 or bf16, ids int32 and weights fp32")
+    if one != 1 or not (ids.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("rows of logits, ids and weights must be contiguous")
+    if weights.shape != shape or shape[0] != T:
+        raise ValueError("ids and weights must be (T, k)")
+    _check("moe_route_topk", lib.moe_route_topk(
+        _ptr(logits), ldl, int(bf16), _ptr(bias), T, E,
+        shape[1], score, int(renorm), scale, n_group, topk_group, _ptr(ids), _ptr(weights),
         _stream(stream)))
 
 
 def _moe_decode(fn, xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, I, addend,
                 scale_fmt, workspace, stream):
+    import torch
+    lib = load()
+    _on_current_device(xq)
     T, H = xq.shape
     k = ids.shape[1]
-    ws, wsb = _workspace(OP_MOE_DECODE, T * k, H, I, 0, workspace, xq.device)
-    _check(fn, getattr(load(), fn)(
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise ValueError("ids must be int32 and weights fp32")
+    if not (xq.is_contiguous() and ids.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("xq, ids and weights must be contiguous")
+    E, per = w13.shape[0], 2 if fn == "fp8_fp4_moe_decode" else 1
+    if ids.shape != weights.shape or ids.shape[0] != T or y.shape != xq.shape or \
+            w13.shape != (E, 2 * I, H // per) or w2.shape != (E, H, I // per):
+        raise ValueError("shapes of tokens, ids, weights and experts do not agree")
+    if workspace is None and stream is not None:
+        # from the launch's stream: memory of the current one may still be in
+        # use there, and is given out again while the launch runs
+        st = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(st):
+            ws, wsb = _workspace(OP_MOE_DECODE, T * k, H, I, 0, None, xq.device)
+    else:
+        ws, wsb = _workspace(OP_MOE_DECODE, T * k, H, I, 0, workspace, xq.device)
+    _check(fn, getattr(lib, fn)(
         _ptr(xq), _ptr(x_scale), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(w13_scale), _ptr(w2),
-        _ptr(w2_scale), _ptr(addend), _ptr(y), T, k, H, I, w13.shape[0], scale_fmt, _ptr(ws), wsb,
+        _ptr(w2_scale), _ptr(addend), _ptr(y), T, k, H, I, E, scale_fmt, _ptr(ws), wsb,
         _stream(stream)))
 
 

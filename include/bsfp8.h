@@ -161,7 +161,9 @@ BSFP8_API int32_t fp8_quant_act(const void* x, int64_t M, int64_t K, int64_t ldx
  *                y is required and the quantization arguments are only
  *                checked).
  * Outputs must not overlap inputs or each other, except residual_out =
- * residual.  NaN and Inf are outside the contract, as for fp8_quant_act.
+ * residual.  NaN and Inf are outside the contract, as for fp8_quant_act, and
+ * so are rows in which x + residual, h * weight or y passes the range of its
+ * type.
  * Errors: EINVAL (null pointers, sizes, strides, eps, enums, misalignment);
  * ENOTSUP (group_k other than 128 or 32, or 32 with STATIC).
  */
@@ -391,7 +393,10 @@ BSFP8_API int32_t fp8_grouped_gemm_silu_mul_quant(const void* xq, const void* x_
  *                addend, or 0.
  *   T <= 128, k <= 16 (ENOTSUP beyond: sort the rows and use
  *   fp8_grouped_gemm); H % 16 == 0, I % 128 == 0, 1 <= E <= 1024.
- *   workspace    >= bsfp8_workspace_size(BSFP8_OP_MOE_DECODE, T * k, H, I, 0).
+ *   workspace    >= bsfp8_workspace_size(BSFP8_OP_MOE_DECODE, T * k, H, I, 0);
+ *                nothing in it is kept from one call to the next.  Calls that
+ *                may overlap need one each.
+ * y must not overlap an input other than addend, nor the workspace.
  * Errors: EINVAL (sizes, null pointers, enums, misalignment); ENOTSUP (T, k,
  * H or I > 2^22, T k I > 2^30); ENOSPC.
  */

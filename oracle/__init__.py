@@ -16,6 +16,8 @@ numpy with fp64 arithmetic wherever the pages do not fix a precision:
   accumulation of dequantized operands.
 * ``fp4``     -- NVFP4-style quantization (e2m1 codes, 16-element e4m3 group
   scales, fp32 tensor scale) and its GEMM.
+* ``layer``   -- residual addition + RMS norm + quantization, a router's
+  top-k choice, and a whole MoE layer from the tokens' expert ids.
 
 Page citations use the page titles:
   [FG-FP8]  "Transformers 中的细粒度 FP8 量化：配置、DeepGEMM 加速路径与 UE8M0

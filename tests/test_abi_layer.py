@@ -120,3 +120,64 @@ def test_norm_binding_refuses_unlike_strides():
     wide = torch.zeros(2, 48, dtype=torch.bfloat16)[:, :32]
     with pytest.raises(ValueError):
         L.fp8_add_rmsnorm_quant(x, x[0], None, None, residual=x, residual_out=wide, y=x, stream=0)
+
+
+def test_norm_binding_refuses_other_shapes_and_orders():
+    import torch
+    x = torch.zeros(32, 32, dtype=torch.bfloat16)
+    for kw in (dict(residual=x[:16], residual_out=x), dict(residual=x, residual_out=x[:, :16]),
+               dict(residual=x.t(), residual_out=x.t())):
+        with pytest.raises(ValueError):
+            L.fp8_add_rmsnorm_quant(x, x[0], None, None, y=x, stream=0, **kw)
+    with pytest.raises(ValueError):
+        L.fp8_add_rmsnorm_quant(x.t(), x[0], None, None, y=x, stream=0)
+
+
+def test_route_binding_refuses_other_types_and_orders():
+    import torch
+    l, ids, w = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for bad in ((l.half(), ids, w), (l.double(), ids, w), (l, ids.long(), w), (l, ids, w.double()),
+                (l.t().contiguous().t(), ids, w), (l, ids.t().contiguous().t(), w),
+                (l, ids, w.t().contiguous().t()), (l, ids[:3], w[:3]), (l, ids, w[:, :1])):
+        with pytest.raises(ValueError):
+            L.moe_route_topk(*bad, stream=0)
+
+
+@pytest.mark.parametrize("w4", [False, True])
+def test_moe_binding_refuses_other_types_and_shapes(w4):
+    import torch
+    T, k, H, I, E, per = 4, 2, 256, 128, 3, 2 if w4 else 1
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    good = dict(xq=u8(T, H), x_scale=torch.ones(T, 2), ids=torch.zeros(T, k, dtype=torch.int32),
+                weights=torch.zeros(T, k), w13=u8(E, 2 * I, H // per), w13_scale=torch.ones(E, 2, 2),
+                w2=u8(E, H, I // per), w2_scale=torch.ones(E, 2, 1),
+                y=torch.zeros(T, H, dtype=torch.bfloat16), workspace=u8(16), stream=0)
+    fn = L.fp8_fp4_moe_decode if w4 else L.fp8_moe_decode
+    with pytest.raises(L.BsFp8Error):              # past the binding: a short workspace
+        fn(**good)
+    for kw in (dict(ids=good["ids"].long()), dict(weights=good["weights"].double()),
+               dict(ids=good["ids"][:2]), dict(weights=good["weights"][:, :1]),
+               dict(ids=good["ids"].t().contiguous().t()), dict(xq=good["xq"].t().contiguous().t()),
+               dict(w13=good["w13"][:2]), dict(w13=good["w13"][:, :I]), dict(w2=good["w2"][:, :128]),
+               dict(w13=u8(E, 2 * I, H // per // 2)), dict(y=good["y"][:2])):
+        with pytest.raises(ValueError):
+            fn(**dict(good, **kw))
+
+
+def test_bindings_refuse_another_device(monkeypatch):
+    """A tensor on GPU 1 while GPU 0 is the current one (stand-ins: no GPU)."""
+    import torch
+
+    class OnGpu1(torch.Tensor):
+        def get_device(self):
+            return 1
+    L.load()
+    monkeypatch.setattr(L, "_device", lambda: 0)
+    t = torch.zeros(4, 256).as_subclass(OnGpu1)
+    ids, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    with pytest.raises(ValueError, match="current device"):
+        L.moe_route_topk(t, ids, w, stream=0)
+    with pytest.raises(ValueError, match="current device"):
+        L.fp8_add_rmsnorm_quant(t, t, None, None, y=t, stream=0)
+    with pytest.raises(ValueError, match="current device"):
+        L.fp8_moe_decode(t, t, ids, w, t, t, torch.zeros(1, 1, 1), t, t, stream=0)

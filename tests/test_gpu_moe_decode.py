@@ -453,3 +453,31 @@ def test_moe_wide(T, k, H, I, E, w4):
     if w4:
         H = H // 32 * 32
     case(T, k, H, I, E, T % 2, w4, add=True, seed=T)
+
+
+def test_moe_own_workspace_on_a_given_stream():
+    """No workspace passed and a stream that is not the current one: the
+    workspace is that stream's, so that memory which the current stream still
+    works on is not written, and later tensors do not get it meanwhile."""
+    import torch
+    from block_scaled_precision_fp8_amd import lib as L
+    T, k, H, I, E = 24, 4, 512, 256, 8
+    dw = [to_dev(a) for a in experts(E, H, I, 0, False)]
+    xq, xs = (to_dev(a) for a in acts(T, H, 0, 3))
+    ids, w = (to_dev(a) for a in routing(T, k, E, 3, 0.1))
+    want = layer(0, False, xq, xs, ids, w, dw)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    need = L.workspace_size(L.OP_MOE_DECODE, T * k, H, I)
+    for _ in range(5):
+        y = torch.zeros_like(want)
+        busy = torch.empty(need, dtype=torch.uint8, device="cuda")
+        st.wait_stream(torch.cuda.current_stream())
+        for i in range(20):
+            busy.fill_(i)
+        del busy                               # the current stream still fills it
+        L.fp8_moe_decode(xq, xs, ids, w, *dw, y, stream=st.cuda_stream)
+        later = [torch.full((need,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+        assert all(bool((t == 0x7F).all()) for t in later)
