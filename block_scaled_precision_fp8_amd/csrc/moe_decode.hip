@@ -54,6 +54,11 @@ struct MoePlan {
   float weight[kMoeMaxSlots];
 };
 
+// A value that all lanes hold, into a scalar register.  64-bit divisions and
+// comparisons leave theirs in vector registers, and a buffer that depends on
+// one gets a loop over the lanes around each of its loads.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // ---- operands ----------------------------------------------------------
 // The products run on the bf16 MFMA: every E4M3 and E2M1 value is a bf16
 // value, and the instruction keeps 24 bits below a group's largest product.
@@ -84,12 +89,12 @@ __device__ __forceinline__ bf8 cvt_e2m1x8(uint32_t a, float s) {
   return bf8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// A stored scale, as loaded: the fp32 value, or the E8M0 byte.
-template <int FMT>
-__device__ __forceinline__ uint32_t ld_scale(__amdgpu_buffer_rsrc_t r, uint32_t i, bool ok) {
-  if (FMT == 0) return __builtin_amdgcn_raw_buffer_load_b32(r, ok ? i * 4 : kOOB, 0, 0);
-  return (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, ok ? i : kOOB, 0, 0);
+// The buffers here have less than 2^31 bytes: no clamp.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, uniform((int)bytes), 0x00020000);
 }
+
+// A stored scale, as loaded: the fp32 value, or the E8M0 byte.
 template <int FMT>
 __device__ __forceinline__ float scale_value(uint32_t s) {
   return FMT == 0 ? __uint_as_float(s) : e8m0_f32(s);
@@ -135,10 +140,10 @@ struct WTile {
   }
   // n <= 16 rows from row0 on; the others give zeros
   __device__ __forceinline__ void aim(const uint8_t* w, const void* sc, int64_t row0, int n) {
-    const int64_t KW = W4 ? K / 2 : K;
-    codes = make_rsrc(w + row0 * KW, n * KW);
+    const uint32_t KW = W4 ? K / 2 : K;
+    codes = row_rsrc(w + row0 * KW, n * KW);
     if (W4 && SM != kScaleChunk)
-      scales = make_rsrc((const uint8_t*)sc + row0 * (K / 32), (int64_t)n * (K / 32));
+      scales = row_rsrc((const uint8_t*)sc + row0 * (K / 32), n * (K / 32));
   }
   __device__ __forceinline__ WFrag<W4> load(int kb) const {
     WFrag<W4> f;
@@ -187,11 +192,13 @@ struct ScaleChunk {
   __device__ __forceinline__ void load(const void* sc, int64_t row0, int n, int64_t K, int kb0,
                                        int lane) {
     const uint32_t row = (uint32_t)(K / 32), kb = kb0 + (lane & 31);
-    const __amdgpu_buffer_rsrc_t r = make_rsrc((const uint8_t*)sc + row0 * row, (int64_t)n * row);
+    const __amdgpu_buffer_rsrc_t r = row_rsrc((const uint8_t*)sc + row0 * row, n * row);
+    // one choice for all eight: a choice at each load becomes a branch around
+    // it, and every such branch waits for all loads in flight
+    const uint32_t o = (lane >> 5) * row + (kb * 4 < row ? kb * 4 : kOOB);
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      v[q] = __builtin_amdgcn_raw_buffer_load_b32(
-          r, kb * 4 < row ? (2 * q + (lane >> 5)) * row + kb * 4 : kOOB, 0, 0);
+      v[q] = __builtin_amdgcn_raw_buffer_load_b32(r, o + 2 * q * row, 0, 0);
   }
   __device__ __forceinline__ void store(uint32_t* lds, int lane) const {
 #pragma unroll
@@ -338,8 +345,6 @@ __device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32
   __syncthreads();
 }
 
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 // ------------------------------------------------------------------------
 template <int FMT, bool W4, bool RAGGED, int RT>
 __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const SortedSlots& p,
@@ -359,7 +364,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
   const int64_t items = (t1 - t0) * KI;
   auto share = [&](int w) { return items * w / kMoeWaves; };
   const int64_t it0 = share(wave);
-  const int cnt = (int)(share(wave + 1) - it0);
+  const int cnt = uniform((int)(share(wave + 1) - it0));
 
   // partial products of tasks that begin or end inside a wave's share: 0
   // begun by an earlier wave, 1 begun here and left to the next
@@ -386,12 +391,12 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
   if (cnt > 0) {
     uint8_t* xbuf = (uint8_t*)&part[(wave * 2 + 1) * 2 * RT * 64];   // free until the last task
     uint32_t* chunks = (uint32_t*)&part[kMoeWaves * 4 * RT * 64] + wave * 2 * kChunkDwords;
-    const __amdgpu_buffer_rsrc_t rows = make_rsrc(a.xq, a.T * K);
-    const __amdgpu_buffer_rsrc_t rscales = make_rsrc(a.xs, (int64_t)a.T * KB * SB);
+    const __amdgpu_buffer_rsrc_t rows = row_rsrc(a.xq, (uint32_t)(a.T * K));
+    const __amdgpu_buffer_rsrc_t rscales = row_rsrc(a.xs, (uint32_t)(a.T * KB * SB));
     // two cursors over the wave's items: loads, and products behind them
     const int64_t task = t0 + it0 / KI;
-    int lseg = (int)(task / CT), lct = (int)(task - (int64_t)lseg * CT);
-    int lki = (int)(it0 - it0 / KI * KI), left = cnt;
+    int lseg = uniform((int)(task / CT)), lct = uniform((int)(task - (int64_t)lseg * CT));
+    int lki = uniform((int)(it0 - it0 / KI * KI)), left = cnt;
     int pseg = lseg, pct = lct, pki = lki, begun = lki;
     const uint32_t xk = (lane & 7) * 16;
     uint32_t xo[2 * RT], so[RT];       // the segment's rows; no row: past the buffers
@@ -419,8 +424,8 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
       wg.aim(a.w13, a.s13, row, 16);
       wu.aim(a.w13, a.s13, row + I, 16);
       if (!W4) {
-        sg = make_rsrc((const uint8_t*)a.s13 + row / 128 * KB * SB, (int64_t)KB * SB);
-        su = make_rsrc((const uint8_t*)a.s13 + (row + I) / 128 * KB * SB, (int64_t)KB * SB);
+        sg = row_rsrc((const uint8_t*)a.s13 + row / 128 * KB * SB, KB * SB);
+        su = row_rsrc((const uint8_t*)a.s13 + (row + I) / 128 * KB * SB, KB * SB);
       }
     };
     struct Item {
@@ -650,12 +655,12 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
 
   const int64_t items = (int64_t)uniform(p.nsegs) * KI;
   const int64_t it0 = items * wave / kMoeWaves;
-  const int cnt = (int)(items * (wave + 1) / kMoeWaves - it0);
-  const int NB = (int)((N + 127) / 128), nrows = (int)min((int64_t)R, N - n0);
-  const __amdgpu_buffer_rsrc_t rows = make_rsrc(hq, (int64_t)T * a.k * K);
-  const __amdgpu_buffer_rsrc_t rscales = make_rsrc(hs, (int64_t)T * a.k * KB * SB);
+  const int cnt = uniform((int)(items * (wave + 1) / kMoeWaves - it0));
+  const int NB = (int)((N + 127) / 128), nrows = uniform((int)min((int64_t)R, N - n0));
+  const __amdgpu_buffer_rsrc_t rows = row_rsrc(hq, (uint32_t)(T * a.k * K));
+  const __amdgpu_buffer_rsrc_t rscales = row_rsrc(hs, (uint32_t)(T * a.k * KB * SB));
   // two cursors over the wave's items: loads, and products behind them
-  int lseg = (int)(it0 / KI), lki = (int)(it0 - (int64_t)lseg * KI), left = cnt;
+  int lseg = uniform((int)(it0 / KI)), lki = uniform((int)(it0 - (int64_t)lseg * KI)), left = cnt;
   int pseg = lseg, pki = lki;
   uint32_t xo[2 * RT], so[RT];         // the segment's rows; no row: past the buffers
   WTile<W4, SM> wt[NT];
@@ -673,8 +678,8 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
     for (int j = 0; j < NT; ++j)
       wt[j].aim(a.w2, a.s2, (int64_t)e * N + n0 + 16 * j, max(0, min(16, nrows - 16 * j)));
     if (!W4)
-      sw = make_rsrc((const uint8_t*)a.s2 + ((int64_t)e * NB + n0 / 128) * KB * SB,
-                     min((int64_t)2, NB - n0 / 128) * KB * SB);
+      sw = row_rsrc((const uint8_t*)a.s2 + ((int64_t)e * NB + n0 / 128) * KB * SB,
+                    min(2, NB - (int)(n0 / 128)) * KB * SB);
     if (!QUANT) {
 #pragma unroll
       for (int r = 0; r < 2 * RT; ++r) {
