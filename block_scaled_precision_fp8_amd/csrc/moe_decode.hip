@@ -14,8 +14,8 @@
 //                       sorted by expert for the next launch.
 //   quant_act_kernel    h to codes and scales, where the down launch does not
 //                       do that itself
-//   moe_down_kernel     one workgroup per 16 output features; its tasks are
-//                       the segments.  Each wave adds its weighted products
+//   moe_down_kernel     one workgroup per R (8 to 32) output features; its tasks
+//                       are the segments.  Each wave adds its weighted products
 //                       to its own fp32 sums per token in LDS, which are
 //                       joined in a fixed order.
 //
@@ -23,7 +23,17 @@
 // block) pairs and stream the weights through a ring of registers across
 // tasks, with no barrier until the end.  No atomics: the same bits on every
 // run.
-#include <algorithm>
+//
+// Measured (gate/up + down, TB/s of the weights read): 1 token x 8 of 256 FP8
+// experts (7168, 2048) 47.2 + 25.1 us (5.0, 4.7), 16 tokens 536 + 256 us (5.6,
+// 5.9); 64 tokens on 32 of them 171 + 75 us (5.5, 6.3); 33 x 2 of 8 MXFP4
+// experts (4096, 14336) 116 + 70 us (4.3, 3.6); 5 x 6 of 64 (2064, 1408) 38.6 +
+// 28.8 us.  A plain read of 235 MB runs at 5.6 to 5.9.  The MXFP4 stream has
+// half the bytes for the same conversions and exchanges, and its ring drains
+// in part wherever a scale chunk is taken up.  Tried without gain: deeper and
+// shallower rings, 16 waves per workgroup, the waves of a workgroup kept in
+// step by barriers, non-temporal weight loads (10% slower), a second LDS buffer
+// for the tokens' rows, encoding h under the first weights.
 #include <type_traits>
 
 #include "bsfp8.h"
@@ -107,7 +117,7 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 template <bool W4>
 struct WFrag {
   uint4 c[W4 ? 1 : 2];
-  uint32_t s[W4 ? 1 : 0];              // not with ScaleChunk
+  uint32_t s[W4 ? 1 : 0];              // with BYTES, below
 };
 // A value per row of a 16-row operand: loaded by the lanes of g4 = 0 only (a
 // load costs its lanes' addresses, not its bytes), spread to all four groups.
@@ -115,18 +125,17 @@ __device__ __forceinline__ uint32_t spread16(uint32_t v, int l16) {
   return (uint32_t)__builtin_amdgcn_ds_bpermute(l16 * 4, (int)v);
 }
 
-// How MXFP4 scale bytes reach a weight lane: a byte per lane and block (rows
-// of scales that do not begin at a dword), a dword per row and block, or
-// through LDS, 32 blocks of 16 rows at a time (ScaleChunk).  A row's scales
-// for 32 blocks share one cache line, which has left the L1 before the next
-// block: the first two fetch it again for every block, as many bytes as four
-// times the weights.
-enum ScaleMode { kScaleByte, kScaleDword, kScaleChunk };
-
-// Up to 16 rows of one expert's weight.  In a row's last, partial K block a
+// Up to 16 rows of one expert's weight.  MXFP4 scales reach a weight lane
+// through LDS, 32 blocks of 16 rows at a time (ScaleChunk), or (BYTES: rows of
+// scales that do not begin at a dword) as a byte per lane and block.  A row's
+// scales for 32 blocks share one cache line, which has left the L1 before the
+// next block: loaded block by block it is fetched again for every one, as
+// many bytes as four times the weights.
+//
+// In a row's last, partial K block a
 // lane reads on into the next row: finite values, which meet zeros of the
 // tokens' rows.  Blocks from KB on give zeros and no traffic.
-template <bool W4, ScaleMode SM>
+template <bool W4, bool BYTES>
 struct WTile {
   __amdgpu_buffer_rsrc_t codes, scales;
   uint32_t lo, slo, K;
@@ -136,13 +145,13 @@ struct WTile {
     KB = (int)((K_ + 127) / 128);
     g4 = lane >> 4;
     lo = (uint32_t)((lane & 15) * (W4 ? K_ / 2 : K_)) + g4 * 16;
-    slo = (uint32_t)((lane & 15) * (K_ / 32)) + (SM == kScaleByte ? g4 : g4 == 0 ? 0 : kOOB);
+    slo = (uint32_t)((lane & 15) * (K_ / 32)) + g4;
   }
   // n <= 16 rows from row0 on; the others give zeros
   __device__ __forceinline__ void aim(const uint8_t* w, const void* sc, int64_t row0, int n) {
     const uint32_t KW = W4 ? K / 2 : K;
     codes = row_rsrc(w + row0 * KW, n * KW);
-    if (W4 && SM != kScaleChunk)
+    if (W4 && BYTES)
       scales = row_rsrc((const uint8_t*)sc + row0 * (K / 32), n * (K / 32));
   }
   __device__ __forceinline__ WFrag<W4> load(int kb) const {
@@ -150,12 +159,10 @@ struct WTile {
     const uint32_t o = lo + (kb < KB ? (uint32_t)kb * (W4 ? 64 : 128) : kOOB);
     f.c[0] = ld_buf16(codes, o);
     if constexpr (W4) {
-      if constexpr (SM == kScaleByte) {
+      if constexpr (BYTES) {
         // the group itself may lie past the row: its scale is another row's
         const bool in = (uint32_t)kb * 128 + g4 * 32 < K;
         f.s[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, in ? slo + (uint32_t)kb * 4 : kOOB, 0, 0);
-      } else if constexpr (SM == kScaleDword) {
-        f.s[0] = __builtin_amdgcn_raw_buffer_load_b32(scales, slo + (kb < KB ? (uint32_t)kb * 4 : 0x40000000u), 0, 0);
       }
     } else {
       f.c[1] = ld_buf16(codes, o + 64);
@@ -164,13 +171,10 @@ struct WTile {
   }
   // the codes as bf16, with MXFP4 times their group's scale; chunk: the
   // block's column of this row's dwords in LDS
-  __device__ __forceinline__ BFrag bf16(const WFrag<W4>& w, int l16, const uint32_t* chunk) const {
+  __device__ __forceinline__ BFrag bf16(const WFrag<W4>& w, const uint32_t* chunk) const {
     BFrag f;
     if constexpr (W4) {
-      uint32_t b;
-      if (SM == kScaleByte) b = w.s[0];
-      else if (SM == kScaleDword) b = spread16(w.s[0], l16) >> (8 * g4) & 0xff;
-      else b = *chunk >> (8 * g4) & 0xff;
+      const uint32_t b = BYTES ? w.s[0] : *chunk >> (8 * g4) & 0xff;
       const float sc = __uint_as_float(b << 23);     // the conversion reads the exponent field
       f.v[0] = cvt_e2m1x8(w.c[0].x, sc); f.v[1] = cvt_e2m1x8(w.c[0].y, sc);
       f.v[2] = cvt_e2m1x8(w.c[0].z, sc); f.v[3] = cvt_e2m1x8(w.c[0].w, sc);
@@ -258,19 +262,26 @@ struct SortedSlots {
 
 // Subtiles of 16 rows per segment, by the average run: a run of more rows
 // reads its weights again, a subtile costs registers and a shorter ring.
+// Measured, gate/up + down us with 1 / 2 / 4: FP8, runs of 8 (7168, 2048, 64
+// experts) 390 + 169 / 392 + 177 / 456 + 225, of 16 (4096, 14336, 8 experts)
+// 291 + 160 / 219 + 140 / 239 + 152, of 32 469 + 270 / 344 + 217 / 272 + 192.
+// MXFP4, where 4 leave no room for two blocks an item: runs of 32 280 + 168 /
+// 228 + 147 / 243 + 173, of 64 - / 370 + 245 / 393 + 266, of 128 - / 516 + 383
+// / 519 + 393.
+template <bool W4>
 __device__ __forceinline__ int subtiles(int total, int runs) {
-  return total <= 10 * runs ? 1 : total <= 20 * runs ? 2 : 4;
+  return total <= 10 * runs ? 1 : W4 || total <= 20 * runs ? 2 : 4;
 }
 
 // By one wave, after eid.  MANY: a run can have more than 16 rows.
-template <bool MANY>
+template <bool W4, bool MANY>
 __device__ __forceinline__ void find_segments(SortedSlots& p, int total, int lane) {
   auto starts_run = [&](int i) { return i < total && (i == 0 || p.eid[i] != p.eid[i - 1]); };
   int rt = 1;
   if (MANY) {
     int runs = 0;
     for (int i0 = 0; i0 < total; i0 += 64) runs += __popcll(__ballot(starts_run(i0 + lane)));
-    rt = subtiles(total, runs);
+    rt = subtiles<W4>(total, runs);
   }
   // a row starts a segment when its place in its run is a multiple of 16 rt
   int n = 0, start = 0;
@@ -295,7 +306,7 @@ __device__ __forceinline__ void find_segments(SortedSlots& p, int total, int lan
 // The sort and the segments, by the whole workgroup: a slot's place is the
 // number of slots of lower experts and of earlier slots of its own.  key:
 // kMoeMaxSlots words.
-template <bool MANY>
+template <bool W4, bool MANY>
 __device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32_t* ids, int S,
                                            int k, int E, int lane, int wave) {
   constexpr int kSkip = 0x7fffffff;                        // behind all others
@@ -313,7 +324,7 @@ __device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32
         p.eid[at] = e;
         p.sl[at] = slot_word(lane, k);
       }
-      find_segments<MANY>(p, __popcll(__ballot(e != kSkip)), lane);
+      find_segments<W4, MANY>(p, __popcll(__ballot(e != kSkip)), lane);
     }
     __syncthreads();
     return;
@@ -341,7 +352,7 @@ __device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32
   }
   if (valid) atomicAdd(&p.total, valid);
   __syncthreads();
-  if (wave == 0) find_segments<MANY>(p, __builtin_amdgcn_readfirstlane(p.total), lane);
+  if (wave == 0) find_segments<W4, MANY>(p, __builtin_amdgcn_readfirstlane(p.total), lane);
   __syncthreads();
 }
 
@@ -349,12 +360,11 @@ __device__ __forceinline__ void sort_slots(SortedSlots& p, int* key, const int32
 template <int FMT, bool W4, bool RAGGED, int RT>
 __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const SortedSlots& p,
                                         v4f* part, int lane, int wave) {
-  constexpr ScaleMode SM = RAGGED ? kScaleByte : RT == 4 ? kScaleDword : kScaleChunk;
-  constexpr bool CHUNK = W4 && SM == kScaleChunk;
+  constexpr bool CHUNK = W4 && !RAGGED;
   // an item: U K blocks, 128 bytes of a weight row (MXFP4: both halves of a
   // cache line in one go)
-  constexpr int U = W4 && RT < 4 ? 2 : 1;
-  constexpr int D = W4 ? (RT == 1 ? 4 : RT == 2 ? 2 : 3) : (RT == 1 ? 5 : RT == 2 ? 4 : 2);
+  constexpr int U = W4 ? 2 : 1;
+  constexpr int D = W4 ? (RT == 1 ? 4 : 2) : (RT == 1 ? 5 : RT == 2 ? 4 : 2);
   constexpr int SB = FMT == 0 ? 4 : 1;
   const int l16 = lane & 15, g4 = lane >> 4;
   const int64_t K = a.H, I = a.I;
@@ -401,7 +411,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
     const uint32_t xk = (lane & 7) * 16;
     uint32_t xo[2 * RT], so[RT];       // the segment's rows; no row: past the buffers
     int e = 0;
-    WTile<W4, SM> wg, wu;
+    WTile<W4, RAGGED> wg, wu;
     __amdgpu_buffer_rsrc_t sg, su;
     wg.init(K, lane);
     wu.init(K, lane);
@@ -516,8 +526,8 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, uint16_t* h, const Sor
 #pragma unroll
             for (int r = 0; r < RT; ++r) x_to_lds(xbuf + r * 2048, ring[d].x[q][r], lane);
             const uint32_t* ch = chunks + l16 * kChunkRow + (pki * U & (kChunk - 1)) + q;
-            const BFrag bg = wg.bf16(ring[d].g[q], l16, ch);
-            const BFrag bu = wu.bf16(ring[d].u[q], l16, ch + kChunkDwords);
+            const BFrag bg = wg.bf16(ring[d].g[q], ch);
+            const BFrag bu = wu.bf16(ring[d].u[q], ch + kChunkDwords);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
               if (r > 0 && prows <= 16 * r) break;
@@ -588,18 +598,18 @@ template <int FMT, bool W4, bool RAGGED, bool MANY>
 __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uint16_t* h,
                                                                   MoePlan* plan) {
   __shared__ SortedSlots p;
-  // partial products of 1, 2 or 4 subtiles, up to 2 with the scale chunks behind
+  // partial products of 1, 2 or 4 (MXFP4: 2) subtiles, the scale chunks behind
   constexpr int kPart = kMoeWaves * 4 * 64, kChunks = W4 ? kMoeWaves * 2 * kChunkDwords / 4 : 0;
-  __shared__ v4f part[MANY ? (4 * kPart > 2 * kPart + kChunks ? 4 * kPart : 2 * kPart + kChunks)
-                           : kPart + kChunks];
+  __shared__ v4f part[(MANY ? (W4 ? 2 : 4) : 1) * kPart + kChunks];
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
-  sort_slots<MANY>(p, (int*)part, a.ids, a.T * a.k, a.k, a.E, lane, wave);
+  sort_slots<W4, MANY>(p, (int*)part, a.ids, a.T * a.k, a.k, a.E, lane, wave);
   const int rt = MANY ? uniform(p.rt) : 1;
   if (rt == 1) gate_up<FMT, W4, RAGGED, 1>(a, h, p, part, lane, wave);
   if constexpr (MANY) {
     if (rt == 2) gate_up<FMT, W4, RAGGED, 2>(a, h, p, part, lane, wave);
-    if (rt == 4) gate_up<FMT, W4, RAGGED, 4>(a, h, p, part, lane, wave);
+    if constexpr (!W4)
+      if (rt == 4) gate_up<FMT, W4, RAGGED, 4>(a, h, p, part, lane, wave);
   }
   if (blockIdx.x == 0) {
     const int total = uniform(p.total), nsegs = uniform(p.nsegs);
@@ -636,15 +646,14 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
                                      const void* hs, const SortedSlots& p, const float* swt,
                                      float* mine, uint8_t* xl, const uint4* hv, int R, int lane,
                                      int wave) {
-  constexpr int U = W4 && (RT < 4 || QUANT) ? 2 : 1;   // K blocks of an item, as above
+  constexpr int U = W4 ? 2 : 1;        // K blocks of an item, as above
   constexpr int D = QUANT ? (NT == 2 ? 3 : 6) : RT == 1 ? 4 : RT == 2 && !W4 ? 3 : 2;
   constexpr int SB = FMT == 0 ? 4 : 1;
   const int l16 = lane & 15, g4 = lane >> 4;
   const int T = a.T;
   const int64_t N = a.H, K = a.I, n0 = (int64_t)blockIdx.x * R;
   const int KB = (int)(K / 128), KI = (KB + U - 1) / U;
-  constexpr ScaleMode SM = RT == 4 && !QUANT ? kScaleDword : kScaleChunk;
-  constexpr bool CHUNK = W4 && SM == kScaleChunk;
+  constexpr bool CHUNK = W4;           // K is a multiple of 128
   // scale chunks; QUANT: codes of the sorted rows, then their scales; else 2
   // KB RT a wave
   uint32_t* chunks = (uint32_t*)xl + wave * NT * kChunkDwords;
@@ -663,7 +672,7 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
   int lseg = uniform((int)(it0 / KI)), lki = uniform((int)(it0 - (int64_t)lseg * KI)), left = cnt;
   int pseg = lseg, pki = lki;
   uint32_t xo[2 * RT], so[RT];         // the segment's rows; no row: past the buffers
-  WTile<W4, SM> wt[NT];
+  WTile<W4, false> wt[NT];
   __amdgpu_buffer_rsrc_t sw;
   uint32_t swo[NT];                    // this lane's four outputs' row of block scales
 #pragma unroll
@@ -821,7 +830,7 @@ __device__ __forceinline__ void down(const MoeArgs& a, const uint16_t* h, const 
             const uint32_t* ch = chunks + l16 * kChunkRow + (pki * U & (kChunk - 1)) + q;
             BFrag bw[NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) bw[j] = wt[j].bf16(ring[d].w[j][q], l16, ch + j * kChunkDwords);
+            for (int j = 0; j < NT; ++j) bw[j] = wt[j].bf16(ring[d].w[j][q], ch + j * kChunkDwords);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
               if (r > 0 && prows <= 16 * r) break;
@@ -929,7 +938,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a, const 
   if (rt == 1) down<FMT, W4, 1, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, hv, R, lane, wave);
   if constexpr (MANY) {
     if (rt == 2) down<FMT, W4, 2, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, hv, R, lane, wave);
-    if (rt == 4) down<FMT, W4, 4, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, hv, R, lane, wave);
+    if constexpr (!W4)
+      if (rt == 4) down<FMT, W4, 4, QUANT, NT>(a, h, hq, hs, p, swt, mine, xl, hv, R, lane, wave);
   }
   __syncthreads();
   const int Q = R / 4;
@@ -965,12 +975,17 @@ inline MoeWorkspace moe_layout(int64_t S, int64_t I) {
 }
 
 constexpr int kMoeGateUpGroups = 256;      // one workgroup per CU
-constexpr int64_t kMoeQuantBytes = 49152;  // h in LDS, quantized by the down launch
+// h in LDS, quantized by the down launch up to here: its encoding, once per
+// workgroup, costs less than a launch (1 x 8 of 7168, 2048: 27.1 us against
+// 4.6 + 24.1; 43 KB at 5 x 6 of 2064, 1408: 29.0 against 4.8 + 25.0)
+constexpr int64_t kMoeQuantBytes = 49152;
 constexpr size_t kMoeDownBytes = 163840 - sizeof(SortedSlots) - kMoeMaxSlots * 4;
 
 // Output features of a down workgroup: a multiple of 4 from 8 to 32 (to 16
 // where the sums of more would not fit the LDS) with the least to do on the
-// busiest of 256 CUs, the larger where that is equal.
+// busiest of 256 CUs, the larger where that is equal (7168 wide: 28 against
+// 16, 16 tokens x 8 of 256 256 us against 317; 8 and 12 read partly empty
+// tiles: 435).
 inline int moe_down_rows(int64_t H, int T) {
   int best = 0;
   int64_t least = 0;
@@ -985,19 +1000,17 @@ inline int moe_down_rows(int64_t H, int T) {
 }
 
 // LDS of a down workgroup: the sums, and the scale chunks of MXFP4 weights
-inline size_t moe_sums_bytes(const MoeArgs& a) {
-  return (size_t)kMoeWaves * a.T * moe_down_rows(a.H, a.T) * 4;
-}
-inline size_t moe_chunk_bytes(const MoeArgs& a) {
-  return a.w4 ? (size_t)kMoeWaves * (moe_down_rows(a.H, a.T) > 16 ? 2 : 1) * kChunkDwords * 4 : 0;
+inline size_t moe_sums_bytes(const MoeArgs& a, int R) { return (size_t)kMoeWaves * a.T * R * 4; }
+inline size_t moe_chunk_bytes(const MoeArgs& a, int R) {
+  return a.w4 ? (size_t)kMoeWaves * (R > 16 ? 2 : 1) * kChunkDwords * 4 : 0;
 }
 
+// lds: bytes beside the sums
 template <int FMT, bool W4, bool QUANT, bool MANY>
 hipError_t launch_moe_down(const MoeArgs& a, const uint16_t* h, const uint8_t* hq, const void* hs,
-                           const MoePlan* plan, size_t lds, hipStream_t s) {
-  const int R = moe_down_rows(a.H, a.T);
+                           const MoePlan* plan, int R, size_t lds, hipStream_t s) {
   const dim3 grid((unsigned)((a.H + R - 1) / R));
-  lds += moe_sums_bytes(a);
+  lds += moe_sums_bytes(a, R);
   if (R <= 16)
     hipLaunchKernelGGL((moe_down_kernel<FMT, W4, QUANT, 1, MANY>), grid, dim3(kMoeThreads), lds, s,
                        a, h, hq, hs, plan, R);
@@ -1023,16 +1036,22 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
   hipError_t r = hipGetLastError();
   if (r != hipSuccess) return r;
   const int64_t codes = S * (a.I + 16 + a.I / 128 * 4);
-  const size_t chunks = moe_chunk_bytes(a);
-  if (codes <= kMoeQuantBytes && (size_t)codes + chunks + moe_sums_bytes(a) <= kMoeDownBytes)
-    return launch_moe_down<FMT, W4, true, MANY>(a, h, nullptr, nullptr, plan, codes + chunks, s);
+  const int R = moe_down_rows(a.H, a.T);
+  const size_t chunks = moe_chunk_bytes(a, R);
+  if (codes <= kMoeQuantBytes && (size_t)codes + chunks + moe_sums_bytes(a, R) <= kMoeDownBytes) {
+    // FP8: one row tile instead of two nearly full ones while all workgroups
+    // are resident, two to a CU: one's encoding of h runs beside the other's
+    // stream (1 token x 8, widths 7168 / 8192 27 / 31 us against 25 / 28; alike
+    // at 6144, R = 24, and slower at 5120, R = 20, 18 against 19, and with
+    // MXFP4, 34 against 36)
+    const int RQ = !W4 && R > 24 && a.H <= 512 * 16 ? 16 : R;
+    return launch_moe_down<FMT, W4, true, MANY>(a, h, nullptr, nullptr, plan, RQ, codes + chunks, s);
+  }
   r = launch_quant_act(h, S, a.I, a.I, FMT, ws + w.hq, ws + w.hs, s);
   if (r != hipSuccess) return r;
-  return launch_moe_down<FMT, W4, false, MANY>(a, h, ws + w.hq, ws + w.hs, plan,
-                                               // 4 subtiles, or up to 2 beside the scale chunks
-                                               MANY ? std::max((size_t)kMoeWaves * 8192,
-                                                               chunks + kMoeWaves * 4096)
-                                                    : chunks + kMoeWaves * 2048, s);
+  return launch_moe_down<FMT, W4, false, MANY>(a, h, ws + w.hq, ws + w.hs, plan, R,
+                                               // the waves' subtiles: 1, 2 or 4 (MXFP4: 2)
+                                               chunks + kMoeWaves * 2048 * (MANY ? (W4 ? 2 : 4) : 1), s);
 }
 
 template <int FMT, bool W4>
