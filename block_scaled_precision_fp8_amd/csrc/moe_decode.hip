@@ -25,10 +25,10 @@
 // run.
 //
 // Measured (gate/up + down, TB/s of the weights read): 1 token x 8 of 256 FP8
-// experts (7168, 2048) 47.2 + 25.1 us (5.0, 4.7), 16 tokens 536 + 256 us (5.6,
-// 5.9); 64 tokens on 32 of them 171 + 75 us (5.5, 6.3); 33 x 2 of 8 MXFP4
-// experts (4096, 14336) 116 + 70 us (4.3, 3.6); 5 x 6 of 64 (2064, 1408) 38.6 +
-// 28.8 us.  A plain read of 235 MB runs at 5.6 to 5.9.  The MXFP4 stream has
+// experts (7168, 2048) 47.4 + 24.8 us (5.0, 4.7), 16 tokens 531 + 255 us (5.6,
+// 5.9); 64 tokens on 32 of them 169 + 75 us (4.8, 5.5); 33 x 2 of 8 MXFP4
+// experts (4096, 14336) 117 + 69 us (4.3, 3.6); 5 x 6 of 64 (2064, 1408) 38.5 +
+// 28.8 us (3.6, 2.4).  A plain read of 235 MB runs at 5.6 to 5.9.  The MXFP4 stream has
 // half the bytes for the same conversions and exchanges, and its ring drains
 // in part wherever a scale chunk is taken up.  Tried without gain: deeper and
 // shallower rings, 16 waves per workgroup, the waves of a workgroup kept in

@@ -12,6 +12,8 @@
 // One wave per token: lane i holds the experts i, i + 64, ...; each of the k
 // rounds takes the wave's largest (key, lowest id).  Bound by latency (one
 // round of loads, k wave reductions) until some thousands of tokens.
+// Measured: 256 experts in 8 groups, top 8, 1 token 5.2 us, 4096 tokens 10.7;
+// 60 experts, top 4, 333 tokens 3.4.
 #include "bsfp8_internal.h"
 
 namespace bsfp8 {

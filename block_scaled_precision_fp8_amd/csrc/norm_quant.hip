@@ -6,7 +6,9 @@
 //   codes, scales = the activation codec of fp8_quant_act on the fp32 y
 //
 // Bound by HBM: per element 2 bytes of x, 2 of the residual and 2 of h, 1
-// byte of codes (and 2 of the optional bf16 y).
+// byte of codes (and 2 of the optional bf16 y).  Measured: 8192 x 4096 46.6 us
+// (235 MB, 5.0 TB/s; a large copy runs at 5.1), 1031 x 5136 without a residual
+// 10.7 (16 MB), 64 x 4096 4.4, 1 x 7168 4.6 (launches).
 //
 // The sum of squares is held in 64 bits (a square of a bf16 value is exact
 // there, and the vector ALU has the time: one conversion and one FMA per
