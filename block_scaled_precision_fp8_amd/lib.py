@@ -101,6 +101,10 @@ def load(path=None):
     global _device, _raw_stream
     _device = getattr(torch._C, "_cuda_getDevice", _device)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+    global _BF16, _BF16S, _CODES, _SCALES
+    _BF16, _BF16S = torch.bfloat16, (torch.bfloat16,)
+    _CODES = (torch.uint8, torch.float8_e4m3fn)
+    _SCALES = ((torch.float32,), (torch.uint8, torch.float8_e8m0fnu))   # by scale_fmt
     lib = ctypes.CDLL(p)
     for name, (res, args) in _SIGS.items():
         fn = getattr(lib, name)
@@ -152,9 +156,19 @@ def gemm_kernel(M, N, K):
 
 
 def _on_current_device(t):
+    """Its device, -1 for none (refused later: shapes can be checked before)."""
     d = t.get_device()
-    if d >= 0 and d != _device():          # -1: not on a GPU
+    if d >= 0 and d != _device():
         raise ValueError("tensors must be on the current device")
+    return d
+
+
+def _operand(name, t, dtypes, shape, dev):
+    """A dense tensor of one of the dtypes, the shape and the device: what
+    the kernels take its address for."""
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be contiguous {tuple(shape)} of "
+                         f"{' or '.join(str(d) for d in dtypes)} on device {dev}")
 
 
 def _workspace(op, M, N, K, E, ws, device):
@@ -299,13 +313,15 @@ def fp8_add_rmsnorm_quant(x, weight, xq, x_scale, residual=None, residual_out=No
                           act_scale=None, stream=None):
     """x: bf16 (M, K) with row stride ldx; weight bf16 (K,); residual and
     residual_out bf16 (M, K) with one row stride; y bf16 (M, K) out or None;
-    xq uint8 (M, K) and x_scale (M, G) out, or both None; act_scale as for
-    fp8_linear."""
+    xq uint8 or float8_e4m3fn (M, K) and x_scale (M, G) out, fp32 or (UE8M0)
+    uint8 or float8_e8m0fnu, or both None; act_scale as for fp8_linear, of
+    x_scale's type."""
     lib = load()
-    _on_current_device(x)
+    dev = _on_current_device(x)
     shape, (ldx, one), ldr = x.shape, x.stride(), 0
     M, K = shape
-    if residual is not None and residual_out is not None:
+    res = residual is not None and residual_out is not None
+    if res:
         if residual.shape != shape or residual_out.shape != shape:
             raise ValueError("residual and residual_out need the shape of x")
         ldr, inner = residual.stride()
@@ -317,6 +333,24 @@ def fp8_add_rmsnorm_quant(x, weight, xq, x_scale, residual=None, residual_out=No
                 raise ValueError("residual and residual_out need the same row stride")
     if one != 1:
         raise ValueError("rows must be contiguous")
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU")
+    bf16 = _BF16
+    if x.dtype is not bf16 or (res and (
+            residual.dtype is not bf16 or residual.get_device() != dev or
+            residual_out.dtype is not bf16 or residual_out.get_device() != dev)):
+        raise ValueError("x, residual and residual_out must be bf16 on one device")
+    _operand("weight", weight, _BF16S, (K,), dev)
+    if y is not None:
+        _operand("y", y, _BF16S, shape, dev)
+    if xq is not None and x_scale is not None and group_k > 0:
+        kinds = _SCALES[scale_fmt == SCALE_UE8M0]
+        _operand("xq", xq, _CODES, shape, dev)
+        _operand("x_scale", x_scale, kinds, (M, -(-K // group_k)), dev)
+        if act_scheme == ACT_STATIC and act_scale is not None and (
+                act_scale.dtype not in kinds or act_scale.numel() < 1 or
+                act_scale.get_device() != dev):
+            raise ValueError("act_scale must be a scale of x_scale's type on its device")
     _check("fp8_add_rmsnorm_quant", lib.fp8_add_rmsnorm_quant(
         _ptr(x), ldx, _ptr(residual), _ptr(residual_out), ldr, _ptr(weight), eps, M, K,
         group_k, act_scheme, scale_fmt, _ptr(act_scale), _ptr(y), _ptr(xq), _ptr(x_scale),

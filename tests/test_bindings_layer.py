@@ -1,0 +1,115 @@
+"""The norm, router and MoE bindings refuse every tensor that the kernels
+would read or write wrongly: type, shape, order of its elements, device.  No
+GPU and no launch: tensors that say they are on GPU 0 or 1 stand in, and the
+library's calls are recorded."""
+
+import os
+
+import pytest
+import torch
+
+from block_scaled_precision_fp8_amd import lib as L
+
+pytestmark = pytest.mark.skipif(not os.path.exists(L.LIB_PATH), reason="libbsfp8.so not built")
+
+BF16, F32, U8, I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+class Gpu0(torch.Tensor):
+    def get_device(self):
+        return 0
+
+
+class Gpu1(torch.Tensor):
+    def get_device(self):
+        return 1
+
+
+def on0(t):
+    return None if t is None else t.as_subclass(Gpu0)
+
+
+class Recorder:
+    """The library with its entry points recorded, not called."""
+
+    def __init__(self, lib):
+        self.bsfp8_workspace_size = lib.bsfp8_workspace_size
+        self.bsfp8_status_string = lib.bsfp8_status_string
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.calls.append((name, a)) or L.OK
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    rec = Recorder(L.load())
+    monkeypatch.setattr(L, "_lib", rec)
+    monkeypatch.setattr(L, "_device", lambda: 0)
+    monkeypatch.setattr(L, "_raw_stream", lambda device: 0)
+    return rec.calls
+
+
+def refuses(calls, f, **kw):
+    with pytest.raises(ValueError):
+        f(**kw)
+    assert calls == []
+
+
+def columns(t):
+    """The same shape and values, with the elements in another order."""
+    return t.t().contiguous().t() if t.dim() == 2 else t.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+
+def inside(t):
+    """The same shape, a slice of wider rows."""
+    wide = torch.zeros(*t.shape[:-1], t.shape[-1] + 16, dtype=t.dtype)
+    return wide[..., :t.shape[-1]]
+
+
+# ------------------------------------------------------------------ norm
+
+def norm_args(fmt=0, group=128, static=False):
+    M, K = 4, 272
+    sdt = U8 if fmt else F32
+    z = lambda *s, t=BF16: torch.zeros(s, dtype=t)
+    return {k: on0(v) for k, v in dict(
+        x=z(M, K), weight=z(K), xq=z(M, K, t=U8), x_scale=z(M, -(-K // group), t=sdt), residual=z(M, K),
+        residual_out=z(M, K), y=z(M, K), act_scale=z(1, t=sdt) if static else None).items()} | dict(
+        group_k=group, scale_fmt=fmt, act_scheme=L.ACT_STATIC if static else L.ACT_DYNAMIC)
+
+
+@pytest.mark.parametrize("fmt,group,static", [(0, 128, False), (1, 32, False), (0, 128, True), (1, 128, True)])
+def test_norm_operands(calls, fmt, group, static):
+    f = L.fp8_add_rmsnorm_quant
+    good = norm_args(fmt, group, static)
+    f(**good)
+    f(**dict(good, y=None))
+    f(**dict(good, xq=None, x_scale=None))
+    f(**dict(good, residual=None, residual_out=None))
+    f(**dict(good, residual_out=good["residual"], x=on0(inside(good["x"]))))
+    f(**dict(good, xq=on0(good["xq"].view(E4M3))))
+    if fmt:
+        f(**dict(good, x_scale=on0(good["x_scale"].view(E8M0))))
+    assert len(calls) == 6 + fmt
+    calls.clear()
+    names = ["x", "weight", "xq", "x_scale", "residual", "residual_out", "y"] + ["act_scale"] * static
+    for n in names:
+        t = good[n]
+        refuses(calls, f, **dict(good, **{n: t.as_subclass(torch.Tensor)}))     # on no GPU
+        refuses(calls, f, **dict(good, **{n: t.as_subclass(Gpu1)}))
+        refuses(calls, f, **dict(good, **{n: on0(t.to(torch.float16))}))
+        refuses(calls, f, **dict(good, **{n: on0(t.to(U8 if t.dtype == F32 else F32))}))
+        if t.dim() == 2:
+            refuses(calls, f, **dict(good, **{n: on0(columns(t))}))
+            refuses(calls, f, **dict(good, **{n: t[:3]}))
+            if n != "x":
+                refuses(calls, f, **dict(good, **{n: t[:, :-1]}))
+    for n in ("xq", "x_scale", "y"):
+        refuses(calls, f, **dict(good, **{n: on0(inside(good[n]))}))
+    refuses(calls, f, **dict(good, weight=good["weight"][:-16]))
+    refuses(calls, f, **dict(good, weight=on0(torch.zeros(544, dtype=BF16)[::2])))
+    refuses(calls, f, **dict(good, x_scale=good["x_scale"].reshape(-1)))
+    if static:
+        refuses(calls, f, **dict(good, act_scale=good["act_scale"][:0]))
