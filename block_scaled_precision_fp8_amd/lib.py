@@ -333,6 +333,8 @@ def fp8_add_rmsnorm_quant(x, weight, xq, x_scale, residual=None, residual_out=No
                 raise ValueError("residual and residual_out need the same row stride")
     if one != 1:
         raise ValueError("rows must be contiguous")
+    if M == 1:                             # any stride: there is no next row
+        ldx = ldr = K
     if dev < 0:
         raise ValueError("tensors must be on a GPU")
     bf16 = _BF16

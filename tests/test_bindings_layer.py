@@ -113,3 +113,15 @@ def test_norm_operands(calls, fmt, group, static):
     refuses(calls, f, **dict(good, x_scale=good["x_scale"].reshape(-1)))
     if static:
         refuses(calls, f, **dict(good, act_scale=good["act_scale"][:0]))
+
+
+def test_norm_single_row_of_any_stride(calls):
+    """One row has no next: a column vector's transpose is a dense row."""
+    good = norm_args()
+    one = {n: good[n][:1] for n in ("x", "xq", "x_scale", "residual", "residual_out", "y")}
+    L.fp8_add_rmsnorm_quant(**dict(good, **one))
+    turned = {n: on0(torch.zeros(272, 1, dtype=BF16).t()) for n in ("x", "residual", "residual_out")}
+    assert turned["x"].stride() == (1, 1)
+    L.fp8_add_rmsnorm_quant(**dict(good, **dict(one, **turned)))
+    (_, a), (_, b) = calls
+    assert a[1] == b[1] == a[4] == b[4] == 272      # ldx, ldr
