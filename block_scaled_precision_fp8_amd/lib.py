@@ -101,10 +101,10 @@ def load(path=None):
     global _device, _raw_stream
     _device = getattr(torch._C, "_cuda_getDevice", _device)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-    global _BF16, _BF16S, _CODES, _SCALES
-    _BF16, _BF16S = torch.bfloat16, (torch.bfloat16,)
-    _CODES = (torch.uint8, torch.float8_e4m3fn)
-    _SCALES = ((torch.float32,), (torch.uint8, torch.float8_e8m0fnu))   # by scale_fmt
+    global _BF16, _FP32, _INT32, _BF16S, _FP32S, _CODES, _SCALES
+    _BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
+    _BF16S, _FP32S, _CODES = (_BF16,), (_FP32,), (torch.uint8, torch.float8_e4m3fn)
+    _SCALES = (_FP32S, (torch.uint8, torch.float8_e8m0fnu))             # by scale_fmt
     lib = ctypes.CDLL(p)
     for name, (res, args) in _SIGS.items():
         fn = getattr(lib, name)
@@ -363,18 +363,21 @@ def moe_route_topk(logits, ids, weights, bias=None, score=SCORE_SOFTMAX, renorm=
                    n_group=1, topk_group=1, stream=None):
     """logits: fp32 or bf16 (T, E) with row stride ldl; bias fp32 (E,) or
     None; ids int32 (T, k) out; weights fp32 (T, k) out."""
-    import torch
     lib = load()
-    _on_current_device(logits)
+    dev = _on_current_device(logits)
     (T, E), (ldl, one), shape = logits.shape, logits.stride(), ids.shape
-    bf16 = logits.dtype is torch.bfloat16
-    if not (bf16 or logits.dtype is torch.float32) or ids.dtype is not torch.int32 or \
-            weights.dtype is not torch.float32:
+    bf16 = logits.dtype is _BF16
+    if not (bf16 or logits.dtype is _FP32) or ids.dtype is not _INT32 or \
+            weights.dtype is not _FP32:
         raise ValueError("logits must be fp32 or bf16, ids int32 and weights fp32")
     if one != 1 or not (ids.is_contiguous() and weights.is_contiguous()):
         raise ValueError("rows of logits, ids and weights must be contiguous")
     if weights.shape != shape or shape[0] != T:
         raise ValueError("ids and weights must be (T, k)")
+    if dev < 0 or ids.get_device() != dev or weights.get_device() != dev:
+        raise ValueError("tensors must be on one GPU")
+    if bias is not None:
+        _operand("bias", bias, _FP32S, (E,), dev)
     _check("moe_route_topk", lib.moe_route_topk(
         _ptr(logits), ldl, int(bf16), _ptr(bias), T, E,
         shape[1], score, int(renorm), scale, n_group, topk_group, _ptr(ids), _ptr(weights),

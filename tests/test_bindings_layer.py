@@ -125,3 +125,34 @@ def test_norm_single_row_of_any_stride(calls):
     L.fp8_add_rmsnorm_quant(**dict(good, **dict(one, **turned)))
     (_, a), (_, b) = calls
     assert a[1] == b[1] == a[4] == b[4] == 272      # ldx, ldr
+
+
+# ----------------------------------------------------------------- router
+
+def route_args(bf16=False):
+    z = lambda *s, t=F32: torch.zeros(s, dtype=t)
+    return {k: on0(v) for k, v in dict(logits=z(4, 24, t=BF16 if bf16 else F32), ids=z(4, 3, t=I32),
+                                       weights=z(4, 3), bias=z(24)).items()}
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_operands(calls, bf16):
+    f = L.moe_route_topk
+    good = route_args(bf16)
+    f(**good)
+    f(**dict(good, bias=None))
+    f(**dict(good, logits=on0(inside(good["logits"]))))
+    assert len(calls) == 3
+    calls.clear()
+    for n, t in good.items():
+        refuses(calls, f, **dict(good, **{n: t.as_subclass(torch.Tensor)}))
+        refuses(calls, f, **dict(good, **{n: t.as_subclass(Gpu1)}))
+        refuses(calls, f, **dict(good, **{n: on0(t.to(torch.float16))}))
+        refuses(calls, f, **dict(good, **{n: on0(t.to(torch.float64))}))
+        if t.dim() == 2:
+            refuses(calls, f, **dict(good, **{n: on0(columns(t))}))
+    for t in (good["bias"][:23], on0(torch.zeros(25)), on0(good["bias"].to(BF16)),
+              on0(torch.zeros(48)[::2]), good["bias"].reshape(1, 24)):
+        refuses(calls, f, **dict(good, bias=t))
+    refuses(calls, f, **dict(good, ids=on0(inside(good["ids"]))))
+    refuses(calls, f, **dict(good, weights=on0(inside(good["weights"]))))
