@@ -374,6 +374,8 @@ def moe_route_topk(logits, ids, weights, bias=None, score=SCORE_SOFTMAX, renorm=
         raise ValueError("rows of logits, ids and weights must be contiguous")
     if weights.shape != shape or shape[0] != T:
         raise ValueError("ids and weights must be (T, k)")
+    if T == 1:                             # any stride: there is no next row
+        ldl = E
     if dev < 0 or ids.get_device() != dev or weights.get_device() != dev:
         raise ValueError("tensors must be on one GPU")
     if bias is not None:

@@ -156,3 +156,12 @@ def test_route_operands(calls, bf16):
         refuses(calls, f, **dict(good, bias=t))
     refuses(calls, f, **dict(good, ids=on0(inside(good["ids"]))))
     refuses(calls, f, **dict(good, weights=on0(inside(good["weights"]))))
+
+
+def test_route_single_token_of_any_stride(calls):
+    good = route_args()
+    one = dict(good, ids=good["ids"][:1], weights=good["weights"][:1])
+    L.moe_route_topk(**dict(one, logits=good["logits"][:1]))
+    L.moe_route_topk(**dict(one, logits=on0(torch.zeros(24, 1).t())))
+    (_, a), (_, b) = calls
+    assert a[1] == b[1] == 24                       # ldl
