@@ -101,9 +101,10 @@ def load(path=None):
     global _device, _raw_stream
     _device = getattr(torch._C, "_cuda_getDevice", _device)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-    global _BF16, _FP32, _INT32, _BF16S, _FP32S, _CODES, _SCALES
+    global _BF16, _FP32, _INT32, _BF16S, _FP32S, _BYTES, _CODES, _SCALES
     _BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
-    _BF16S, _FP32S, _CODES = (_BF16,), (_FP32,), (torch.uint8, torch.float8_e4m3fn)
+    _BF16S, _FP32S, _BYTES = (_BF16,), (_FP32,), (torch.uint8,)
+    _CODES = (torch.uint8, torch.float8_e4m3fn)
     _SCALES = (_FP32S, (torch.uint8, torch.float8_e8m0fnu))             # by scale_fmt
     lib = ctypes.CDLL(p)
     for name, (res, args) in _SIGS.items():
@@ -388,22 +389,45 @@ def moe_route_topk(logits, ids, weights, bias=None, score=SCORE_SOFTMAX, renorm=
 
 def _moe_decode(fn, xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, I, addend,
                 scale_fmt, workspace, stream):
-    import torch
     lib = load()
-    _on_current_device(xq)
+    dev = _on_current_device(xq)
     T, H = xq.shape
     k = ids.shape[1]
-    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
+    if ids.dtype is not _INT32 or weights.dtype is not _FP32:
         raise ValueError("ids must be int32 and weights fp32")
     if not (xq.is_contiguous() and ids.is_contiguous() and weights.is_contiguous()):
         raise ValueError("xq, ids and weights must be contiguous")
-    E, per = w13.shape[0], 2 if fn == "fp8_fp4_moe_decode" else 1
+    E, w4 = w13.shape[0], fn == "fp8_fp4_moe_decode"
+    per = 2 if w4 else 1
     if ids.shape != weights.shape or ids.shape[0] != T or y.shape != xq.shape or \
             w13.shape != (E, 2 * I, H // per) or w2.shape != (E, H, I // per):
         raise ValueError("shapes of tokens, ids, weights and experts do not agree")
+    # a workspace that is too small is the library's to refuse
+    if workspace is None or workspace.numel() * workspace.element_size() >= \
+            workspace_size(OP_MOE_DECODE, T * k, H, I):
+        if dev < 0 or ids.get_device() != dev or weights.get_device() != dev:
+            raise ValueError("tensors must be on one GPU")
+        if xq.dtype not in _CODES:
+            raise ValueError("xq must be E4M3 codes")
+        if workspace is not None and not (workspace.get_device() == dev and workspace.is_contiguous()):
+            raise ValueError("the workspace must be contiguous, on the device of xq")
+        kinds, HB = _SCALES[scale_fmt == SCALE_UE8M0], -(-H // 128)
+        _operand("x_scale", x_scale, kinds, (T, HB), dev)
+        _operand("y", y, _BF16S, (T, H), dev)
+        if addend is not None:
+            _operand("addend", addend, _BF16S, (T, H), dev)
+        if w4:
+            codes, kinds, s13, s2 = _BYTES, _SCALES[1], (E, 2 * I, H // 32), (E, H, I // 32)
+        else:
+            codes, s13, s2 = _CODES, (E, -(-2 * I // 128), HB), (E, HB, -(-I // 128))
+        _operand("w13", w13, codes, w13.shape, dev)
+        _operand("w13_scale", w13_scale, kinds, s13, dev)
+        _operand("w2", w2, codes, w2.shape, dev)
+        _operand("w2_scale", w2_scale, kinds, s2, dev)
     if workspace is None and stream is not None:
         # from the launch's stream: memory of the current one may still be in
         # use there, and is given out again while the launch runs
+        import torch
         st = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         with torch.cuda.stream(st):
             ws, wsb = _workspace(OP_MOE_DECODE, T * k, H, I, 0, None, xq.device)
@@ -417,8 +441,11 @@ def _moe_decode(fn, xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, 
 
 def fp8_moe_decode(xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, addend=None,
                    scale_fmt=SCALE_FLOAT, workspace=None, stream=None):
-    """xq (T, H) E4M3; ids int32 (T, k); weights fp32 (T, k); w13 (E, 2I, H);
-    w2 (E, H, I); addend bf16 (T, H) or None; y bf16 (T, H) out."""
+    """xq (T, H), w13 (E, 2I, H) and w2 (E, H, I) E4M3 codes (uint8 or
+    float8_e4m3fn); their scales fp32, or (UE8M0) uint8 or float8_e8m0fnu,
+    x_scale (T, ceil(H/128)), w13_scale (E, 2I/128, ceil(H/128)), w2_scale
+    (E, ceil(H/128), I/128); ids int32 (T, k); weights fp32 (T, k); addend
+    bf16 (T, H) or None; y bf16 (T, H) out."""
     _moe_decode("fp8_moe_decode", xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y,
                 w2.shape[2], addend, scale_fmt, workspace, stream)
 

@@ -165,3 +165,49 @@ def test_route_single_token_of_any_stride(calls):
     L.moe_route_topk(**dict(one, logits=on0(torch.zeros(24, 1).t())))
     (_, a), (_, b) = calls
     assert a[1] == b[1] == 24                       # ldl
+
+
+# -------------------------------------------------------------- MoE layer
+
+def moe_args(w4, fmt):
+    T, k, H, I, E = 4, 2, 288, 256, 3
+    z = lambda *s, t=U8: torch.zeros(s, dtype=t)
+    sdt = U8 if fmt else F32
+    if w4:
+        w = dict(w13=z(E, 2 * I, H // 2), w13_scale=z(E, 2 * I, H // 32), w2=z(E, H, I // 2),
+                 w2_scale=z(E, H, I // 32))
+    else:
+        w = dict(w13=z(E, 2 * I, H), w13_scale=z(E, 4, 3, t=sdt), w2=z(E, H, I), w2_scale=z(E, 3, 2, t=sdt))
+    t = dict(w, xq=z(T, H), x_scale=z(T, 3, t=sdt), ids=z(T, k, t=I32), weights=z(T, k, t=F32),
+             y=z(T, H, t=BF16), addend=z(T, H, t=BF16), workspace=z(1 << 20))
+    return {n: on0(v) for n, v in t.items()} | dict(scale_fmt=fmt)
+
+
+@pytest.mark.parametrize("w4", [False, True])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_moe_operands(calls, w4, fmt):
+    f = L.fp8_fp4_moe_decode if w4 else L.fp8_moe_decode
+    good = moe_args(w4, fmt)
+    tensors = {n: t for n, t in good.items() if n != "scale_fmt"}
+    f(**good)
+    f(**dict(good, addend=None))
+    f(**dict(good, addend=good["y"], xq=on0(good["xq"].view(E4M3))))
+    f(**dict(good, **{n: on0(t.view(E8M0)) for n, t in tensors.items() if "scale" in n and t.dtype == U8}))
+    if not w4:
+        f(**dict(good, w13=on0(good["w13"].view(E4M3)), w2=on0(good["w2"].view(E4M3))))
+    assert len(calls) == 4 + (not w4)
+    calls.clear()
+    for n, t in tensors.items():
+        refuses(calls, f, **dict(good, **{n: t.as_subclass(torch.Tensor)}))     # on no GPU
+        refuses(calls, f, **dict(good, **{n: t.as_subclass(Gpu1)}))
+        if n == "workspace":
+            refuses(calls, f, **dict(good, workspace=on0(torch.zeros(2 << 20, dtype=U8)[::2])))
+            continue
+        refuses(calls, f, **dict(good, **{n: on0(t.to(torch.float16))}))
+        refuses(calls, f, **dict(good, **{n: on0(t.to(U8 if t.dtype == F32 else F32))}))
+        refuses(calls, f, **dict(good, **{n: on0(columns(t))}))
+        refuses(calls, f, **dict(good, **{n: on0(inside(t))}))
+        refuses(calls, f, **dict(good, **{n: t[:1]}))
+        refuses(calls, f, **dict(good, **{n: t[..., :-1]}))
+    refuses(calls, f, **dict(good, scale_fmt=1 - fmt))
+    refuses(calls, f, **dict(good, addend=good["addend"][0]))
