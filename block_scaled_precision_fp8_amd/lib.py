@@ -402,9 +402,9 @@ def _moe_decode(fn, xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, 
     if ids.shape != weights.shape or ids.shape[0] != T or y.shape != xq.shape or \
             w13.shape != (E, 2 * I, H // per) or w2.shape != (E, H, I // per):
         raise ValueError("shapes of tokens, ids, weights and experts do not agree")
-    # a workspace that is too small is the library's to refuse
-    if workspace is None or workspace.numel() * workspace.element_size() >= \
-            workspace_size(OP_MOE_DECODE, T * k, H, I):
+    need = lib.bsfp8_workspace_size(OP_MOE_DECODE, T * k, H, I, 0)
+    wsb = need if workspace is None else workspace.numel() * workspace.element_size()
+    if wsb >= need:                        # one that is too small is the library's to refuse
         if dev < 0 or ids.get_device() != dev or weights.get_device() != dev:
             raise ValueError("tensors must be on one GPU")
         if xq.dtype not in _CODES:
@@ -420,22 +420,24 @@ def _moe_decode(fn, xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, 
             codes, kinds, s13, s2 = _BYTES, _SCALES[1], (E, 2 * I, H // 32), (E, H, I // 32)
         else:
             codes, s13, s2 = _CODES, (E, -(-2 * I // 128), HB), (E, HB, -(-I // 128))
-        _operand("w13", w13, codes, w13.shape, dev)
+        if w13.dtype not in codes or not w13.is_contiguous() or w13.get_device() != dev or \
+                w2.dtype not in codes or not w2.is_contiguous() or w2.get_device() != dev:
+            raise ValueError("w13 and w2 must be contiguous codes on the device of xq")
         _operand("w13_scale", w13_scale, kinds, s13, dev)
-        _operand("w2", w2, codes, w2.shape, dev)
         _operand("w2_scale", w2_scale, kinds, s2, dev)
-    if workspace is None and stream is not None:
-        # from the launch's stream: memory of the current one may still be in
-        # use there, and is given out again while the launch runs
+    if workspace is None:
         import torch
-        st = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        with torch.cuda.stream(st):
-            ws, wsb = _workspace(OP_MOE_DECODE, T * k, H, I, 0, None, xq.device)
-    else:
-        ws, wsb = _workspace(OP_MOE_DECODE, T * k, H, I, 0, workspace, xq.device)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
+        else:
+            # from the launch's stream: memory of the current one may still be
+            # in use there, and is given out again while the launch runs
+            st = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            with torch.cuda.stream(st):
+                workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
     _check(fn, getattr(lib, fn)(
         _ptr(xq), _ptr(x_scale), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(w13_scale), _ptr(w2),
-        _ptr(w2_scale), _ptr(addend), _ptr(y), T, k, H, I, E, scale_fmt, _ptr(ws), wsb,
+        _ptr(w2_scale), _ptr(addend), _ptr(y), T, k, H, I, E, scale_fmt, _ptr(workspace), wsb,
         _stream(stream)))
 
 
