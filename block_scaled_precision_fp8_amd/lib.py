@@ -165,11 +165,12 @@ def _on_current_device(t):
 
 
 def _operand(name, t, dtypes, shape, dev):
-    """A dense tensor of one of the dtypes, the shape and the device: what
-    the kernels take its address for."""
+    """The address of a tensor that is as the kernels take it to be: dense, of
+    one of the dtypes, the shape, on the device."""
     if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name} must be contiguous {tuple(shape)} of "
                          f"{' or '.join(str(d) for d in dtypes)} on device {dev}")
+    return t.data_ptr()
 
 
 def _workspace(op, M, N, K, E, ws, device):
@@ -343,21 +344,22 @@ def fp8_add_rmsnorm_quant(x, weight, xq, x_scale, residual=None, residual_out=No
             residual.dtype is not bf16 or residual.get_device() != dev or
             residual_out.dtype is not bf16 or residual_out.get_device() != dev)):
         raise ValueError("x, residual and residual_out must be bf16 on one device")
-    _operand("weight", weight, _BF16S, (K,), dev)
-    if y is not None:
-        _operand("y", y, _BF16S, shape, dev)
-    if xq is not None and x_scale is not None and group_k > 0:
+    pw = _operand("weight", weight, _BF16S, (K,), dev)
+    py = None if y is None else _operand("y", y, _BF16S, shape, dev)
+    if xq is None or x_scale is None or group_k <= 0:
+        pq, ps = _ptr(xq), _ptr(x_scale)   # refused by the library, but for two None
+    else:
         kinds = _SCALES[scale_fmt == SCALE_UE8M0]
-        _operand("xq", xq, _CODES, shape, dev)
-        _operand("x_scale", x_scale, kinds, (M, -(-K // group_k)), dev)
+        pq = _operand("xq", xq, _CODES, shape, dev)
+        ps = _operand("x_scale", x_scale, kinds, (M, -(-K // group_k)), dev)
         if act_scheme == ACT_STATIC and act_scale is not None and (
                 act_scale.dtype not in kinds or act_scale.numel() < 1 or
                 act_scale.get_device() != dev):
             raise ValueError("act_scale must be a scale of x_scale's type on its device")
     _check("fp8_add_rmsnorm_quant", lib.fp8_add_rmsnorm_quant(
-        _ptr(x), ldx, _ptr(residual), _ptr(residual_out), ldr, _ptr(weight), eps, M, K,
-        group_k, act_scheme, scale_fmt, _ptr(act_scale), _ptr(y), _ptr(xq), _ptr(x_scale),
-        _stream(stream)))
+        x.data_ptr(), ldx, _ptr(residual), _ptr(residual_out), ldr, pw, eps, M, K, group_k,
+        act_scheme, scale_fmt, _ptr(act_scale), py, pq, ps,
+        _raw_stream(dev) if stream is None else stream))
 
 
 def moe_route_topk(logits, ids, weights, bias=None, score=SCORE_SOFTMAX, renorm=True, scale=1.0,
@@ -379,12 +381,11 @@ def moe_route_topk(logits, ids, weights, bias=None, score=SCORE_SOFTMAX, renorm=
         ldl = E
     if dev < 0 or ids.get_device() != dev or weights.get_device() != dev:
         raise ValueError("tensors must be on one GPU")
-    if bias is not None:
-        _operand("bias", bias, _FP32S, (E,), dev)
+    pb = None if bias is None else _operand("bias", bias, _FP32S, (E,), dev)
     _check("moe_route_topk", lib.moe_route_topk(
-        _ptr(logits), ldl, int(bf16), _ptr(bias), T, E,
-        shape[1], score, int(renorm), scale, n_group, topk_group, _ptr(ids), _ptr(weights),
-        _stream(stream)))
+        logits.data_ptr(), ldl, int(bf16), pb, T, E, shape[1], score, int(renorm), scale, n_group,
+        topk_group, ids.data_ptr(), weights.data_ptr(),
+        _raw_stream(dev) if stream is None else stream))
 
 
 def _moe_decode(fn, xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, I, addend,
