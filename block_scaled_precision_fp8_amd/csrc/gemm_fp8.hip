@@ -35,12 +35,65 @@ namespace detail {
 
 constexpr int kRowBytes = 128;   // one K block of FP8 codes
 
+__device__ __forceinline__ v8i join(uint4 a, uint4 b) {
+  v8i r;
+  r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+  r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+  return r;
+}
+
 // compile-time loop: f(std::integral_constant<int, 0>) .. f(<N - 1>)
 template <int N, int I = 0, class F>
 __device__ __forceinline__ void static_for(F&& f) {
   if constexpr (I < N) {
     f(std::integral_constant<int, I>{});
     static_for<N, I + 1>(f);
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ float load_scale(const void* p, int64_t idx) {
+  if (FMT == 0) return ((const float*)p)[idx];
+  return __int_as_float(((const uint8_t*)p)[idx]);   // carries the byte
+}
+
+// MFMA step for one 16x16 tile and one K block.
+template <int FMT>
+__device__ __forceinline__ v4f mfma_step(v4f acc, const v8i& a, const v8i& b, float sa,
+                                         float sw) {
+  if (FMT == 0) {
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+    v4f t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 127, 0, 127);
+    const float c = sa * sw;
+    acc[0] = fmaf(t[0], c, acc[0]);
+    acc[1] = fmaf(t[1], c, acc[1]);
+    acc[2] = fmaf(t[2], c, acc[2]);
+    acc[3] = fmaf(t[3], c, acc[3]);
+    return acc;
+  } else {
+    // A = W (scale S_w), B = X (scale S_a); E8M0 bytes in bits [7:0].
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        a, b, acc, 0, 0, 0, __float_as_int(sw), 0, __float_as_int(sa));
+  }
+}
+
+// MFMA step with an MXFP4 weight fragment (A operand, format E2M1: 16
+// bytes per lane in the low half of the register block) and its lane's
+// E8M0 block scale (the 32 weights this lane carries); X stays FP8.
+template <int FMT>
+__device__ __forceinline__ v4f mfma_step_w4(v4f acc, const v8i& a, const v8i& b, float sa,
+                                            int sw4) {
+  if (FMT == 0) {
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+    v4f t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 4, 0, 0, sw4, 0, 127);
+    acc[0] = fmaf(t[0], sa, acc[0]);
+    acc[1] = fmaf(t[1], sa, acc[1]);
+    acc[2] = fmaf(t[2], sa, acc[2]);
+    acc[3] = fmaf(t[3], sa, acc[3]);
+    return acc;
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sw4, 0,
+                                                            __float_as_int(sa));
   }
 }
 

@@ -34,8 +34,6 @@
 // shallower rings, 16 waves per workgroup, the waves of a workgroup kept in
 // step by barriers, non-temporal weight loads (10% slower), a second LDS buffer
 // for the tokens' rows, encoding h under the first weights.
-#include <type_traits>
-
 #include "bsfp8.h"
 #include "bsfp8_internal.h"
 
@@ -57,7 +55,7 @@ __device__ __forceinline__ int nth_of(int w) { return w >> 18; }      // -1 for 
 // The sorted slots and their segments, left by the gate/up launch for the
 // down launch (which loads all arrays before it knows the counts).
 struct MoePlan {
-  int32_t total, nsegs, subtiles, pad;
+  int32_t nsegs, subtiles, pad[2];
   uint16_t seg[kMoeMaxSlots + 8];      // first row of every segment, and total
   int32_t expert[kMoeMaxSlots];
   int32_t slot[kMoeMaxSlots];          // slot words
@@ -614,7 +612,6 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a, uin
   if (blockIdx.x == 0) {
     const int total = uniform(p.total), nsegs = uniform(p.nsegs);
     if (threadIdx.x == 0) {
-      plan->total = total;
       plan->nsegs = nsegs;
       plan->subtiles = rt;
     }
