@@ -199,6 +199,46 @@ __device__ __forceinline__ float e8m0_f32(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : b << 23);   // 2^(b - 127)
 }
 
+typedef unsigned long long u64;
+
+// Exchanges between the lanes of a wave on the vector ALU: inside rows of 16
+// lanes (lane ^ 1, lane ^ 2, mirrored in eight and in sixteen), then the four
+// rows' results one by one.  An exchange through LDS takes ten times as long
+// and was a third of a short row's time.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ u64 dpp64(u64 v) {
+  return (u64)dpp<CTRL>((uint32_t)(v >> 32)) << 32 | dpp<CTRL>((uint32_t)v);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  return __longlong_as_double((long long)dpp64<CTRL>((u64)__double_as_longlong(v)));
+}
+__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+  const u64 u = (u64)__double_as_longlong(v);
+  return __longlong_as_double((long long)((u64)lane_u32((uint32_t)(u >> 32), lane) << 32 |
+                                          lane_u32((uint32_t)u, lane)));
+}
+__device__ __forceinline__ double row16_sum(double v) {
+  v += dpp_f64<kXor1>(v);
+  v += dpp_f64<kXor2>(v);
+  v += dpp_f64<kMirror8>(v);
+  v += dpp_f64<kMirror16>(v);
+  return v;
+}
+// The sum over the wave, in every lane.
+__device__ __forceinline__ double wave_sum(double v) {
+  v = row16_sum(v);
+  return (lane_f64(v, 0) + lane_f64(v, 16)) + (lane_f64(v, 32) + lane_f64(v, 48));
+}
+
 }  // namespace detail
 
 // ---------------------------------------------------------------- host

@@ -19,8 +19,6 @@
 namespace bsfp8 {
 namespace detail {
 
-typedef unsigned long long u64;
-
 constexpr int kRouteWaves = 4;
 constexpr u64 kNever = 0;            // the key of an expert that is never chosen
 
@@ -37,16 +35,7 @@ __device__ __forceinline__ double unordered64(u64 k) {
   return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
 }
 
-// Wave maxima on the vector ALU: exchanges inside rows of 16 lanes, then the
-// four rows' results (an exchange through LDS takes ten times as long).
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
-}
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
-__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int lane) {
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
-}
+// Wave maxima, as wave_sum.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = max(v, dpp<kXor1>(v));
   v = max(v, dpp<kXor2>(v));
@@ -63,24 +52,6 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(__uint_as_float(lane_u32(u, 0)), __uint_as_float(lane_u32(u, 16))),
                fmaxf(__uint_as_float(lane_u32(u, 32)), __uint_as_float(lane_u32(u, 48))));
 }
-template <int CTRL>
-__device__ __forceinline__ u64 dpp64(u64 v) {
-  return (u64)dpp<CTRL>((uint32_t)(v >> 32)) << 32 | dpp<CTRL>((uint32_t)v);
-}
-__device__ __forceinline__ double wave_sum(double v) {
-  v += __longlong_as_double((long long)dpp64<kXor1>((u64)__double_as_longlong(v)));
-  v += __longlong_as_double((long long)dpp64<kXor2>((u64)__double_as_longlong(v)));
-  v += __longlong_as_double((long long)dpp64<kMirror8>((u64)__double_as_longlong(v)));
-  v += __longlong_as_double((long long)dpp64<kMirror16>((u64)__double_as_longlong(v)));
-  double s = 0.0;
-#pragma unroll
-  for (int r = 0; r < 64; r += 16) {
-    const u64 u = (u64)__double_as_longlong(v);
-    s += __longlong_as_double((long long)((u64)lane_u32((uint32_t)(u >> 32), r) << 32 | lane_u32((uint32_t)u, r)));
-  }
-  return s;
-}
-
 // The two largest of two such pairs.
 __device__ __forceinline__ void merge2(u64& a0, u64& a1, u64 b0, u64 b1) {
   const u64 lo = a0 < b0 ? a0 : b0, hi = a0 < b0 ? b0 : a0;

@@ -39,34 +39,6 @@ __device__ __forceinline__ double square_sum8(uint4 v, double s) {
   return s;
 }
 
-// The sum over the wave, in every lane: four steps inside rows of 16 lanes
-// on the vector ALU (lane exchanges through LDS cost ten times as much and
-// were a third of a short row's time), then the four rows' sums.
-template <int CTRL>
-__device__ __forceinline__ double dpp_f64(double v) {
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
-  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
-}
-__device__ __forceinline__ double row16_sum(double v) {
-  v += dpp_f64<0xB1>(v);               // lane ^ 1
-  v += dpp_f64<0x4E>(v);               // lane ^ 2
-  v += dpp_f64<0x141>(v);              // mirrored in eight lanes: the other four
-  v += dpp_f64<0x140>(v);              // mirrored in sixteen: the other eight
-  return v;
-}
-__device__ __forceinline__ double lane_f64(double v, int lane) {
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
-}
-__device__ __forceinline__ double wave_sum(double v) {
-  v = row16_sum(v);
-  return (lane_f64(v, 0) + lane_f64(v, 16)) + (lane_f64(v, 32) + lane_f64(v, 48));
-}
-
 struct RowScale { float hi, lo; };   // rs = hi + lo
 
 // Streaming stores, like the loads: 8192 x 4096 rows 59 us without the hint
