@@ -974,7 +974,9 @@ inline MoeWorkspace moe_layout(int64_t S, int64_t I) {
 constexpr int kMoeGateUpGroups = 256;      // one workgroup per CU
 // h in LDS, quantized by the down launch up to here: its encoding, once per
 // workgroup, costs less than a launch (1 x 8 of 7168, 2048: 27.1 us against
-// 4.6 + 24.1; 43 KB at 5 x 6 of 2064, 1408: 29.0 against 4.8 + 25.0)
+// 4.6 + 24.1; 43 KB at 5 x 6 of 2064, 1408: 29.0 against 4.8 + 25.0; above it
+// 51 KB at 3 x 8 of 7168, 2048: 58.8 against 4.8 + 52.2; 68 KB at 4 x 8: 96
+// against 4.8 + 70.8)
 constexpr int64_t kMoeQuantBytes = 49152;
 constexpr size_t kMoeDownBytes = 163840 - sizeof(SortedSlots) - kMoeMaxSlots * 4;
 
@@ -1036,12 +1038,15 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
   const int R = moe_down_rows(a.H, a.T);
   const size_t chunks = moe_chunk_bytes(a, R);
   if (codes <= kMoeQuantBytes && (size_t)codes + chunks + moe_sums_bytes(a, R) <= kMoeDownBytes) {
-    // FP8: one row tile instead of two nearly full ones while all workgroups
-    // are resident, two to a CU: one's encoding of h runs beside the other's
-    // stream (1 token x 8, widths 7168 / 8192 27 / 31 us against 25 / 28; alike
-    // at 6144, R = 24, and slower at 5120, R = 20, 18 against 19, and with
-    // MXFP4, 34 against 36)
-    const int RQ = !W4 && R > 24 && a.H <= 512 * 16 ? 16 : R;
+    // FP8, up to 16 tokens: one row tile instead of two nearly full ones while
+    // all workgroups are resident, two to a CU: one's encoding of h runs beside
+    // the other's stream (1 token x 8, widths 7168 / 8192 27.1 / 31 us against
+    // 25.2 / 28, 16 tokens of one expert each 34.3 against 34.2; alike at 6144,
+    // R = 24, and slower at 5120, R = 20, 18 against 19, and with MXFP4, 34
+    // against 36).  The kernel for more tokens has registers for one workgroup
+    // per CU: at 7168 two rounds of R = 16 take 56.3 us for 20 tokens and 61.9
+    // for 32, one round of R = 28 44.9 and 48.7
+    const int RQ = !W4 && !MANY && R > 24 && a.H <= 512 * 16 ? 16 : R;
     return launch_moe_down<FMT, W4, true, MANY>(a, h, nullptr, nullptr, plan, RQ, codes + chunks, s);
   }
   r = launch_quant_act(h, S, a.I, a.I, FMT, ws + w.hq, ws + w.hs, s);

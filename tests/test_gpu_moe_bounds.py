@@ -11,7 +11,7 @@ from oracle import formats as F
 from oracle import quant as Q
 
 from gpu_util import to_dev, to_dev_bf16, bf16_bits, rel_fro, say
-from test_gpu_moe_decode import codes_of, experts, layer, probe, routing
+from test_gpu_moe_decode import case, codes_of, experts, layer, probe, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,11 @@ def test_layer_within_its_arithmetic(T, k, H, I, E, fmt, w4):
     off = np.abs(y - ref)
     say(f"  y at {np.max(off / tol):.3f} of its bound, rel fro {rel_fro(y, ref):.2e}")
     assert np.all(off <= tol)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("T,k,H,I,E", [(17, 1, 7168, 256, 3), (32, 1, 8192, 128, 2), (24, 2, 7184, 128, 4)])
+def test_wide_rows_many_tokens(T, k, H, I, E, fmt):
+    """More than 16 tokens whose h is quantized in the down launch, 28 or 32
+    output features to a workgroup."""
+    case(T, k, H, I, E, fmt, add=True, seed=T)
