@@ -8,7 +8,7 @@
 #include <cstring>
 
 #include "bsfp8.h"
-#include "bsfp8_internal.h"
+#include "bsfp8_layer.h"
 
 using namespace bsfp8;
 

@@ -57,6 +57,10 @@ __device__ __forceinline__ float load_scale(const void* p, int64_t idx) {
   return __int_as_float(((const uint8_t*)p)[idx]);   // carries the byte
 }
 
+__device__ __forceinline__ float e8m0_f32(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b << 23);   // 2^(b - 127)
+}
+
 // MFMA step for one 16x16 tile and one K block.
 template <int FMT>
 __device__ __forceinline__ v4f mfma_step(v4f acc, const v8i& a, const v8i& b, float sa,

@@ -35,7 +35,7 @@
 // step by barriers, non-temporal weight loads (10% slower), a second LDS buffer
 // for the tokens' rows, encoding h under the first weights.
 #include "bsfp8.h"
-#include "bsfp8_internal.h"
+#include "bsfp8_layer.h"
 
 namespace bsfp8 {
 namespace detail {

@@ -14,7 +14,7 @@
 // round of loads, k wave reductions) until some thousands of tokens.
 // Measured: 256 experts in 8 groups, top 8, 1 token 5.2 us, 4096 tokens 10.7;
 // 60 experts, top 4, 333 tokens 3.4.
-#include "bsfp8_internal.h"
+#include "bsfp8_layer.h"
 
 namespace bsfp8 {
 namespace detail {

@@ -17,7 +17,7 @@
 // codes and scales do not depend on how a row is dealt to lanes.  y is not
 // rounded to bf16 before it is quantized: the codes then carry one rounding,
 // and a group's scale does not jump by a bf16 step.
-#include "bsfp8_internal.h"
+#include "bsfp8_layer.h"
 
 namespace bsfp8 {
 namespace detail {

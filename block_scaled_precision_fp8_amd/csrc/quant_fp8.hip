@@ -16,7 +16,7 @@
 //          exact correction for a normal s, IEEE division otherwise).
 //   UE8M0: s = 2^e, e = ceil(log2(amax / 448)) clamped to [-127, 127] (fp32
 //          scales round *up* to UE8M0), code = E4M3(x * 2^-e) (exact scaling).
-#include "bsfp8_internal.h"
+#include "bsfp8_layer.h"
 
 namespace bsfp8 {
 namespace detail {
