@@ -5,8 +5,10 @@
 //   h    = bf16(silu(g) u), quantized in 1 x 128 groups (fp8_quant_act)
 //   y_t  = bf16(addend_t + sum_j wt[t][j] (h_q W2_e^T)),  summed in fp32
 //
-// Bound by HBM: every expert that a token chose is read once, 3 H I bytes
-// (half with MXFP4 weights); the tokens' own data is small and stays in L2.
+// Bound by HBM: an expert that a token chose is read once for every segment
+// of 16, 32 or 64 of its slots (see subtiles), once where it has no more: 3 H I
+// bytes (half with MXFP4 weights); the tokens' own data is small and stays in
+// L2.
 //
 //   moe_gate_up_kernel  one workgroup per CU; its tasks are (segment of an
 //                       expert's slots, 16 columns of h), dealt in equal
@@ -21,14 +23,17 @@
 //
 // In both a workgroup's waves take equal contiguous shares of its (task, K
 // block) pairs and stream the weights through a ring of registers across
-// tasks, with no barrier until the end.  No atomics: the same bits on every
-// run.
+// tasks, with no barrier until the end.  No sum depends on an order that
+// varies (the one atomic counts slots, in LDS): the same bits on every run.
 //
 // Measured (gate/up + down, TB/s of the weights read): 1 token x 8 of 256 FP8
-// experts (7168, 2048) 47.4 + 24.8 us (5.0, 4.7), 16 tokens 531 + 255 us (5.6,
-// 5.9); 64 tokens on 32 of them 169 + 75 us (4.8, 5.5); 33 x 2 of 8 MXFP4
-// experts (4096, 14336) 117 + 69 us (4.3, 3.6); 5 x 6 of 64 (2064, 1408) 38.5 +
-// 28.8 us (3.6, 2.4).  A plain read of 235 MB runs at 5.6 to 5.9.  The MXFP4 stream has
+// experts (7168, 2048) 47.5 + 25.0 us (4.9, 4.7), 16 tokens 542 + 255 us (5.5,
+// 5.9); 64 tokens on 32 of them 174 + 76 us (4.7, 5.3); 33 x 2 of 8 MXFP4
+// experts (4096, 14336) 121 + 73 us (4.1, 3.4); 5 x 6 of 64 (2064, 1408) 40.6 +
+// 30.2 us (3.4, 2.3); boxes differ by 3%.  128 tokens: 2 of 8 FP8 experts (4096,
+// 14336) 273 + 189 us, MXFP4 236 + 152; 8 of 64 (7168, 2048) 498 + 285; one of
+// those 64 for all 128 tokens and the others for one each 436 + 204.  A plain
+// read of 235 MB runs at 5.6 to 5.9.  The MXFP4 stream has
 // half the bytes for the same conversions and exchanges, and its ring drains
 // in part wherever a scale chunk is taken up.  Tried without gain: deeper and
 // shallower rings, 16 waves per workgroup, the waves of a workgroup kept in
@@ -258,8 +263,9 @@ struct SortedSlots {
   int nsegs, total, rt;                // rt: subtiles of a segment
 };
 
-// Subtiles of 16 rows per segment, by the average run: a run of more rows
-// reads its weights again, a subtile costs registers and a shorter ring.
+// Subtiles of 16 rows per segment, by the average run of an expert's slots: a
+// run of more rows reads its weights again, a subtile costs registers and a
+// shorter ring.  The average says little where one expert has most slots.
 // Measured, gate/up + down us with 1 / 2 / 4: FP8, runs of 8 (7168, 2048, 64
 // experts) 390 + 169 / 392 + 177 / 456 + 225, of 16 (4096, 14336, 8 experts)
 // 291 + 160 / 219 + 140 / 239 + 152, of 32 469 + 270 / 344 + 217 / 272 + 192.
@@ -1042,10 +1048,10 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
     // all workgroups are resident, two to a CU: one's encoding of h runs beside
     // the other's stream (1 token x 8, widths 7168 / 8192 27.1 / 31 us against
     // 25.2 / 28, 16 tokens of one expert each 34.3 against 34.2; alike at 6144,
-    // R = 24, and slower at 5120, R = 20, 18 against 19, and with MXFP4, 34
-    // against 36).  The kernel for more tokens has registers for one workgroup
-    // per CU: at 7168 two rounds of R = 16 take 56.3 us for 20 tokens and 61.9
-    // for 32, one round of R = 28 44.9 and 48.7
+    // R = 24, and slower at 5120, R = 20, 18 against 19, and with MXFP4, 7168 /
+    // 8192 19.2 / 20.8 against 22.0 / 22.6).  The kernel for more tokens has
+    // registers for one workgroup per CU: at 7168 two rounds of R = 16 take
+    // 56.3 us for 20 tokens and 61.9 for 32, one round of R = 28 44.9 and 48.7
     const int RQ = !W4 && !MANY && R > 24 && a.H <= 512 * 16 ? 16 : R;
     return launch_moe_down<FMT, W4, true, MANY>(a, h, nullptr, nullptr, plan, RQ, codes + chunks, s);
   }

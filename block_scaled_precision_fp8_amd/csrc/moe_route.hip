@@ -10,10 +10,13 @@
 //   weights = s[ids] (divided by their sum: renorm) * scale
 //
 // One wave per token: lane i holds the experts i, i + 64, ...; each of the k
-// rounds takes the wave's largest (key, lowest id).  Bound by latency (one
-// round of loads, k wave reductions) until some thousands of tokens.
-// Measured: 256 experts in 8 groups, top 8, 1 token 5.2 us, 4096 tokens 10.7;
-// 60 experts, top 4, 333 tokens 3.4.
+// rounds takes the wave's largest (key, lowest id).  Bound by latency for a
+// token (one round of loads, k wave reductions), by vector issue for a prompt:
+// with 256 experts in 8 groups, sigmoid, top 8, a token takes 958 vector
+// instructions, and the four waves that 4096 tokens give each SIMD issue for
+// 15.3 thousand of the 18.3 thousand cycles that a wave lives.
+// Measured: those 256 experts, 1 token 5.1 us, 4096 tokens 10.8; 60 experts, top
+// 4, 333 tokens 3.3.
 #include "bsfp8_layer.h"
 
 namespace bsfp8 {
@@ -84,11 +87,15 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_topk_kernel(RouteArgs 
   }
   if (SOFT) top = wave_max(top);
 
-  // in 64 bits: scores that fp32 cannot hold still have a ratio.  At the top
-  // 1, +inf included; -inf gives 0
+  // Scores in 64 bits: those that fp32 cannot hold still have a ratio.  At
+  // the top 1, +inf included; -inf gives 0
   auto expo = [&](float v) -> double { return v == top ? 1.0 : exp((double)v - (double)top); };
-  // softmax denominators: needed for the scores as such, not where the
-  // chosen ones are divided by their own sum
+  // Softmax denominators: needed for the scores as such, not where the
+  // chosen ones are divided by their own sum.  Where they do not enter the
+  // keys their terms e^d, d = v - top, are fp32 values (d rounded: |d| 2^-24 of
+  // the term, the exponential 2^-22), summed in 64 bits: off by the terms'
+  // average |d| + 4, times 2^-24, of the weight, which is rounded to fp32
+  // itself.  64-bit exponentials of all experts are left to keys that need them
   double Z = 1.0;
   if (SOFT && (K64 || !a.renorm)) {
     Z = 0.0;

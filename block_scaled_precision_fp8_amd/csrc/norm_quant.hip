@@ -6,17 +6,25 @@
 //   codes, scales = the activation codec of fp8_quant_act on the fp32 y
 //
 // Bound by HBM: per element 2 bytes of x, 2 of the residual and 2 of h, 1
-// byte of codes (and 2 of the optional bf16 y).  Measured: 8192 x 4096 46.6 us
-// (235 MB, 5.0 TB/s; a large copy runs at 5.1), 1031 x 5136 without a residual
-// 10.7 (16 MB), 64 x 4096 4.4, 1 x 7168 4.6 (launches).
+// byte of codes (and 2 of the optional bf16 y).  Measured, launches in the
+// profiler: 8192 x 4096 46 to 49 us (235 MB, 4.8 to 5.1 TB/s; a large copy runs
+// at 5.1), 1031 x 5136 without a residual 11.8 (16 MB), 64 x 4096 4.4, 1 x 7168
+// 4.7.  Rows of two chunks a lane (520 to 1024 values, 8200 to 16384) load the
+// second one after the first, and rows of 4104 to 8192 values leave up to half
+// of 1024 lanes idle: 8192 x 1024 16.4 us where its 59 MB copy in 11.6, 1031 x
+// 5136 with its residual 14.2 (37 MB: 7.3).
 //
 // The sum of squares is held in 64 bits (a square of a bf16 value is exact
 // there, and the vector ALU has the time: one conversion and one FMA per
-// element under the loads).  h w is exact in fp32 (8 + 8 significant bits),
-// so with rs as a sum of two fp32 values y is the correctly rounded h w rs:
-// codes and scales do not depend on how a row is dealt to lanes.  y is not
-// rounded to bf16 before it is quantized: the codes then carry one rounding,
-// and a group's scale does not jump by a bf16 step.
+// element under the loads): it errs by at most K 2^-53 of itself, rs by half
+// of that.  h w is exact in fp32 (8 + 8 significant bits; products below
+// 2^-126 aside), rs is a sum of two fp32 values (2^-48 of it lost) and its
+// small part's product is rounded before the sum (as much again): y is h w rs
+// rounded once, to within 1/2 + (K + 128) 2^-31 units in the last place.  Only
+// values that near a border between two fp32 numbers can depend on how a row
+// is dealt to lanes.  y is not rounded to bf16 before it is quantized: the
+// codes then carry one rounding, and a group's scale does not jump by a bf16
+// step.
 #include "bsfp8_layer.h"
 
 namespace bsfp8 {
@@ -42,7 +50,7 @@ __device__ __forceinline__ double square_sum8(uint4 v, double s) {
 struct RowScale { float hi, lo; };   // rs = hi + lo
 
 // Streaming stores, like the loads: 8192 x 4096 rows 59 us without the hint
-// on either store, 49 with it on the codes, 47.5 on both.
+// on either store, 49 with it on the codes, 47 on both.
 __device__ __forceinline__ void st_stream16(void* p, uint4 v) {
   __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, (u32x4*)p);
 }
@@ -186,10 +194,10 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
                      row_grid(TPR < 256 ? (a.M + 256 / TPR - 1) / (256 / TPR) : a.M), \
                      dim3(TPR < 256 ? 256 : TPR), 0, s, a)
   // One chunk per lane where a workgroup has the lanes: the fewest registers
-  // and the most rows in flight (8192 x 4096: 512 lanes 50 us, 256 lanes of two
-  // chunks 52, one wave of eight 70).  Below 1024 values a whole workgroup
-  // per row costs more in barriers than it spreads (8192 x 1024: one wave of
-  // two chunks 17 us, 256 lanes 22).
+  // and the most rows in flight (8192 x 4096: 512 lanes 47.1 us, 256 lanes of
+  // two chunks 46.1, one wave of eight 65).  Up to 1024 values a whole
+  // workgroup per row costs more in barriers than it spreads (8192 x 1024: one
+  // wave of two chunks 16.4 us, 256 lanes 20.5).
   const int64_t C = a.K / 8;
   if (C <= 64) BSFP8_NORM(64, 1);
   else if (C <= 128) BSFP8_NORM(64, 2);

@@ -141,9 +141,8 @@ BSFP8_API int32_t fp8_quant_act(const void* x, int64_t M, int64_t K, int64_t ldx
  *   codes, scales = those of fp8_quant_act's codec (per group_k group, or
  *   the static scale) applied to the fp32 row y, which is not rounded to
  *   bf16 in between.
- * The mean is held in 64 bits and y is correctly rounded (one fp32 rounding
- * of the exact product), so the results do not depend on the row's length
- * or on how it is dealt to the hardware.
+ * The mean is held in 64 bits and y is the product rounded once, to within
+ * 1/2 + (K + 128) 2^-31 units in the last place.
  *
  *   x            bf16 [M][ldx], read-only; K % 16 == 0, ldx >= K, ldx % 8 == 0.
  *   residual     bf16 [M][ldr] or NULL; residual_out bf16 [M][ldr], out: h.
@@ -188,7 +187,10 @@ BSFP8_API int32_t fp8_add_rmsnorm_quant(const void* x, int64_t ldx, const void* 
  *   weights = s[ids], divided by their sum when renorm is 1, times scale
  * Ties go to the lower expert or group.  An expert whose logit is NaN or
  * -inf, or whose key is, is never chosen (NaN and -inf logits count as
- * score 0); a slot with no expert left gets id -1 and weight 0.
+ * score 0); a slot with no expert left gets id -1 and weight 0.  Scores
+ * below what 64 bits hold are 0 (sigmoid of logits under about -745, softmax
+ * of logits that far below the row's largest), and so are all weights of a
+ * token whose chosen scores are.
  *
  *   logits       [T][ldl], fp32 or (logits_bf16 = 1) bf16, ldl >= E, any
  *                ldl; aligned to its type only.
@@ -375,8 +377,11 @@ BSFP8_API int32_t fp8_grouped_gemm_silu_mul_quant(const void* xq, const void* x_
  *   y[t] = bf16_rne( addend[t] + sum_j weights[t][j] * d(t, j) )
  *
  * that is fp8_grouped_gemm_silu_mul_quant, fp8_grouped_gemm and the
- * weighted sum, without rounding d to bf16.  Every expert that some token
- * names is read once.  Deterministic: the same call gives the same bits.
+ * weighted sum, without rounding d to bf16.  An expert that some token
+ * names is read once for every 16 of its slots (32, FP8 also 64, where
+ * experts have more than 10, 20 slots each on average).  From 16 to 32 slots
+ * an expert on average on, the sorted path's two GEMMs take less time.
+ * Deterministic: the same call gives the same bits.
  *
  *   xq, x_scale  as written by fp8_quant_act or fp8_add_rmsnorm_quant
  *                (T rows of H, 1 x 128 groups).
