@@ -379,8 +379,9 @@ BSFP8_API int32_t fp8_grouped_gemm_silu_mul_quant(const void* xq, const void* x_
  * that is fp8_grouped_gemm_silu_mul_quant, fp8_grouped_gemm and the
  * weighted sum, without rounding d to bf16.  An expert that some token
  * names is read once for every 16 of its slots (32, FP8 also 64, where
- * experts have more than 10, 20 slots each on average).  From 16 to 32 slots
- * an expert on average on, the sorted path's two GEMMs take less time.
+ * experts have more than 10, 20 slots each on average).  From some 8 (experts
+ * of 7168 x 2048) to 32 (4096 x 14336) slots an expert on average on, the
+ * sorted path's two GEMMs take less time.
  * Deterministic: the same call gives the same bits.
  *
  *   xq, x_scale  as written by fp8_quant_act or fp8_add_rmsnorm_quant
