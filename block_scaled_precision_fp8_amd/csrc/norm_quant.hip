@@ -20,11 +20,12 @@
 // of that.  h w is exact in fp32 (8 + 8 significant bits; products below
 // 2^-126 aside), rs is a sum of two fp32 values (2^-48 of it lost) and its
 // small part's product is rounded before the sum (as much again): y is h w rs
-// rounded once, to within 1/2 + (K + 128) 2^-31 units in the last place.  Only
-// values that near a border between two fp32 numbers can depend on how a row
-// is dealt to lanes.  y is not rounded to bf16 before it is quantized: the
-// codes then carry one rounding, and a group's scale does not jump by a bf16
-// step.
+// rounded once, to within 1/2 + (K + 140) 2^-30 units in the last place, where
+// no small part runs out of exponents (root mean squares below 2^100, y above
+// 2^-100).  Only values that near a border between two fp32 numbers can depend
+// on how a row is dealt to lanes.  y is not rounded to bf16 before it is
+// quantized: the codes then carry one rounding, and a group's scale does not
+// jump by a bf16 step.
 #include "bsfp8_layer.h"
 
 namespace bsfp8 {

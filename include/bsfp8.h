@@ -142,7 +142,8 @@ BSFP8_API int32_t fp8_quant_act(const void* x, int64_t M, int64_t K, int64_t ldx
  *   the static scale) applied to the fp32 row y, which is not rounded to
  *   bf16 in between.
  * The mean is held in 64 bits and y is the product rounded once, to within
- * 1/2 + (K + 128) 2^-31 units in the last place.
+ * 1/2 + (K + 140) 2^-30 units in the last place (rows of a root mean square
+ * below 2^100, |y| above 2^-100).
  *
  *   x            bf16 [M][ldx], read-only; K % 16 == 0, ldx >= K, ldx % 8 == 0.
  *   residual     bf16 [M][ldr] or NULL; residual_out bf16 [M][ldr], out: h.
