@@ -8,7 +8,7 @@
 #include <cstring>
 
 #include "bsfp8.h"
-#include "bsfp8_layer.h"
+#include "bsfp8_attn.h"
 
 using namespace bsfp8;
 
@@ -54,6 +54,50 @@ int32_t check_gemm(const void* xq, const void* xs, const void* wq, const void* w
   if (!xq || !xs || !wq || !ws || !y) return BSFP8_EINVAL;
   if (!al16(xq) || !al16(wq) || !al16(y) || (bias && !al16(bias))) return BSFP8_EINVAL;
   if (!al16(xs) || !al16(ws)) return BSFP8_EINVAL;
+  return BSFP8_OK;
+}
+
+
+// ---- the paged cache and attention over it
+
+constexpr int32_t kAttnMaxHeads = 1024;
+bool valid_head(int32_t D) { return D == 64 || D == 128 || D == 256; }
+
+int32_t check_page_size(int32_t page_size) {
+  if (page_size <= 0) return BSFP8_EINVAL;
+  if (page_size < 16 || (page_size & (page_size - 1)) != 0) return BSFP8_ENOTSUP;
+  return BSFP8_OK;
+}
+
+int32_t check_cache(int32_t fmt, int64_t num_pages, int32_t page_size, const void* kc,
+                    const void* vc, const void* ks, const void* vs) {
+  if (fmt != BSFP8_KV_FP8_FLOAT && fmt != BSFP8_KV_FP8_UE8M0 && fmt != BSFP8_KV_BF16)
+    return BSFP8_EINVAL;
+  int32_t r = check_page_size(page_size);
+  if (r != BSFP8_OK) return r;
+  if (num_pages < 1 || !fits_i32(num_pages)) return BSFP8_EINVAL;
+  if (!kc || !vc || !al16(kc) || !al16(vc) || !al16(ks) || !al16(vs)) return BSFP8_EINVAL;
+  if (fmt != BSFP8_KV_BF16 && (!ks || !vs)) return BSFP8_EINVAL;
+  return BSFP8_OK;
+}
+
+int32_t check_attn_sizes(int64_t T, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                         int64_t max_pages, int32_t page_size, int64_t prefix_len) {
+  if (T < 0 || B < 0 || !fits_i32(T) || !fits_i32(B)) return BSFP8_EINVAL;
+  if (Hkv < 1 || Hq < Hkv || Hq > kAttnMaxHeads || Hq % Hkv != 0 || D <= 0) return BSFP8_EINVAL;
+  int32_t r = check_page_size(page_size);
+  if (r != BSFP8_OK) return r;
+  if (max_pages < 0 || prefix_len < 0 || !fits_i32(max_pages)) return BSFP8_EINVAL;
+  if (!valid_head(D) || B > kAttnMaxSeqs) return BSFP8_ENOTSUP;
+  if (max_pages * page_size > kAttnMaxKeys || prefix_len > kAttnMaxKeys) return BSFP8_ENOTSUP;
+  if (T * Hq > 0x7fffffffLL) return BSFP8_ENOTSUP;
+  if (T == 0 || B == 0) return BSFP8_OK;
+  // work units and partial rows are counted in 32 bits
+  const int64_t blocks = T * (Hq / Hkv) / 16 + B + 1;
+  if ((double)blocks * Hkv * (((double)max_pages * page_size + prefix_len) / 128 + 2) > 2e9)
+    return BSFP8_ENOTSUP;
+  const AttnPlan p = attn_plan(T, B, Hq, Hkv, D, max_pages * page_size, prefix_len);
+  if (p.own_slots * p.own_rows + p.pre_slots * p.pre_rows > 0x7fffffffLL) return BSFP8_ENOTSUP;
   return BSFP8_OK;
 }
 
@@ -313,6 +357,123 @@ int32_t moe_route_topk(const void* logits, int64_t ldl, int32_t logits_bf16, con
   a.k = k; a.score = score; a.renorm = renorm; a.scale = scale;
   a.n_group = n_group; a.topk_group = topk_group; a.ids = ids; a.weights = weights;
   return hip_status(launch_route_topk(a, (hipStream_t)stream));
+}
+
+int32_t rope_inv_freq(int32_t scaling, int64_t rot_dim, double base, double factor, double low,
+                      double high, double orig_len, float* inv_freq, void* stream) {
+  if (scaling != BSFP8_ROPE_PLAIN && scaling != BSFP8_ROPE_LINEAR && scaling != BSFP8_ROPE_BY_PARTS)
+    return BSFP8_EINVAL;
+  if (rot_dim < 0 || rot_dim % 16 != 0) return BSFP8_EINVAL;
+  if (rot_dim > 256) return BSFP8_ENOTSUP;
+  if (!(base >= 1.0) || !(base <= 1e30)) return BSFP8_EINVAL;
+  if (scaling != BSFP8_ROPE_PLAIN && (!(factor > 0.0) || !(factor <= 1e30))) return BSFP8_EINVAL;
+  if (scaling == BSFP8_ROPE_BY_PARTS &&
+      (!(low >= 0.0) || !(high > low) || !(high <= 1e30) || !(orig_len > 0.0) || !(orig_len <= 1e30)))
+    return BSFP8_EINVAL;
+  if (rot_dim == 0) return BSFP8_OK;
+  if (!inv_freq || ((uintptr_t)inv_freq & 3u)) return BSFP8_EINVAL;
+  int32_t r = check_device(stream);
+  if (r != BSFP8_OK) return r;
+  return hip_status(launch_rope_inv_freq(scaling, (int)rot_dim, base, factor, low, high, orig_len,
+                                         inv_freq, (hipStream_t)stream));
+}
+
+int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const void* k,
+                       int64_t ldk, const void* v, int64_t ldv, const int32_t* positions,
+                       const float* inv_freq, int64_t rot_dim, int32_t interleaved, float mscale,
+                       const int64_t* slots, int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                       int32_t kv_fmt, int64_t num_pages, int32_t page_size, void* k_cache,
+                       void* v_cache, void* k_scale, void* v_scale, void* stream) {
+  if (T < 0 || !fits_i32(T)) return BSFP8_EINVAL;
+  if (interleaved != 0 && interleaved != 1) return BSFP8_EINVAL;
+  if (rot_dim < 0 || rot_dim % 16 != 0 || rot_dim > D) return BSFP8_EINVAL;
+  if (!(mscale > 0.0f) || !(mscale <= 3.4028234663852886e38f)) return BSFP8_EINVAL;
+  if (D <= 0) return BSFP8_EINVAL;
+  if (!valid_head(D)) return BSFP8_ENOTSUP;
+  if ((!q) != (!q_out) || (!k) != (!v) || (!q && !k && T > 0)) return BSFP8_EINVAL;
+  if (T == 0) return BSFP8_OK;
+  if (rot_dim && (!positions || !inv_freq || ((uintptr_t)positions & 3u) || ((uintptr_t)inv_freq & 3u)))
+    return BSFP8_EINVAL;
+  if (q) {
+    if (Hq < 1 || Hq > kAttnMaxHeads) return BSFP8_EINVAL;
+    if (ldq < (int64_t)Hq * D || ldq % 8 != 0 || ldqo < (int64_t)Hq * D || ldqo % 8 != 0)
+      return BSFP8_EINVAL;
+    if (!al16(q) || !al16(q_out)) return BSFP8_EINVAL;
+  }
+  if (k) {
+    if (Hkv < 1 || Hkv > kAttnMaxHeads) return BSFP8_EINVAL;
+    if (ldk < (int64_t)Hkv * D || ldk % 8 != 0 || ldv < (int64_t)Hkv * D || ldv % 8 != 0)
+      return BSFP8_EINVAL;
+    int32_t r = check_cache(kv_fmt, num_pages, page_size, k_cache, v_cache, k_scale, v_scale);
+    if (r != BSFP8_OK) return r;
+    if (!al16(k) || !al16(v) || !slots || ((uintptr_t)slots & 7u)) return BSFP8_EINVAL;
+  }
+  int32_t r = check_device(stream);
+  if (r != BSFP8_OK) return r;
+  RopeKvArgs a{};
+  a.q = (const uint16_t*)q; a.ldq = ldq; a.q_out = (uint16_t*)q_out; a.ldqo = ldqo;
+  a.k = (const uint16_t*)k; a.ldk = ldk; a.v = (const uint16_t*)v; a.ldv = ldv;
+  a.positions = positions; a.inv_freq = inv_freq; a.rot = (int)rot_dim;
+  a.interleaved = interleaved; a.mscale = mscale; a.slots = slots; a.T = T; a.Hq = Hq; a.Hkv = Hkv;
+  a.D = D; a.fmt = k ? kv_fmt : kKvBf16;
+  if (k) {
+    a.log2_page = __builtin_ctz((unsigned)page_size);
+    a.num_slots = num_pages * page_size;
+  }
+  a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
+  return hip_status(launch_rope_kv_append(a, (hipStream_t)stream));
+}
+
+size_t paged_attn_workspace_size(int64_t T, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                 int64_t max_pages, int32_t page_size, int64_t prefix_len) {
+  if (check_attn_sizes(T, B, Hq, Hkv, D, max_pages, page_size, prefix_len) != BSFP8_OK)
+    return (size_t)-1;
+  if (T == 0 || B == 0) return 0;
+  return attn_plan(T, B, Hq, Hkv, D, max_pages * page_size, prefix_len).bytes;
+}
+
+int32_t paged_attn(const void* q, int64_t ldq, const int32_t* q_start, const int32_t* kv_len,
+                   const int32_t* page_table, int64_t max_pages, const int32_t* prefix_table,
+                   int64_t prefix_len, const void* k_cache, const void* v_cache,
+                   const void* k_scale, const void* v_scale, int32_t kv_fmt, int64_t num_pages,
+                   int32_t page_size, int64_t T, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                   float scale, int64_t window, void* y, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  int32_t r = check_attn_sizes(T, B, Hq, Hkv, D, max_pages, page_size, prefix_len);
+  if (r != BSFP8_OK) return r;
+  if (!(scale > 0.0f) || !(scale <= 1e30f)) return BSFP8_EINVAL;
+  if (window < 0 || !fits_i32(window)) return BSFP8_EINVAL;
+  if (ldq < (int64_t)Hq * D || ldq % 8 != 0) return BSFP8_EINVAL;
+  if (!q_start && T != B) return BSFP8_EINVAL;
+  if (T == 0 || B == 0) return BSFP8_OK;
+  r = check_cache(kv_fmt, num_pages, page_size, k_cache, v_cache, k_scale, v_scale);
+  if (r != BSFP8_OK) return r;
+  if (!q || !kv_len || (max_pages && !page_table) || (prefix_len && !prefix_table) || !y)
+    return BSFP8_EINVAL;
+  if (!al16(q) || !al16(y) || ((uintptr_t)q_start & 3u) || ((uintptr_t)kv_len & 3u) ||
+      ((uintptr_t)page_table & 3u) || ((uintptr_t)prefix_table & 3u))
+    return BSFP8_EINVAL;
+  const AttnPlan p = attn_plan(T, B, Hq, Hkv, D, max_pages * page_size, prefix_len);
+  if (!workspace || ((uintptr_t)workspace & 15u)) return BSFP8_EINVAL;
+  if (workspace_bytes < p.bytes) return BSFP8_ENOSPC;
+  r = check_device(stream);
+  if (r != BSFP8_OK) return r;
+  AttnArgs a{};
+  a.q = (const uint16_t*)q; a.ldq = ldq; a.q_start = q_start; a.kv_len = kv_len;
+  a.table = page_table; a.max_pages = (int)max_pages; a.prefix_table = prefix_table;
+  a.prefix_len = (int)prefix_len;
+  a.kc = (const uint8_t*)k_cache; a.vc = (const uint8_t*)v_cache;
+  a.ks = (const uint8_t*)k_scale; a.vs = (const uint8_t*)v_scale;
+  a.fmt = kv_fmt; a.log2_page = __builtin_ctz((unsigned)page_size);
+  a.num_pages = (int)num_pages;
+  a.T = (int)T; a.B = (int)B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.G = Hq / Hkv;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  a.window = (int)window; a.y = (uint16_t*)y;
+  a.meta = (int2*)workspace;
+  a.ml = (float2*)((char*)workspace + p.off_ml);
+  a.part = (float*)((char*)workspace + p.off_part);
+  a.plan = p;
+  return hip_status(launch_paged_attn(a, (hipStream_t)stream));
 }
 
 int32_t fp8_dequant_weight(const void* wq, int64_t N, int64_t K, int32_t block_n,

@@ -1,0 +1,966 @@
+// Attention of new tokens over a paged cache of keys and values.
+//
+//   y = sum_j e^(s_j) v_j / sum_j e^(s_j),   s_j = scale q . k_j
+//
+// over the keys that a row (a token's query head) sees; 0 where it sees none.
+//
+// Arithmetic.  One pass over the keys in tiles of 32 with a reference
+// exponent r per row: p_j = 2^(s_j log2 e - r), w_j = p_j (v's scale), sums of
+// p_j in fp32, and sums of w_j (v's codes) on the matrix cores.  r is raised to
+// the row's largest log2 w_j only when some w_j passes 2^10, which the first
+// tile does and few others: the sums are rescaled then, and not at every tile.
+// E4M3 codes are exact in bf16 (keys, beside the bf16 query) and in fp16
+// (values); w_j is rounded to fp16, 2^-12 of itself, where a bf16 w_j would lose
+// as much as rounding the output does.  A bf16 value keeps its type, and w_j is
+// the sum of two bf16 numbers then (2^-17 of it lost).
+//
+// Layout.  The score tile is computed transposed, keys x rows: a lane then
+// holds 8 keys of one row, which is what the second product wants of it as an
+// operand once the values' order of summation is that same order.  Nothing
+// goes through LDS, and a row's statistics are exchanged between four lanes.
+// The values' transposition is a byte permutation of what a lane itself loads
+// (8 keys x D/16 values), so that keys and values go from memory to registers
+// to the matrix cores.
+#include "bsfp8_attn.h"
+
+namespace bsfp8 {
+namespace detail {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTile = 32;              // keys of a wave's step
+constexpr int kUnit = 4 * kTile;       // keys of a step of four waves that split them
+constexpr float kLowest = -3.4028234663852886e38f;
+constexpr float kMostW = 1024.0f;      // a larger w raises the reference exponent
+constexpr float kLeastScale = 0x1p-100f;
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) {
+  return v < lo ? lo : (v > hi ? hi : v);
+}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The maximum over the four lanes that share lane % 16.
+__device__ __forceinline__ float group_max(float v) {
+  u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(
+      __float_as_uint(v), __float_as_uint(v), false, false));
+  v = fmaxf(__uint_as_float(a.x), __uint_as_float(a.y));
+  a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(
+      __float_as_uint(v), __float_as_uint(v), false, false));
+  return fmaxf(__uint_as_float(a.x), __uint_as_float(a.y));
+}
+__device__ __forceinline__ float group_sum(float v) {
+  u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(
+      __float_as_uint(v), __float_as_uint(v), false, false));
+  v = __uint_as_float(a.x) + __uint_as_float(a.y);
+  a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(
+      __float_as_uint(v), __float_as_uint(v), false, false));
+  return __uint_as_float(a.x) + __uint_as_float(a.y);
+}
+// The maximum over the 16 lanes of a row of lanes (any sign).
+__device__ __forceinline__ int row16_max(int v) {
+  v = max(v, (int)dpp<kXor1>((uint32_t)v));
+  v = max(v, (int)dpp<kXor2>((uint32_t)v));
+  v = max(v, (int)dpp<kMirror8>((uint32_t)v));
+  return max(v, (int)dpp<kMirror16>((uint32_t)v));
+}
+
+// ------------------------------------------------- sequences, rows, blocks
+
+struct Seq { int q0, n, len; };        // first token, tokens, own cached tokens
+
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+  Seq s;
+  s.q0 = b;
+  s.n = 1;
+  if (a.q_start) {
+    s.q0 = clampi(a.q_start[b], 0, a.T);
+    s.n = clampi(a.q_start[b + 1], s.q0, a.T) - s.q0;
+  }
+  const int64_t room = (int64_t)a.max_pages << a.log2_page;
+  const int len = a.kv_len[b];
+  s.len = len < 0 ? 0 : (len > room ? (int)room : len);
+  return s;
+}
+
+// Own keys that the sequence's first and last token bound: [first, len).
+__device__ __forceinline__ int first_key(const AttnArgs& a, const Seq& s) {
+  if (!a.window) return 0;
+  const int64_t lo = (int64_t)s.len - s.n - a.window + 1;
+  return lo > 0 ? (int)lo : 0;
+}
+__device__ __forceinline__ int units_of(const AttnArgs& a, const Seq& s) {
+  if (s.n == 0 || s.len == 0) return 0;
+  return (s.len + kUnit - 1) / kUnit - first_key(a, s) / kUnit;
+}
+// Number of a sequence's first block among all, with gaps: a bound of what
+// the sequences before it have.
+__device__ __forceinline__ int block_base(const AttnArgs& a, int b, int q0, int rows) {
+  return (int)((int64_t)q0 * a.G / rows) + b;
+}
+
+// The sequence of a token, -1 for none.  One lane's search.
+__device__ __forceinline__ int seq_of_token(const AttnArgs& a, int t) {
+  if (!a.q_start) return t;
+  int lo = 0, hi = a.B;                // q_start[lo] <= t < q_start[hi], if in any
+  if (t < a.q_start[0] || t >= a.q_start[a.B]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.q_start[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// What a row block works on: rows row0 .. row0 + rows of the sequence (or,
+// of the prefix, of all tokens), key head h, keys of a table.
+struct Block {
+  int q0;                    // token of row 0
+  int row0, rows;
+  int h;
+  const int32_t* table;
+  int keys;                  // of the table
+  int pre;                   // 1: the prefix's keys
+  int n, len;                // the sequence's (own blocks)
+};
+
+// ----------------------------------------------------------- a wave's rows
+
+template <int KV, int D, int RT>
+struct Wave {
+  static constexpr bool F8 = KV != kKvBf16;
+  static constexpr int ES = F8 ? 1 : 2;            // bytes of a cached value
+  static constexpr int KQ = D * 16 * ES / 1024;    // 16-byte pieces of a lane's 16-key part
+  static constexpr int DPL = D / 16;               // values of a key that a lane holds
+  static constexpr int VW = DPL * ES / 4;          // dwords of them
+
+  struct Raw {
+    uint4 k[2][KQ];
+    uint32_t v[8][VW];
+    float ks[8], vs[8];
+    int id[2];               // page ids, -1: none
+  };
+
+  const AttnArgs& a;
+  bf16x8 q[RT][D / 32];
+  v4f o[RT][DPL];
+  float ref[RT], sum[RT];
+  int lo[RT], hi[RT];        // the lane's row's visible keys
+  int lo_most, lo_least, hi_least, hi_most;        // over the wave's rows
+  int lane, n, g;
+
+  __device__ __forceinline__ explicit Wave(const AttnArgs& args) : a(args) {
+    lane = threadIdx.x & 63;
+    n = lane & 15;
+    g = lane >> 4;
+  }
+
+  // Queries and visible keys of rows row0 + 16 rt + n of the block.
+  __device__ __forceinline__ void begin(const Block& b, int row0) {
+    int lom = 0, lol = 0x7fffffff, hil = 0x7fffffff, him = 0;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = row0 + 16 * rt + n;
+      const bool live = r < b.rows;
+      const int i = live ? (b.row0 + r) / a.G : 0;
+      const int head = b.h * a.G + (b.row0 + r - i * a.G);
+      lo[rt] = hi[rt] = 0;
+      if (live) {
+        if (!b.pre) {
+          const int pos = b.len - b.n + i;         // among the own keys
+          hi[rt] = clampi(pos + 1, 0, b.keys);
+          if (a.window) lo[rt] = (int)max((int64_t)pos - a.window + 1, (int64_t)0);
+        } else {
+          const int s = seq_of_token(a, i);
+          if (s >= 0) {
+            const Seq sq = seq_of(a, s);
+            const int64_t pos = (int64_t)a.prefix_len + sq.len - sq.n + (i - sq.q0);
+            hi[rt] = (int)min(max(pos + 1, (int64_t)0), (int64_t)b.keys);
+            if (a.window)
+              lo[rt] = (int)min(max(pos - a.window + 1, (int64_t)0), (int64_t)b.keys);
+          }
+        }
+        lom = max(lom, lo[rt]);
+        lol = min(lol, lo[rt]);
+        hil = min(hil, hi[rt]);
+        him = max(him, hi[rt]);
+      }
+      const uint16_t* src = a.q + (int64_t)(b.q0 + i) * a.ldq + (int64_t)head * D;
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) {
+        const int d = F8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) v = *(const uint4*)(src + d);
+        q[rt][s] = __builtin_bit_cast(bf16x8, v);
+      }
+#pragma unroll
+      for (int t = 0; t < DPL; ++t) o[rt][t] = v4f{0, 0, 0, 0};
+      ref[rt] = kLowest;
+      sum[rt] = 0.0f;
+    }
+    lo_most = uniform(row16_max(lom));
+    lo_least = -uniform(row16_max(-lol));
+    hi_least = -uniform(row16_max(-hil));
+    hi_most = uniform(row16_max(him));
+  }
+
+  // Page ids of the 32 tiles tile0, tile0 + step, ..: lane 2 i + s has that
+  // of keys 16 s .. of the i-th one.
+  __device__ __forceinline__ int page_ids(const Block& b, int tile0, int step) const {
+    const int64_t key = ((int64_t)tile0 + (int64_t)(lane >> 1) * step) * kTile + 16 * (lane & 1);
+    int id = -1;
+    if (key < b.keys) {
+      id = b.table[key >> a.log2_page];
+      if (id < 0 || id >= a.num_pages) id = -1;
+    }
+    return id;
+  }
+
+  __device__ __forceinline__ void load(const Block& b, int tile, int id0, int id1, Raw& x) const {
+    const int in_page = (1 << a.log2_page) - 1;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int id = s ? id1 : id0;
+      x.id[s] = id;
+      // keys without a page: those of page 0 are loaded and not used
+      const int64_t row = (((int64_t)(id < 0 ? 0 : id) * a.Hkv + b.h) << a.log2_page) +
+                          ((tile * kTile + 16 * s) & in_page);
+      const uint8_t* kp = a.kc + row * (D * ES);
+      const uint8_t* vp = a.vc + row * (D * ES);
+#pragma unroll
+      for (int i = 0; i < KQ; ++i)
+        x.k[s][i] = ld_stream16(kp + (uint32_t)(n * (D * ES) + 64 * i + 16 * g));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* p = vp + (uint32_t)((4 * g + j) * (D * ES) + n * (DPL * ES));
+        uint32_t* v = x.v[4 * s + j];
+        if constexpr (VW == 1) {
+          v[0] = __builtin_nontemporal_load((const uint32_t*)p);
+        } else if constexpr (VW == 2) {
+          const u32x2 w = __builtin_nontemporal_load((const u32x2*)p);
+          v[0] = w.x;
+          v[1] = w.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < VW; i += 4) {
+            const uint4 w = ld_stream16(p + 4 * i);
+            v[i] = w.x;
+            v[i + 1] = w.y;
+            v[i + 2] = w.z;
+            v[i + 3] = w.w;
+          }
+        }
+      }
+      if constexpr (KV == kKvFloat) {
+        const float4 e = *(const float4*)(a.ks + 4 * row + 16 * g);
+        const float4 f = *(const float4*)(a.vs + 4 * row + 16 * g);
+        x.ks[4 * s] = e.x; x.ks[4 * s + 1] = e.y; x.ks[4 * s + 2] = e.z; x.ks[4 * s + 3] = e.w;
+        x.vs[4 * s] = f.x; x.vs[4 * s + 1] = f.y; x.vs[4 * s + 2] = f.z; x.vs[4 * s + 3] = f.w;
+      } else if constexpr (KV == kKvUe8m0) {
+        const uint32_t e = *(const uint32_t*)(a.ks + row + 4 * g);
+        const uint32_t f = *(const uint32_t*)(a.vs + row + 4 * g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x.ks[4 * s + j] = e8m0_f32((e >> (8 * j)) & 255u);
+          x.vs[4 * s + j] = e8m0_f32((f >> (8 * j)) & 255u);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ static bf16x8 key_operand(uint2 c) {
+    if constexpr (F8) {
+      const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, 1.0f, false);
+      const bf16x2 f = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, 1.0f, true);
+      const bf16x2 i = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, false);
+      const bf16x2 j = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, true);
+      return bf16x8{e[0], e[1], f[0], f[1], i[0], i[1], j[0], j[1]};
+    }
+    return bf16x8{};
+  }
+
+  // A code or value that is not finite: its mark in each byte or half.
+  __device__ __forceinline__ static uint32_t odd_marks(uint32_t v) {
+    if (F8) return ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    return ((v & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+  }
+
+  // Values that are not finite in a tile that some rows see only part of:
+  // they are taken out of the tile (0 w would not be 0) and added, one by one,
+  // to the rows that see them.
+  __device__ __forceinline__ void odd_values(const Block& b, int tile, Raw& x,
+                                             const float (&w)[RT][8], const uint32_t (&seen)[RT]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        const uint32_t m = odd_marks(x.v[j][i]);
+        x.v[j][i] &= ~((m >> (F8 ? 7 : 15)) * (F8 ? 0xffu : 0xffffu));
+      }
+    const int in_page = (1 << a.log2_page) - 1;
+    for (int k = 0; k < kTile; ++k) {
+      const int s = k >> 4, j = (k & 3) + 4 * s, from = ((k >> 2) & 3) * 16 + n;
+      const int id = s ? x.id[1] : x.id[0];
+      if (id < 0) continue;
+      const int64_t row = (((int64_t)id * a.Hkv + b.h) << a.log2_page) + ((tile * kTile + k) & in_page);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        float mine = w[rt][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mine = i == j ? w[rt][i] : mine;
+        const float wk = __shfl(mine, from);
+        const bool sees = (__shfl((int)seen[rt], from) >> j) & 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < DPL; ++t) {
+            const int64_t at = row * D + DPL * (4 * g + i) + t;
+            float val = 0.0f;
+            bool odd;
+            if (F8) {
+              odd = (a.vc[at] & 0x7fu) == 0x7fu;
+              if (odd) val = __uint_as_float(0x7fc00000u);
+            } else {
+              const uint32_t bits = ((const uint16_t*)a.vc)[at];
+              odd = (bits & 0x7f80u) == 0x7f80u;
+              val = __uint_as_float(bits << 16);
+            }
+            if (sees && odd) o[rt][t][i] += wk * val;
+          }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void tile(const Block& b, int tile, Raw& x) {
+    const int key0 = tile * kTile;
+    if (key0 >= hi_most || key0 + kTile <= lo_least) return;
+    const bool whole = x.id[0] >= 0 && x.id[1] >= 0 && key0 >= lo_most && key0 + kTile <= hi_least;
+
+    v4f s[RT][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        bf16x8 k;
+        if constexpr (F8) {
+          const uint4 c = x.k[h][i / 2];
+          k = key_operand(i % 2 ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y));
+        } else {
+          k = __builtin_bit_cast(bf16x8, x.k[h][i]);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[rt][i], s[rt][h], 0, 0, 0);
+      }
+
+    float ksl[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ksl[j] = F8 ? x.ks[j] * a.scale_log2 : a.scale_log2;
+
+    float w[RT][8];
+    uint32_t seen[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      seen[rt] = 0xffu;
+      if (!whole) {
+        seen[rt] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
+          const bool ok = x.id[j >> 2] >= 0 && key >= lo[rt] && key < hi[rt];
+          seen[rt] |= (uint32_t)ok << j;
+        }
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float p[8];
+      auto weigh = [&]() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(fmaf(s[rt][j >> 2][j & 3], ksl[j], -ref[rt]));
+          w[rt][j] = F8 ? p[j] * x.vs[j] : p[j];
+        }
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const bool ok = (seen[rt] >> j) & 1;
+            p[j] = ok ? p[j] : 0.0f;
+            w[rt][j] = ok ? w[rt][j] : 0.0f;
+          }
+        }
+      };
+      weigh();
+      float most = w[rt][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) most = fmaxf(most, w[rt][j]);
+      if (__any(!(most <= kMostW))) {
+        float top = kLowest;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float e = s[rt][j >> 2][j & 3] * ksl[j];
+          if (F8) e += __builtin_amdgcn_logf(fmaxf(x.vs[j], kLeastScale));
+          if ((seen[rt] >> j) & 1) top = fmaxf(top, e);
+        }
+        top = fmaxf(ref[rt], group_max(top));
+        const float down = __builtin_amdgcn_exp2f(ref[rt] - top);
+        ref[rt] = top;
+        sum[rt] *= down;
+#pragma unroll
+        for (int t = 0; t < DPL; ++t) o[rt][t] *= down;
+        weigh();
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[rt] += p[j];
+    }
+
+    if (!whole) {
+      // keys that no row sees may hold anything
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
+        const bool ok = x.id[j >> 2] >= 0 && key >= lo_least && key < hi_most;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) x.v[j][i] = ok ? x.v[j][i] : 0;
+      }
+      if (lo_least != lo_most || hi_least != hi_most) {
+        uint32_t marks = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < VW; ++i) marks |= odd_marks(x.v[j][i]);
+        if (__any(marks != 0)) odd_values(b, tile, x, w, seen);
+      }
+    }
+
+    if constexpr (F8) {
+      f16x8 wq[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const f16x2 c = __builtin_convertvector((f32x2{w[rt][j], w[rt][j + 1]}), f16x2);
+          wq[rt][j] = c[0];
+          wq[rt][j + 1] = c[1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VW; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t c[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            c[j] = __builtin_bit_cast(uint32_t, h ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.v[j][i], 1.0f, true)
+                                                  : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.v[j][i], 1.0f, false));
+          u32x4 e, f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x05040100u);
+            f[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x07060302u);
+          }
+          const int t = 4 * i + 2 * h;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, e), wq[rt], o[rt][t], 0, 0, 0);
+            o[rt][t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, f), wq[rt], o[rt][t + 1], 0, 0, 0);
+          }
+        }
+    } else {
+      bf16x8 wh[RT], wl[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const bf16x2 c = __builtin_convertvector((f32x2{w[rt][j], w[rt][j + 1]}), bf16x2);
+          const bf16x2 d = __builtin_convertvector((f32x2{w[rt][j] - (float)c[0], w[rt][j + 1] - (float)c[1]}), bf16x2);
+          wh[rt][j] = c[0];
+          wh[rt][j + 1] = c[1];
+          wl[rt][j] = d[0];
+          wl[rt][j + 1] = d[1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        u32x4 e, f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          e[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][i], x.v[2 * j][i], 0x05040100u);
+          f[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][i], x.v[2 * j][i], 0x07060302u);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          v4f& u = o[rt][2 * i];
+          v4f& v = o[rt][2 * i + 1];
+          u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wh[rt], u, 0, 0, 0);
+          v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wh[rt], v, 0, 0, 0);
+          u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wl[rt], u, 0, 0, 0);
+          v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wl[rt], v, 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  // Tiles first, first + step, .. below end.
+  __device__ __forceinline__ void walk(const Block& b, int first, int end, int step) {
+    const int count = end > first ? (end - first + step - 1) / step : 0;
+    Raw x, z;
+    int ids = 0;
+    auto fetch = [&](int i, Raw& r) {
+      if (i >= count) return;
+      if (i % 32 == 0) ids = page_ids(b, first + i * step, step);
+      const int at = 2 * (i % 32);
+      load(b, first + i * step, __builtin_amdgcn_readlane(ids, at),
+           __builtin_amdgcn_readlane(ids, at + 1), r);
+    };
+    fetch(0, x);
+    for (int i = 0; i < count; i += 2) {
+      fetch(i + 1, z);
+      tile(b, first + i * step, x);
+      fetch(i + 2, x);
+      if (i + 1 < count) tile(b, first + (i + 1) * step, z);
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) sum[rt] = group_sum(sum[rt]);
+  }
+
+  // The lane's 4 DPL values of a row: y, or a partial result.
+  __device__ __forceinline__ void out_row(const Block& b, int row0, int rt, int64_t slot,
+                                          int block_rows, bool direct) const {
+    const int r = row0 + 16 * rt + n;
+    if (r >= b.rows) return;
+    if (direct) {
+      const int i = (b.row0 + r) / a.G;
+      const int head = b.h * a.G + (b.row0 + r - i * a.G);
+      const float f = sum[rt] == 0.0f ? 0.0f : 1.0f / sum[rt];
+      uint16_t* y = a.y + ((int64_t)(b.q0 + i) * a.Hq + head) * D + 4 * DPL * g;
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) {
+        uint32_t c[DPL / 2];
+#pragma unroll
+        for (int t = 0; t < DPL; t += 2)
+          c[t / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
+              (f32x2{o[rt][t][i4] * f, o[rt][t + 1][i4] * f}), bf16x2));
+        uint16_t* p = y + DPL * i4;
+        if constexpr (DPL == 4) *(uint2*)p = make_uint2(c[0], c[1]);
+        else
+#pragma unroll
+          for (int t = 0; t < DPL / 2; t += 4) *(uint4*)(p + 2 * t) = make_uint4(c[t], c[t + 1], c[t + 2], c[t + 3]);
+      }
+    } else {
+      const int64_t at = slot * block_rows + r;
+      if (g == 0) a.ml[at] = make_float2(ref[rt], sum[rt]);
+      float* p = a.part + at * D + 4 * DPL * g;
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4)
+#pragma unroll
+        for (int t = 0; t < DPL; t += 4)
+          *(float4*)(p + DPL * i4 + t) = make_float4(o[rt][t][i4], o[rt][t + 1][i4], o[rt][t + 2][i4], o[rt][t + 3][i4]);
+    }
+  }
+};
+
+// ------------------------------------------ few rows: four waves split keys
+
+// All (sequence, block of 16 rows, key head) in a row, each its units of 128
+// keys; every workgroup takes as many consecutive units as the others.  The
+// lengths are read from the device, so that one launch shape (and one graph)
+// serves them all.  The prefix, where its rows are few too, comes last, as a
+// sequence of its own whose rows are all tokens'.
+template <int KV, int D>
+__global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
+  constexpr int DPL = D / 16;
+  __shared__ int before[kAttnMaxSeqs + 2];
+  __shared__ int wave_total[4];
+  __shared__ float merge[2][16][D + 4];
+  __shared__ float2 merge_ml[2][16];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const bool pre = a.prefix_len > 0 && !a.plan.pre_wide;
+  const int items = a.B + (pre ? 1 : 0);
+  const int pre_blocks = (int)(((int64_t)a.T * a.G + 15) / 16);
+  const int pre_units = (a.prefix_len + kUnit - 1) / kUnit;
+
+  int total = 0;
+  for (int base = 0; base < items; base += 256) {
+    const int b = base + tid;
+    int v = 0;
+    if (b < a.B) {
+      const Seq s = seq_of(a, b);
+      v = units_of(a, s) * ((s.n * a.G + 15) / 16) * a.Hkv;
+    } else if (b < items) {
+      v = pre_units * pre_blocks * a.Hkv;
+    }
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(incl, d);
+      if (lane >= d) incl += u;
+    }
+    if (lane == 63) wave_total[wave] = incl;
+    __syncthreads();
+    int add = total;
+    for (int i = 0; i < wave; ++i) add += wave_total[i];
+    if (b < items) before[b] = add + incl - v;
+    total += wave_total[0] + wave_total[1] + wave_total[2] + wave_total[3];
+    __syncthreads();
+  }
+  if (tid == 0) before[items] = total;
+  __syncthreads();
+  total = uniform(total);
+
+  const int groups = a.plan.own_groups;
+  const int per = total / groups + (total % groups ? 1 : 0);
+  if (per <= 0) return;
+  int x = (int)min((int64_t)blockIdx.x * per, (int64_t)total);
+  const int xe = (int)min((int64_t)x + per, (int64_t)total);
+  if (x >= xe) return;
+  int b = 0;
+  {
+    int hi = items;                      // before[b] <= x < before[hi]
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (before[mid] <= x) b = mid;
+      else hi = mid;
+    }
+    b = uniform(b);
+  }
+
+  Wave<KV, D, 1> w(a);
+  while (x < xe) {
+    while (b + 1 < items && uniform(before[b + 1]) <= x) ++b;
+    Block k;
+    int unit0, units, id;
+    const int rel = x - uniform(before[b]);
+    int part;
+    if (b < a.B) {
+      Seq s = seq_of(a, b);
+      s.q0 = uniform(s.q0);
+      s.n = uniform(s.n);
+      s.len = uniform(s.len);
+      units = units_of(a, s);
+      unit0 = first_key(a, s) / kUnit;
+      part = rel / units;
+      const int j = part / a.Hkv;
+      k.q0 = s.q0;
+      k.row0 = 16 * j;
+      k.rows = min(16, s.n * a.G - 16 * j);
+      k.h = part - j * a.Hkv;
+      k.table = a.table + (int64_t)b * a.max_pages;
+      k.keys = s.len;
+      k.pre = 0;
+      k.n = s.n;
+      k.len = s.len;
+      id = (block_base(a, b, s.q0, 16) + j) * a.Hkv + k.h;
+    } else {
+      units = pre_units;
+      unit0 = 0;
+      part = rel / units;
+      const int j = part / a.Hkv;
+      k.q0 = 0;
+      k.row0 = 16 * j;
+      k.rows = (int)min((int64_t)16, (int64_t)a.T * a.G - 16 * j);
+      k.h = part - j * a.Hkv;
+      k.table = a.prefix_table;
+      k.keys = a.prefix_len;
+      k.pre = 1;
+      k.n = k.len = 0;
+      id = (a.plan.own_blocks + j) * a.Hkv + k.h;
+    }
+    const int u = rel - part * units;
+    const int ue = min(units, u + (xe - x));
+    const int w0 = (x - u) / per, w1 = (x - u + units - 1) / per;
+    const bool direct = w0 == w1 && a.prefix_len == 0;
+    const int64_t slot = (int64_t)blockIdx.x + id;
+    if (u == 0 && tid == 0) a.meta[id] = make_int2(w0 + id, direct ? -1 : w1 - w0 + 1);
+
+    w.begin(k, 0);
+    w.walk(k, (unit0 + u) * 4 + wave, (unit0 + ue) * 4, 4);
+
+    // the waves' sums in two steps: 2 and 3 to 0 and 1, then 1 to 0
+#pragma unroll
+    for (int step = 2; step; step >>= 1) {
+      if (wave >= step && wave < 2 * step) {
+        float* m = merge[wave - step][w.n];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < DPL; t += 4)
+            *(float4*)(m + DPL * (4 * w.g + i) + t) =
+                make_float4(w.o[0][t][i], w.o[0][t + 1][i], w.o[0][t + 2][i], w.o[0][t + 3][i]);
+        if (w.g == 0) merge_ml[wave - step][w.n] = make_float2(w.ref[0], w.sum[0]);
+      }
+      __syncthreads();
+      if (wave < step) {
+        const float* m = merge[wave][w.n];
+        const float2 e = merge_ml[wave][w.n];
+        const float top = fmaxf(w.ref[0], e.x);
+        const float f0 = __builtin_amdgcn_exp2f(w.ref[0] - top), f1 = __builtin_amdgcn_exp2f(e.x - top);
+        w.ref[0] = top;
+        w.sum[0] = w.sum[0] * f0 + e.y * f1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < DPL; t += 4) {
+            const float4 c = *(const float4*)(m + DPL * (4 * w.g + i) + t);
+            w.o[0][t][i] = w.o[0][t][i] * f0 + c.x * f1;
+            w.o[0][t + 1][i] = w.o[0][t + 1][i] * f0 + c.y * f1;
+            w.o[0][t + 2][i] = w.o[0][t + 2][i] * f0 + c.z * f1;
+            w.o[0][t + 3][i] = w.o[0][t + 3][i] * f0 + c.w * f1;
+          }
+      }
+      __syncthreads();
+    }
+    if (wave == 0) w.out_row(k, 0, 0, slot, 16, direct);
+    x += ue - u;
+  }
+}
+
+// --------------------------------------------- many rows: a wave has its own
+
+// A workgroup takes 64 RT rows of a block and key head; every wave walks all of
+// its split of the keys.  PRE: the blocks are of all tokens, the keys the
+// prefix's.
+template <int KV, int D, int RT, bool PRE>
+__global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
+  constexpr int ROWS = 64 * RT;
+  __shared__ int found[4];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int splits = PRE ? a.plan.pre_splits : a.plan.own_splits;
+  const int blocks = PRE ? a.plan.pre_blocks : a.plan.own_blocks;
+  const int64_t wg = grid_row();
+  if (wg >= (int64_t)blocks * splits * a.Hkv) return;
+  Block k;
+  k.h = (int)(wg % a.Hkv);
+  const int64_t rest = wg / a.Hkv;
+  const int split = (int)(rest % splits);
+  const int blk = blocks - 1 - (int)(rest / splits);   // a sequence's last block has the most keys
+  int first = 0, end;
+  if constexpr (PRE) {
+    k.q0 = 0;
+    k.row0 = blk * ROWS;
+    k.rows = (int)min((int64_t)ROWS, (int64_t)a.T * a.G - k.row0);
+    k.table = a.prefix_table;
+    k.keys = a.prefix_len;
+    k.pre = 1;
+    k.n = k.len = 0;
+    end = (k.keys + kTile - 1) / kTile;
+  } else {
+    int count = 0;                     // sequences whose blocks begin at or before this one
+    for (int b = threadIdx.x; b < a.B; b += 256) {
+      const int q0 = a.q_start ? clampi(a.q_start[b], 0, a.T) : b;
+      count += block_base(a, b, q0, ROWS) <= blk;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d);
+    if (lane == 0) found[wave] = count;
+    __syncthreads();
+    const int b = uniform(found[0] + found[1] + found[2] + found[3]) - 1;
+    if (b < 0) return;
+    Seq s = seq_of(a, b);
+    const int j = blk - block_base(a, b, s.q0, ROWS);
+    if (j < 0 || (int64_t)j * ROWS >= (int64_t)s.n * a.G) return;
+    k.q0 = s.q0;
+    k.row0 = j * ROWS;
+    k.rows = min(ROWS, s.n * a.G - k.row0);
+    k.table = a.table + (int64_t)b * a.max_pages;
+    k.keys = s.len;
+    k.pre = 0;
+    k.n = s.n;
+    k.len = s.len;
+    const int pos0 = s.len - s.n + k.row0 / a.G, pos1 = s.len - s.n + (k.row0 + k.rows - 1) / a.G;
+    end = (clampi(pos1 + 1, 0, s.len) + kTile - 1) / kTile;
+    if (a.window) first = (int)(max((int64_t)pos0 - a.window + 1, (int64_t)0) / kTile);
+  }
+  const int tiles = max(end - first, 0);
+  const int per = (tiles + splits - 1) / splits;
+  const int parts = per ? (tiles + per - 1) / per : 0;
+  const int id = (PRE ? a.plan.own_blocks + blk : blk) * a.Hkv + k.h;
+  const int64_t slot = ((int64_t)blk * a.Hkv + k.h) * splits + split + (PRE ? a.plan.own_slots * a.plan.own_rows / ROWS : 0);
+  const bool direct = !PRE && parts <= 1 && a.prefix_len == 0;
+  if (split == 0 && threadIdx.x == 0)
+    a.meta[id] = make_int2((int)slot, direct ? -1 : parts);
+  if (split >= parts && !(direct && split == 0)) return;
+  const int row0 = wave * 16 * RT;
+  if (row0 >= k.rows) return;
+  Wave<KV, D, RT> w(a);
+  w.begin(k, row0);
+  w.walk(k, first + split * per, min(first + (split + 1) * per, end), 1);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) w.out_row(k, row0, rt, slot, ROWS, direct);
+}
+
+// ------------------------------------------------------------ joined results
+
+// A row's partial results (of its own keys, of the prefix) to y.  WPR waves
+// per row.
+template <int D, int WPR>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  constexpr int LPR = D / 4, SUB = 64 / LPR;       // lanes of a partial row, rows at once
+  constexpr int RPB = 4 / WPR;
+  __shared__ float4 acc[4][64];
+  __shared__ float accl[4][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t row = grid_row() * RPB + wave / WPR;
+  if (row >= (int64_t)a.T * a.Hq) return;          // WPR = 4: the whole workgroup
+  const int t = uniform((int)(row / a.Hq)), head = uniform((int)(row - (int64_t)t * a.Hq));
+  const int h = head / a.G, gq = head - h * a.G;
+  int b = t;
+  if (a.q_start) {
+    int count = 0;                     // sequences that end at or before the token
+    for (int i = lane; i < a.B; i += 64) count += a.q_start[i + 1] <= t;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d);
+    b = uniform(count);
+    if (b >= a.B || t < a.q_start[b]) return;
+  }
+  const Seq s = seq_of(a, b);
+  if (t >= s.q0 + s.n) return;
+  const int local = (t - s.q0) * a.G + gq;
+  const int orows = a.plan.own_rows, prows = a.plan.pre_rows;
+  int c0 = 0, c1 = 0;
+  int64_t f0 = 0, f1 = 0;              // the first partial's rows
+  if (s.len > 0) {
+    const int id = (block_base(a, b, s.q0, orows) + local / orows) * a.Hkv + h;
+    const int2 m = a.meta[id];
+    if (m.y < 0) return;               // written already
+    c0 = uniform(m.y);
+    f0 = (int64_t)uniform(m.x) * orows + local % orows;
+  }
+  if (a.prefix_len > 0) {
+    const int64_t all = (int64_t)t * a.G + gq;
+    const int2 m = a.meta[(a.plan.own_blocks + (int)(all / prows)) * a.Hkv + h];
+    c1 = uniform(m.y);
+    f1 = (int64_t)uniform(m.x) * prows + all % prows;
+  }
+  const int count = c0 + c1;
+  auto place = [&](int i) { return i < c0 ? f0 + (int64_t)i * orows : f1 + (int64_t)(i - c0) * prows; };
+  float top = kLowest;
+  for (int i = lane; i < count; i += 64) top = fmaxf(top, a.ml[place(i)].x);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const int sub = lane / LPR + SUB * (wave % WPR), d4 = lane % LPR;
+  float4 o = make_float4(0, 0, 0, 0);
+  float l = 0.0f;
+  for (int i = sub; i < count; i += SUB * WPR) {
+    const int64_t at = place(i);
+    const float2 e = a.ml[at];
+    const float4 c = *(const float4*)(a.part + at * D + 4 * d4);
+    const float f = __builtin_amdgcn_exp2f(e.x - top);
+    l += e.y * f;
+    o.x += c.x * f;
+    o.y += c.y * f;
+    o.z += c.z * f;
+    o.w += c.w * f;
+  }
+#pragma unroll
+  for (int d = LPR; d < 64; d <<= 1) {
+    l += __shfl_xor(l, d);
+    o.x += __shfl_xor(o.x, d);
+    o.y += __shfl_xor(o.y, d);
+    o.z += __shfl_xor(o.z, d);
+    o.w += __shfl_xor(o.w, d);
+  }
+  if constexpr (WPR > 1) {
+    acc[wave][lane] = o;
+    accl[wave][lane] = l;
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) {
+      const float4 c = acc[i][lane];
+      l += accl[i][lane];
+      o.x += c.x;
+      o.y += c.y;
+      o.z += c.z;
+      o.w += c.w;
+    }
+  }
+  if (lane >= LPR) return;
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+  const bf16x2 lo = __builtin_convertvector((f32x2{o.x * f, o.y * f}), bf16x2);
+  const bf16x2 hi = __builtin_convertvector((f32x2{o.z * f, o.w * f}), bf16x2);
+  *(uint2*)(a.y + row * D + 4 * d4) = make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+}
+
+template <int KV, int D>
+hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
+  constexpr int RT = attn_row_tiles(D);
+  const AttnPlan& p = a.plan;
+  if (p.pre_wide)
+    hipLaunchKernelGGL((attn_rows_kernel<KV, D, RT, true>),
+                       row_grid((int64_t)p.pre_blocks * p.pre_splits * a.Hkv), dim3(256), 0, s, a);
+  if (p.own_wide)
+    hipLaunchKernelGGL((attn_rows_kernel<KV, D, RT, false>),
+                       row_grid((int64_t)p.own_blocks * p.own_splits * a.Hkv), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_split_kernel<KV, D>), dim3(p.own_groups), dim3(256), 0, s, a);
+  const int64_t rows = (int64_t)a.T * a.Hq;
+  if (rows <= 2048)
+    hipLaunchKernelGGL((attn_join_kernel<D, 4>), row_grid(rows), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<D, 1>), row_grid((rows + 3) / 4), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int KV>
+hipError_t launch_attn_d(const AttnArgs& a, hipStream_t s) {
+  if (a.D == 64) return launch_attn<KV, 64>(a, s);
+  if (a.D == 128) return launch_attn<KV, 128>(a, s);
+  return launch_attn<KV, 256>(a, s);
+}
+
+}  // namespace detail
+using namespace detail;
+
+AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, int64_t prefix_len) {
+  AttnPlan p{};
+  const int64_t G = Hq / Hkv, rows = T * G;
+  const int wide = 64 * attn_row_tiles(D);
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  auto splits = [&](int64_t blocks, int64_t most) {
+    const int64_t want = up(1024, blocks * Hkv), tiles = up(most, 8 * kTile);
+    return (int)(want < tiles ? want : (tiles > 1 ? tiles : 1));
+  };
+  p.own_wide = rows > 32 * B;
+  p.pre_wide = prefix_len > 0 && (p.own_wide || rows > 32);
+  p.own_rows = p.own_wide ? wide : 16;
+  p.pre_rows = p.pre_wide ? wide : 16;
+  p.own_blocks = (int)(rows / p.own_rows + B);
+  p.pre_blocks = prefix_len > 0 ? (int)up(rows, p.pre_rows) : 0;
+  if (p.own_wide) {
+    p.own_splits = splits(p.own_blocks, keys);
+    p.own_slots = (int64_t)p.own_blocks * Hkv * p.own_splits;
+  } else {
+    const int64_t own = up(keys, kUnit) * (rows / 16 + B) * Hkv;
+    const int64_t pre = p.pre_wide ? 0 : up(prefix_len, kUnit) * p.pre_blocks * Hkv;
+    const int64_t most = own + pre > 0 ? own + pre : 1;
+    p.own_groups = (int)(most < 768 ? most : 768);
+    p.own_slots = p.own_groups + (int64_t)(p.own_blocks + (p.pre_wide ? 0 : p.pre_blocks)) * Hkv;
+  }
+  if (p.pre_wide) {
+    p.pre_splits = splits(p.pre_blocks, prefix_len);
+    p.pre_slots = (int64_t)p.pre_blocks * Hkv * p.pre_splits;
+    // the prefix's partials begin at a whole block of theirs
+    p.own_slots = up(p.own_slots * p.own_rows, p.pre_rows) * p.pre_rows / p.own_rows;
+  }
+  auto aligned = [](size_t v) { return (v + 255) & ~size_t(255); };
+  const int64_t prow = p.own_slots * p.own_rows + p.pre_slots * p.pre_rows;
+  p.off_ml = aligned((size_t)(p.own_blocks + p.pre_blocks) * Hkv * sizeof(int2));
+  p.off_part = p.off_ml + aligned((size_t)prow * sizeof(float2));
+  p.bytes = p.off_part + (size_t)prow * D * sizeof(float);
+  return p;
+}
+
+hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s) {
+  if (a.fmt == kKvFloat) return launch_attn_d<kKvFloat>(a, s);
+  if (a.fmt == kKvUe8m0) return launch_attn_d<kKvUe8m0>(a, s);
+  return launch_attn_d<kKvBf16>(a, s);
+}
+
+}  // namespace bsfp8

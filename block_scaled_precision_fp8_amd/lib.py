@@ -23,6 +23,8 @@ OP_BLOCK_GEMM, OP_LINEAR, OP_GROUPED_GEMM, OP_FP4_QUANT, OP_FP4_GEMM, OP_FP8_FP4
 OP_LINEAR_B32 = 6
 OP_MOE_DECODE = 7
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+KV_FP8_FLOAT, KV_FP8_UE8M0, KV_BF16 = 0, 1, 2
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BY_PARTS = 0, 1, 2
 GEMM_NONE, GEMM_TILE_128x256, GEMM_TILE_256x256, GEMM_DECODE = 0, 2, 3, 4
 
 EXPORTS = ("bsfp8_version", "bsfp8_status_string", "bsfp8_workspace_size", "bsfp8_gemm_kernel",
@@ -30,7 +32,8 @@ EXPORTS = ("bsfp8_version", "bsfp8_status_string", "bsfp8_workspace_size", "bsfp
            "fp8_grouped_gemm", "fp4_quant", "fp4_group_gemm", "fp8_dequant_weight",
            "fp8_scale_to_ue8m0", "mxfp4_quant_weight", "fp8_fp4_gemm",
            "fp8_grouped_gemm_silu_mul_quant", "fp8_linear_noalloc", "fp8_fp4_grouped_gemm",
-           "fp8_add_rmsnorm_quant", "moe_route_topk", "fp8_moe_decode", "fp8_fp4_moe_decode")
+           "fp8_add_rmsnorm_quant", "moe_route_topk", "fp8_moe_decode", "fp8_fp4_moe_decode",
+           "rope_inv_freq", "rope_kv_append", "paged_attn", "paged_attn_workspace_size")
 NOALLOC_SCRATCH_BYTES = 32 << 20     # BSFP8_NOALLOC_SCRATCH_BYTES
 
 
@@ -44,6 +47,7 @@ _lib = None
 
 _P = ctypes.c_void_p
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
@@ -78,6 +82,12 @@ _SIGS = {
                               _I32, _I32, _P, _SZ, _P]),
     "fp8_fp4_moe_decode": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64,
                                   _I32, _I32, _P, _SZ, _P]),
+    "rope_inv_freq": (_I32, [_I32, _I64, _F64, _F64, _F64, _F64, _F64, _P, _P]),
+    "rope_kv_append": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _F32, _P,
+                              _I64, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P]),
+    "paged_attn": (_I32, [_P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _I32, _I64, _I32,
+                          _I64, _I64, _I32, _I32, _I32, _F32, _I64, _P, _P, _SZ, _P]),
+    "paged_attn_workspace_size": (_SZ, [_I64, _I64, _I32, _I32, _I32, _I64, _I32, _I64]),
     "fp4_quant": (_I32, [_P, _I64, _I64, _I32, _P, _P, _P, _P, _SZ, _P]),
     "fp4_group_gemm": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
 }
@@ -102,11 +112,13 @@ def load(path=None):
     global _device, _raw_stream
     _device = getattr(torch._C, "_cuda_getDevice", _device)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-    global _BF16, _FP32, _INT32, _BF16S, _FP32S, _BYTES, _CODES, _SCALES
+    global _BF16, _FP32, _INT32, _BF16S, _FP32S, _BYTES, _CODES, _SCALES, _INT32S, _INT64S, _CACHES
     _BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
+    _INT32S, _INT64S = (_INT32,), (torch.int64,)
     _BF16S, _FP32S, _BYTES = (_BF16,), (_FP32,), (torch.uint8,)
     _CODES = (torch.uint8, torch.float8_e4m3fn)
     _SCALES = (_FP32S, (torch.uint8, torch.float8_e8m0fnu))             # by scale_fmt
+    _CACHES = (_CODES, _CODES, _BF16S)                                  # by kv_fmt
     lib = ctypes.CDLL(p)
     for name, (res, args) in _SIGS.items():
         fn = getattr(lib, name)
@@ -172,6 +184,47 @@ def _operand(name, t, dtypes, shape, dev):
         raise ValueError(f"{name} must be contiguous {tuple(shape)} of "
                          f"{' or '.join(str(d) for d in dtypes)} on device {dev}")
     return t.data_ptr()
+
+
+def _heads(name, t, T, dev):
+    """(address, row stride, heads, head size) of a bf16 (T, heads, size)
+    tensor whose rows are dense; any row stride for a single row."""
+    if t.dtype is not _BF16 or t.dim() != 3 or t.get_device() != dev:
+        raise ValueError(f"{name} must be bf16 (T, heads, size) on device {dev}")
+    n, H, D = t.shape
+    ld, lh, one = t.stride()
+    if n != T or (one != 1 and D != 1) or (lh != D and H != 1):
+        raise ValueError(f"rows of {name} must be contiguous, and {T} of them")
+    return t.data_ptr(), (H * D if n <= 1 else ld), H, D
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, kv_fmt, Hkv, D, dev):
+    """(pages, page size) of a paged cache, its tensors checked."""
+    if kv_fmt not in (KV_FP8_FLOAT, KV_FP8_UE8M0, KV_BF16):
+        raise ValueError("kv_fmt must be one of KV_FP8_FLOAT, KV_FP8_UE8M0, KV_BF16")
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] != Hkv or shape[3] != D:
+        raise ValueError("caches must be (pages, key heads, page size, head size)")
+    _operand("k_cache", k_cache, _CACHES[kv_fmt], shape, dev)
+    _operand("v_cache", v_cache, _CACHES[kv_fmt], shape, dev)
+    if kv_fmt != KV_BF16:
+        if k_scale is None or v_scale is None:
+            raise ValueError("FP8 caches need k_scale and v_scale")
+        _operand("k_scale", k_scale, _SCALES[kv_fmt], shape[:3], dev)
+        _operand("v_scale", v_scale, _SCALES[kv_fmt], shape[:3], dev)
+    return shape[0], shape[2]
+
+
+def _launch_workspace(need, device, stream):
+    """Workspace for one launch, from that launch's stream: memory of the
+    current one may still be in use there, and is given out again while the
+    launch runs."""
+    import torch
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    st = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(st):
+        return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def _workspace(op, M, N, K, E, ws, device):
@@ -428,15 +481,7 @@ def _moe_decode(fn, xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y, 
         _operand("w13_scale", w13_scale, kinds, s13, dev)
         _operand("w2_scale", w2_scale, kinds, s2, dev)
     if workspace is None:
-        import torch
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
-        else:
-            # from the launch's stream: memory of the current one may still be
-            # in use there, and is given out again while the launch runs
-            st = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-            with torch.cuda.stream(st):
-                workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
+        workspace = _launch_workspace(need, xq.device, stream)
     _check(fn, getattr(lib, fn)(
         _ptr(xq), _ptr(x_scale), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(w13_scale), _ptr(w2),
         _ptr(w2_scale), _ptr(addend), _ptr(y), T, k, H, I, E, scale_fmt, _ptr(workspace), wsb,
@@ -460,3 +505,119 @@ def fp8_fp4_moe_decode(xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, 
     uint8 (E, 2I, H/32); w2 uint8 (E, H, I/2), w2_scale uint8 (E, H, I/32)."""
     _moe_decode("fp8_fp4_moe_decode", xq, x_scale, ids, weights, w13, w13_scale, w2, w2_scale, y,
                 2 * w2.shape[2], addend, scale_fmt, workspace, stream)
+
+
+def rope_inv_freq(inv_freq, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, low=1.0, high=32.0,
+                  orig_len=0.0, stream=None):
+    """inv_freq: fp32 (rot_dim / 2,) out, the rotary angles per position."""
+    lib = load()
+    dev = _on_current_device(inv_freq)
+    if inv_freq.dim() != 1 or dev < 0:
+        raise ValueError("inv_freq must be (rot_dim / 2,) on a GPU")
+    p = _operand("inv_freq", inv_freq, _FP32S, inv_freq.shape, dev)
+    _check("rope_inv_freq", lib.rope_inv_freq(
+        scaling, 2 * inv_freq.shape[0], base, factor, low, high, orig_len, p,
+        _raw_stream(dev) if stream is None else stream))
+
+
+def rope_kv_append(positions, inv_freq, q=None, q_out=None, k=None, v=None, slots=None,
+                   k_cache=None, v_cache=None, k_scale=None, v_scale=None, kv_fmt=KV_FP8_FLOAT,
+                   interleaved=False, mscale=1.0, stream=None):
+    """positions: int32 (T,); inv_freq: fp32 (rot_dim / 2,) or None (nothing
+    is rotated); q and q_out bf16 (T, Hq, D), k and v bf16 (T, Hkv, D), each
+    with a row stride; slots int64 (T,); caches (pages, Hkv, page size, D),
+    uint8 or float8_e4m3fn or (KV_BF16) bf16; scales (pages, Hkv, page size),
+    fp32 or (KV_FP8_UE8M0) uint8 or float8_e8m0fnu."""
+    lib = load()
+    lead = q if q is not None else k
+    if lead is None or (q is None) != (q_out is None) or (k is None) != (v is None):
+        raise ValueError("q and q_out, or k and v, or both pairs are needed")
+    dev = _on_current_device(lead)
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU")
+    T = lead.shape[0]
+    rot, pp, pf = 0, None, None
+    if inv_freq is not None and inv_freq.shape[0]:
+        rot = 2 * inv_freq.shape[0]
+        pf = _operand("inv_freq", inv_freq, _FP32S, (rot // 2,), dev)
+        pp = _operand("positions", positions, _INT32S, (T,), dev)
+    pq = po = pk = pv = psl = pkc = pvc = pks = pvs = None
+    ldq = ldo = ldk = ldv = Hq = Hkv = pages = 0
+    page = 16
+    if q is not None:
+        pq, ldq, Hq, D = _heads("q", q, T, dev)
+        po, ldo, Ho, Do = _heads("q_out", q_out, T, dev)
+        if (Ho, Do) != (Hq, D):
+            raise ValueError("q and q_out need the same shape")
+    if k is not None:
+        pk, ldk, Hkv, Dk = _heads("k", k, T, dev)
+        pv, ldv, Hv, Dv = _heads("v", v, T, dev)
+        if q is None:
+            D = Dk
+        if Hv != Hkv or Dk != D or Dv != D:
+            raise ValueError("k and v need the same shape, and the head size of q")
+        if slots is None or k_cache is None or v_cache is None:
+            raise ValueError("k and v need slots, k_cache and v_cache")
+        psl = _operand("slots", slots, _INT64S, (T,), dev)
+        pages, page = _cache(k_cache, v_cache, k_scale, v_scale, kv_fmt, Hkv, D, dev)
+        pkc, pvc = k_cache.data_ptr(), v_cache.data_ptr()
+        if kv_fmt != KV_BF16:
+            pks, pvs = k_scale.data_ptr(), v_scale.data_ptr()
+    _check("rope_kv_append", lib.rope_kv_append(
+        pq, ldq, po, ldo, pk, ldk, pv, ldv, pp, pf, rot, int(interleaved), mscale, psl, T, Hq, Hkv,
+        D, kv_fmt, pages, page, pkc, pvc, pks, pvs,
+        _raw_stream(dev) if stream is None else stream))
+
+
+def paged_attn_workspace_size(T, B, Hq, Hkv, D, max_pages, page_size, prefix_len=0):
+    return int(load().paged_attn_workspace_size(T, B, Hq, Hkv, D, max_pages, page_size, prefix_len))
+
+
+def paged_attn(q, k_cache, v_cache, kv_len, page_table, y, k_scale=None, v_scale=None,
+               kv_fmt=KV_FP8_FLOAT, q_start=None, prefix_table=None, prefix_len=0, scale=None,
+               window=0, workspace=None, stream=None):
+    """q: bf16 (T, Hq, D) with a row stride; caches and scales as for
+    rope_kv_append; kv_len int32 (B,); page_table int32 (B, max_pages);
+    q_start int32 (B + 1,) or None (T == B); prefix_table int32
+    (>= ceil(prefix_len / page size),) or None; scale 1 / sqrt(D) unless
+    given; y bf16 (T, Hq, D) out."""
+    lib = load()
+    dev = _on_current_device(q)
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU")
+    T = q.shape[0]
+    pq, ldq, Hq, D = _heads("q", q, T, dev)
+    py = _operand("y", y, _BF16S, (T, Hq, D), dev)
+    if k_cache.dim() != 4:
+        raise ValueError("caches must be (pages, key heads, page size, head size)")
+    Hkv = k_cache.shape[1]
+    pages, page = _cache(k_cache, v_cache, k_scale, v_scale, kv_fmt, Hkv, D, dev)
+    pks, pvs = (None, None) if kv_fmt == KV_BF16 else (k_scale.data_ptr(), v_scale.data_ptr())
+    if kv_len.dim() != 1 or page_table.dim() != 2:
+        raise ValueError("kv_len must be (B,) and page_table (B, max_pages)")
+    B, most = page_table.shape
+    pl = _operand("kv_len", kv_len, _INT32S, (B,), dev)
+    pt = _operand("page_table", page_table, _INT32S, (B, most), dev)
+    if q_start is None and T != B:
+        raise ValueError("q_start is needed where sequences have other than one token")
+    ps = None if q_start is None else _operand("q_start", q_start, _INT32S, (B + 1,), dev)
+    pp = None
+    if prefix_len > 0:
+        if prefix_table is None or prefix_table.dim() != 1 or \
+                prefix_table.shape[0] * page < prefix_len:
+            raise ValueError("prefix_table must be (>= ceil(prefix_len / page size),)")
+        pp = _operand("prefix_table", prefix_table, _INT32S, prefix_table.shape, dev)
+    need = lib.paged_attn_workspace_size(T, B, Hq, Hkv, D, most, page, prefix_len)
+    if need == ctypes.c_size_t(-1).value:  # sizes that the library refuses by a status
+        need = 0
+    if workspace is None:
+        workspace = _launch_workspace(need, q.device, stream) if need else None
+        wsb = need
+    else:
+        wsb = workspace.numel() * workspace.element_size()
+        if wsb >= need and not (workspace.get_device() == dev and workspace.is_contiguous()):
+            raise ValueError("the workspace must be contiguous, on the device of q")
+    _check("paged_attn", lib.paged_attn(
+        pq, ldq, ps, pl, pt, most, pp, prefix_len, k_cache.data_ptr(), v_cache.data_ptr(), pks, pvs,
+        kv_fmt, pages, page, T, B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, py,
+        _ptr(workspace), wsb, _raw_stream(dev) if stream is None else stream))

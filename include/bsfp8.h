@@ -70,6 +70,21 @@ typedef enum { BSFP8_ACT_DYNAMIC = 0, BSFP8_ACT_STATIC = 1 } bsfp8_act_scheme;
 /* Scores of moe_route_topk. */
 typedef enum { BSFP8_SCORE_SOFTMAX = 0, BSFP8_SCORE_SIGMOID = 1 } bsfp8_score;
 
+/* Formats of a paged key/value cache: E4M3 codes with one scale per token and
+   head, of a scale_fmt, or bf16 values. */
+typedef enum {
+  BSFP8_KV_FP8_FLOAT = 0,
+  BSFP8_KV_FP8_UE8M0 = 1,
+  BSFP8_KV_BF16 = 2
+} bsfp8_kv_fmt;
+
+/* Angle tables of rope_inv_freq. */
+typedef enum {
+  BSFP8_ROPE_PLAIN = 0,
+  BSFP8_ROPE_LINEAR = 1,
+  BSFP8_ROPE_BY_PARTS = 2
+} bsfp8_rope_scaling;
+
 /* Operation ids for bsfp8_workspace_size. */
 typedef enum {
   BSFP8_OP_BLOCK_GEMM = 0,
@@ -429,6 +444,132 @@ BSFP8_API int32_t fp8_fp4_moe_decode(const void* xq, const void* x_scale, const 
                                      int64_t T, int32_t k, int64_t H, int64_t I, int32_t E,
                                      int32_t scale_fmt, void* workspace, size_t workspace_bytes,
                                      void* stream);
+
+/*
+ * rope_inv_freq -- the table of rotary angles per position:
+ *
+ *   theta_i = base^(-2 i / rot_dim),  i < rot_dim / 2
+ *   PLAIN     theta_i
+ *   LINEAR    theta_i / factor  (positions interpolated)
+ *   BY_PARTS  theta_i g + theta_i / factor (1 - g), with
+ *             g = clamp((orig_len theta_i / (2 pi) - low) / (high - low), 0, 1):
+ *             what turns `high` times or more within the original context
+ *             keeps its angle, what turns `low` times or less is interpolated
+ *             (YaRN's "NTK-by-parts", arXiv 2309.00071)
+ *
+ * in 64 bits, rounded once to fp32.
+ *
+ *   rot_dim   rot_dim % 16 == 0, <= 256.  base >= 1.
+ *   factor    > 0, for LINEAR and BY_PARTS;  0 <= low < high and orig_len > 0
+ *             for BY_PARTS.  What a scaling does not use is not looked at.
+ *   inv_freq  out, fp32 [rot_dim / 2].
+ * Errors: EINVAL; ENOTSUP (rot_dim > 256).
+ */
+BSFP8_API int32_t rope_inv_freq(int32_t scaling, int64_t rot_dim, double base, double factor,
+                                double low, double high, double orig_len, float* inv_freq,
+                                void* stream);
+
+/*
+ * rope_kv_append -- rotary positions for queries and keys, and keys and
+ * values into a paged cache:
+ *
+ *   t = positions[row] inv_freq[i]
+ *   a' = mscale (a cos t - b sin t),  b' = mscale (b cos t + a sin t)
+ *
+ * for the pairs (a, b) = (x[i], x[i + rot_dim/2]) or, interleaved,
+ * (x[2i], x[2i+1]) of each head's first rot_dim values; the others stay.
+ *   q_out  = bf16_rne(q')
+ *   cache: KV_BF16  bf16_rne(k'), v
+ *          KV_FP8_* per token and head the codes and the scale that
+ *          fp8_quant_act gives a group of the D values of k' (in fp32, not
+ *          rounded to bf16 before) or v, in scale_fmt FLOAT or UE8M0
+ *
+ *   q, q_out   bf16 [T][Hq][D], row strides ldq and ldqo; q_out may be q, or
+ *              lie apart from it.  Both NULL: no queries.
+ *   k, v       bf16 [T][Hkv][D], row strides ldk and ldv.  Both NULL: no
+ *              cache (slots and the caches are not looked at).
+ *   positions  DEVICE int32 [T];  inv_freq DEVICE fp32 [rot_dim / 2].  The
+ *              angle is exact (64 bits) before its sine and cosine are taken.
+ *              rot_dim 0: neither is looked at.
+ *   slots      DEVICE int64 [T]: page * page_size + place in the page; a token
+ *              whose slot is negative or >= num_pages * page_size is not
+ *              cached (padding), its query is rotated.  Slots of one call
+ *              must differ: of two tokens with the same one, parts of either
+ *              may stay.
+ *   k_cache, v_cache   [num_pages][Hkv][page_size][D] E4M3 bytes or bf16.
+ *   k_scale, v_scale   [num_pages][Hkv][page_size] fp32 or E8M0 bytes; not
+ *              looked at for KV_BF16.
+ *   D 64, 128 or 256 (else ENOTSUP); rot_dim % 16 == 0, <= D; Hq, Hkv <= 1024;
+ *   page_size a power of two from 16 on (else ENOTSUP); row strides % 8 == 0.
+ * Values that are not finite are outside the contract of KV_FP8_*, as for
+ * fp8_quant_act, and reach their own token's heads only.
+ * Errors: EINVAL; ENOTSUP.
+ */
+BSFP8_API int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo,
+                                 const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                 const int32_t* positions, const float* inv_freq, int64_t rot_dim,
+                                 int32_t interleaved, float mscale, const int64_t* slots,
+                                 int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t kv_fmt,
+                                 int64_t num_pages, int32_t page_size, void* k_cache,
+                                 void* v_cache, void* k_scale, void* v_scale, void* stream);
+
+/*
+ * paged_attn -- causal attention of each sequence's newest tokens over the
+ * paged cache (which holds their own keys and values too):
+ *
+ *   y[t][h] = bf16_rne( sum_j e^(s_j) v_j / sum_j e^(s_j) ),
+ *   s_j = scale q[t][h] . k_j      (key head h / (Hq / Hkv))
+ *
+ * Sequence b has the tokens [q_start[b], q_start[b+1]) and sees prefix_len
+ * keys that all sequences share, then kv_len[b] of its own; its last token
+ * stands at position prefix_len + kv_len[b] - 1, the others before it.  A
+ * token sees the keys at its own position and before, with a window only the
+ * last `window` of these (itself among them).  No key seen: y = 0.  The
+ * prefix's keys and values are read once for the batch, not once per
+ * sequence.  Deterministic: the same call gives the same bits.
+ *
+ *   q           bf16 [T][Hq][D], row stride ldq (ldq % 8 == 0).
+ *   q_start     DEVICE int32 [B+1], not decreasing, or NULL: one token per
+ *               sequence (T == B).  Rows of y before q_start[0] and from
+ *               q_start[B] on stay as they are.
+ *   kv_len      DEVICE int32 [B]; negative counts as 0, more than
+ *               max_pages * page_size as that.
+ *   page_table  DEVICE int32 [B][max_pages]: pages of the own keys in order.
+ *               Entries that no key needs are not used.  Keys of a page
+ *               outside [0, num_pages) count as not seen.
+ *   prefix_table  DEVICE int32 [ceil(prefix_len / page_size)], the same for
+ *               the prefix; own keys begin on a page of their own.  Not
+ *               looked at for prefix_len 0.
+ *   k_cache .. kv_fmt, num_pages, page_size   as rope_kv_append writes them.
+ *               What they hold behind a sequence's or the prefix's last key,
+ *               or before the window, reaches no result, NaN and infinities
+ *               included.
+ *   scale       > 0.  window  0: none.
+ *   y           out, bf16 [T][Hq][D] (dense); must not overlap an input.
+ *   workspace   >= paged_attn_workspace_size(...) bytes, 16-byte aligned;
+ *               nothing in it is kept from one call to the next.  Calls that
+ *               may overlap need one each.
+ *   D 64, 128 or 256; page_size a power of two from 16 on; B <= 4096;
+ *   max_pages * page_size and prefix_len <= 2^30 (ENOTSUP beyond);
+ *   Hq % Hkv == 0, Hq <= 1024.
+ * The launches depend on the sizes above alone, not on what kv_len, q_start
+ * and the tables hold: a captured call serves other lengths.
+ * Errors: EINVAL; ENOTSUP (also sizes whose partial results cannot be counted
+ * in 32 bits); ENOSPC.
+ */
+BSFP8_API int32_t paged_attn(const void* q, int64_t ldq, const int32_t* q_start,
+                             const int32_t* kv_len, const int32_t* page_table, int64_t max_pages,
+                             const int32_t* prefix_table, int64_t prefix_len, const void* k_cache,
+                             const void* v_cache, const void* k_scale, const void* v_scale,
+                             int32_t kv_fmt, int64_t num_pages, int32_t page_size, int64_t T,
+                             int64_t B, int32_t Hq, int32_t Hkv, int32_t D, float scale,
+                             int64_t window, void* y, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Bytes of workspace of paged_attn; (size_t)-1 for sizes that it refuses. */
+BSFP8_API size_t paged_attn_workspace_size(int64_t T, int64_t B, int32_t Hq, int32_t Hkv,
+                                           int32_t D, int64_t max_pages, int32_t page_size,
+                                           int64_t prefix_len);
 
 /*
  * fp4_quant -- NVFP4-style quantization ([NVFP4]: 4-bit float weights and
