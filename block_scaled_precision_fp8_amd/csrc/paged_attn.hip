@@ -142,6 +142,7 @@ struct Wave {
     uint4 k[2][KQ];
     uint32_t v[8][VW];
     float ks[8], vs[8];
+    uint32_t ks8[2], vs8[2]; // E8M0 bytes of four keys each
     int id[2];               // page ids, -1: none
   };
 
@@ -222,51 +223,56 @@ struct Wave {
 
   __device__ __forceinline__ void load(const Block& b, int tile, int id0, int id1, Raw& x) const {
     const int in_page = (1 << a.log2_page) - 1;
+    int64_t row[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int id = s ? id1 : id0;
       x.id[s] = id;
       // keys without a page: those of page 0 are loaded and not used
-      const int64_t row = (((int64_t)(id < 0 ? 0 : id) * a.Hkv + b.h) << a.log2_page) +
-                          ((tile * kTile + 16 * s) & in_page);
-      const uint8_t* kp = a.kc + row * (D * ES);
-      const uint8_t* vp = a.vc + row * (D * ES);
+      row[s] = (((int64_t)(id < 0 ? 0 : id) * a.Hkv + b.h) << a.log2_page) +
+               ((tile * kTile + 16 * s) & in_page);
+      const auto kr = make_rsrc(a.kc + row[s] * (D * ES), 16 * D * ES);
 #pragma unroll
       for (int i = 0; i < KQ; ++i)
-        x.k[s][i] = ld_stream16(kp + (uint32_t)(n * (D * ES) + 64 * i + 16 * g));
+        x.k[s][i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+            kr, n * (D * ES) + 16 * g + 64 * i, 0, 0));
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if constexpr (KV == kKvFloat) {
+        const float4 e = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(
+            make_rsrc(a.ks + 4 * row[s], 64), 16 * g, 0, 0));
+        const float4 f = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(
+            make_rsrc(a.vs + 4 * row[s], 64), 16 * g, 0, 0));
+        x.ks[4 * s] = e.x; x.ks[4 * s + 1] = e.y; x.ks[4 * s + 2] = e.z; x.ks[4 * s + 3] = e.w;
+        x.vs[4 * s] = f.x; x.vs[4 * s + 1] = f.y; x.vs[4 * s + 2] = f.z; x.vs[4 * s + 3] = f.w;
+      } else if constexpr (KV == kKvUe8m0) {
+        x.ks8[s] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(a.ks + row[s], 16), 4 * g, 0, 0);
+        x.vs8[s] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(a.vs + row[s], 16), 4 * g, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const auto vr = make_rsrc(a.vc + row[s] * (D * ES), 16 * D * ES);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint8_t* p = vp + (uint32_t)((4 * g + j) * (D * ES) + n * (DPL * ES));
+        const int p = (4 * g + j) * (D * ES) + n * (DPL * ES);
         uint32_t* v = x.v[4 * s + j];
         if constexpr (VW == 1) {
-          v[0] = __builtin_nontemporal_load((const uint32_t*)p);
+          v[0] = __builtin_amdgcn_raw_buffer_load_b32(vr, p, 0, 0);
         } else if constexpr (VW == 2) {
-          const u32x2 w = __builtin_nontemporal_load((const u32x2*)p);
+          const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vr, p, 0, 0));
           v[0] = w.x;
           v[1] = w.y;
         } else {
 #pragma unroll
           for (int i = 0; i < VW; i += 4) {
-            const uint4 w = ld_stream16(p + 4 * i);
+            const uint4 w = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(vr, p + 4 * i, 0, 0));
             v[i] = w.x;
             v[i + 1] = w.y;
             v[i + 2] = w.z;
             v[i + 3] = w.w;
           }
-        }
-      }
-      if constexpr (KV == kKvFloat) {
-        const float4 e = *(const float4*)(a.ks + 4 * row + 16 * g);
-        const float4 f = *(const float4*)(a.vs + 4 * row + 16 * g);
-        x.ks[4 * s] = e.x; x.ks[4 * s + 1] = e.y; x.ks[4 * s + 2] = e.z; x.ks[4 * s + 3] = e.w;
-        x.vs[4 * s] = f.x; x.vs[4 * s + 1] = f.y; x.vs[4 * s + 2] = f.z; x.vs[4 * s + 3] = f.w;
-      } else if constexpr (KV == kKvUe8m0) {
-        const uint32_t e = *(const uint32_t*)(a.ks + row + 4 * g);
-        const uint32_t f = *(const uint32_t*)(a.vs + row + 4 * g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x.ks[4 * s + j] = e8m0_f32((e >> (8 * j)) & 255u);
-          x.vs[4 * s + j] = e8m0_f32((f >> (8 * j)) & 255u);
         }
       }
     }
@@ -337,8 +343,7 @@ struct Wave {
 
   __device__ __forceinline__ void tile(const Block& b, int tile, Raw& x) {
     const int key0 = tile * kTile;
-    if (key0 >= hi_most || key0 + kTile <= lo_least) return;
-    const bool whole = x.id[0] >= 0 && x.id[1] >= 0 && key0 >= lo_most && key0 + kTile <= hi_least;
+    const bool whole = uniform(x.id[0] >= 0 && x.id[1] >= 0 && key0 >= lo_most && key0 + kTile <= hi_least);
 
     v4f s[RT][2];
 #pragma unroll
@@ -359,6 +364,13 @@ struct Wave {
           s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[rt][i], s[rt][h], 0, 0, 0);
       }
 
+    if constexpr (KV == kKvUe8m0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x.ks[j] = e8m0_f32((x.ks8[j >> 2] >> (8 * (j & 3))) & 255u);
+        x.vs[j] = e8m0_f32((x.vs8[j >> 2] >> (8 * (j & 3))) & 255u);
+      }
+    }
     float ksl[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) ksl[j] = F8 ? x.ks[j] * a.scale_log2 : a.scale_log2;
@@ -507,24 +519,31 @@ struct Wave {
     }
   }
 
-  // Tiles first, first + step, .. below end.
+  // Tiles first, first + step, .. below end.  The next tile's loads go out
+  // before a tile is computed, without a branch around them (the last tile's
+  // go out again at the end): behind one the compiler waits for all of them.
   __device__ __forceinline__ void walk(const Block& b, int first, int end, int step) {
-    const int count = end > first ? (end - first + step - 1) / step : 0;
+    // those that some row sees
+    end = min(end, (hi_most + kTile - 1) / kTile);
+    if (lo_least >= (first + 1) * kTile) first += (lo_least / kTile - first + step - 1) / step * step;
+    if (first >= end) return;
+    const int count = (end - first + step - 1) / step;
     Raw x, z;
     int ids = 0;
     auto fetch = [&](int i, Raw& r) {
-      if (i >= count) return;
-      if (i % 32 == 0) ids = page_ids(b, first + i * step, step);
-      const int at = 2 * (i % 32);
-      load(b, first + i * step, __builtin_amdgcn_readlane(ids, at),
+      if (i < count && i % 32 == 0) ids = page_ids(b, first + i * step, step);
+      const int c = min(i, count - 1), at = 2 * (c % 32);
+      load(b, first + c * step, __builtin_amdgcn_readlane(ids, at),
            __builtin_amdgcn_readlane(ids, at + 1), r);
     };
     fetch(0, x);
-    for (int i = 0; i < count; i += 2) {
+    for (int i = 0;;) {
       fetch(i + 1, z);
       tile(b, first + i * step, x);
-      fetch(i + 2, x);
-      if (i + 1 < count) tile(b, first + (i + 1) * step, z);
+      if (++i >= count) break;
+      fetch(i + 1, x);
+      tile(b, first + i * step, z);
+      if (++i >= count) break;
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) sum[rt] = group_sum(sum[rt]);
@@ -574,13 +593,13 @@ struct Wave {
 // serves them all.  The prefix, where its rows are few too, comes last, as a
 // sequence of its own whose rows are all tokens'.
 template <int KV, int D>
-__global__ __launch_bounds__(256) void attn_split_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, D * (KV == kKvBf16 ? 2 : 1) >= 256 ? 1 : 2) void attn_split_kernel(AttnArgs a) {
   constexpr int DPL = D / 16;
   __shared__ int before[kAttnMaxSeqs + 2];
   __shared__ int wave_total[4];
   __shared__ float merge[2][16][D + 4];
   __shared__ float2 merge_ml[2][16];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63;
   const bool pre = a.prefix_len > 0 && !a.plan.pre_wide;
   const int items = a.B + (pre ? 1 : 0);
   const int pre_blocks = (int)(((int64_t)a.T * a.G + 15) / 16);
@@ -730,7 +749,7 @@ template <int KV, int D, int RT, bool PRE>
 __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
   constexpr int ROWS = 64 * RT;
   __shared__ int found[4];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int splits = PRE ? a.plan.pre_splits : a.plan.own_splits;
   const int blocks = PRE ? a.plan.pre_blocks : a.plan.own_blocks;
   const int64_t wg = grid_row();
@@ -900,6 +919,7 @@ hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
                        row_grid((int64_t)p.own_blocks * p.own_splits * a.Hkv), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((attn_split_kernel<KV, D>), dim3(p.own_groups), dim3(256), 0, s, a);
+  if (p.own_wide && p.own_splits == 1 && a.prefix_len == 0) return hipGetLastError();   // y is complete
   const int64_t rows = (int64_t)a.T * a.Hq;
   if (rows <= 2048)
     hipLaunchKernelGGL((attn_join_kernel<D, 4>), row_grid(rows), dim3(256), 0, s, a);
