@@ -37,6 +37,7 @@ constexpr int kTile = 32;              // keys of a wave's step
 constexpr int kUnit = 4 * kTile;       // keys of a step of four waves that split them
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kMostW = 1024.0f;      // a larger w raises the reference exponent
+constexpr float kMostSum = 8192.0f;    // the same of a bound of 8 of them
 constexpr float kLeastScale = 0x1p-100f;
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) {
@@ -128,6 +129,24 @@ struct Block {
   int n, len;                // the sequence's (own blocks)
 };
 
+// The keys [lo, hi) of the block's table that its row r sees.
+__device__ __forceinline__ void row_range(const AttnArgs& a, const Block& b, int r, int* lo, int* hi) {
+  const int i = (b.row0 + r) / a.G;
+  *lo = *hi = 0;
+  if (!b.pre) {
+    const int pos = b.len - b.n + i;               // among the own keys
+    *hi = clampi(pos + 1, 0, b.keys);
+    if (a.window) *lo = (int)max((int64_t)pos - a.window + 1, (int64_t)0);
+  } else {
+    const int s = seq_of_token(a, i);
+    if (s < 0) return;
+    const Seq sq = seq_of(a, s);
+    const int64_t pos = (int64_t)a.prefix_len + sq.len - sq.n + (i - sq.q0);
+    *hi = (int)min(max(pos + 1, (int64_t)0), (int64_t)b.keys);
+    if (a.window) *lo = (int)min(max(pos - a.window + 1, (int64_t)0), (int64_t)b.keys);
+  }
+}
+
 // ----------------------------------------------------------- a wave's rows
 
 template <int KV, int D, int RT>
@@ -171,20 +190,7 @@ struct Wave {
       const int head = b.h * a.G + (b.row0 + r - i * a.G);
       lo[rt] = hi[rt] = 0;
       if (live) {
-        if (!b.pre) {
-          const int pos = b.len - b.n + i;         // among the own keys
-          hi[rt] = clampi(pos + 1, 0, b.keys);
-          if (a.window) lo[rt] = (int)max((int64_t)pos - a.window + 1, (int64_t)0);
-        } else {
-          const int s = seq_of_token(a, i);
-          if (s >= 0) {
-            const Seq sq = seq_of(a, s);
-            const int64_t pos = (int64_t)a.prefix_len + sq.len - sq.n + (i - sq.q0);
-            hi[rt] = (int)min(max(pos + 1, (int64_t)0), (int64_t)b.keys);
-            if (a.window)
-              lo[rt] = (int)min(max(pos - a.window + 1, (int64_t)0), (int64_t)b.keys);
-          }
-        }
+        row_range(a, b, r, &lo[rt], &hi[rt]);
         lom = max(lom, lo[rt]);
         lol = min(lol, lo[rt]);
         hil = min(hil, hi[rt]);
@@ -742,13 +748,468 @@ __global__ __launch_bounds__(256, D * (KV == kKvBf16 ? 2 : 1) >= 256 ? 1 : 2) vo
 
 // --------------------------------------------- many rows: a wave has its own
 
+// Keys and values of KT = 8192 / D keys at a time go through LDS, converted
+// once for the workgroup's 64 RT rows, each 16-byte piece where a lane of the
+// matrix product reads it: lanes read and write consecutive pieces.  While a
+// tile is computed the next but one is on its way in registers and the next
+// one in the other half of LDS; one barrier per tile.
+template <int KV, int D, int RT>
+struct Rows {
+  static constexpr bool F8 = KV != kKvBf16;
+  static constexpr int ES = F8 ? 1 : 2;
+  static constexpr int KT = 8192 / D;              // keys of a tile: 32, 64 or 128
+  static constexpr int SUBS = KT / 16, NS = KT / 32;
+  static constexpr int COLS = D / 64;              // 64-value columns
+  static constexpr int KP = 2 * ES;                // 16-byte pieces of keys of a thread
+  static constexpr int NO = D / 16;                // output registers of four
+  static constexpr int kIdTiles = 64 / SUBS;       // tiles that one load of page ids covers
+
+  struct Shared {
+    uint4 k[2][SUBS * (D / 32) * 64];
+    uint4 v[2][NS * NO * 64];
+    float ks[2][KT], vs[2][KT];
+    int there[2][SUBS];      // whether the 16 keys have a page
+    int odd[2][4];           // values that are not finite were taken out
+    int range[4][4];
+  };
+  struct Raw {
+    uint4 k[KP];
+    u32x2 v[8];              // E4M3: the first dword
+    uint32_t ks, vs;
+    int id;                  // of the 16 keys whose scales the thread has
+  };
+
+  const AttnArgs& a;
+  Shared& sh;
+  bf16x8 q[RT][D / 32];
+  v4f o[RT][NO];             // o[4 i + t][r]: value 64 i + 16 g + 4 r + t
+  float ref[RT], sum[RT];
+  int lo[RT], hi[RT];
+  int lo_most, lo_least, hi_least, hi_most;        // of the workgroup's rows
+  int wlo_most, whi_least;                         // of the wave's rows
+  int wave, lane, n, g;
+
+  __device__ __forceinline__ Rows(const AttnArgs& args, Shared& shared) : a(args), sh(shared) {
+    wave = uniform(threadIdx.x >> 6);
+    lane = threadIdx.x & 63;
+    n = lane & 15;
+    g = lane >> 4;
+  }
+
+  __device__ __forceinline__ void begin(const Block& b, int row0) {
+    int lom = 0, lol = 0x7fffffff, hil = 0x7fffffff, him = 0;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = row0 + 16 * rt + n;
+      const bool live = r < b.rows;
+      const int i = live ? (b.row0 + r) / a.G : 0;
+      const int head = b.h * a.G + (b.row0 + r - i * a.G);
+      lo[rt] = hi[rt] = 0;
+      if (live) {
+        row_range(a, b, r, &lo[rt], &hi[rt]);
+        lom = max(lom, lo[rt]);
+        lol = min(lol, lo[rt]);
+        hil = min(hil, hi[rt]);
+        him = max(him, hi[rt]);
+      }
+      const uint16_t* src = a.q + (int64_t)(b.q0 + i) * a.ldq + (int64_t)head * D + 8 * g;
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) v = *(const uint4*)(src + 32 * s);
+        q[rt][s] = __builtin_bit_cast(bf16x8, v);
+      }
+#pragma unroll
+      for (int t = 0; t < NO; ++t) o[rt][t] = v4f{0, 0, 0, 0};
+      ref[rt] = kLowest;
+      sum[rt] = 0.0f;
+    }
+    wlo_most = uniform(row16_max(lom));
+    whi_least = -uniform(row16_max(-hil));
+    if (lane == 0) {
+      sh.range[wave][0] = wlo_most;
+      sh.range[wave][2] = whi_least;
+    }
+    lol = -row16_max(-lol);
+    him = row16_max(him);
+    if (lane == 0) {
+      sh.range[wave][1] = lol;
+      sh.range[wave][3] = him;
+    }
+    __syncthreads();
+    lo_most = uniform(max(max(sh.range[0][0], sh.range[1][0]), max(sh.range[2][0], sh.range[3][0])));
+    lo_least = uniform(min(min(sh.range[0][1], sh.range[1][1]), min(sh.range[2][1], sh.range[3][1])));
+    hi_least = uniform(min(min(sh.range[0][2], sh.range[1][2]), min(sh.range[2][2], sh.range[3][2])));
+    hi_most = uniform(max(max(sh.range[0][3], sh.range[1][3]), max(sh.range[2][3], sh.range[3][3])));
+  }
+
+  // Page ids of 64 times 16 keys from tile on.
+  __device__ __forceinline__ int page_ids(const Block& b, int tile) const {
+    const int64_t key = (int64_t)tile * KT + 16 * lane;
+    int id = -1;
+    if (key < b.keys) {
+      id = b.table[key >> a.log2_page];
+      if (id < 0 || id >= a.num_pages) id = -1;
+    }
+    return id;
+  }
+  // The first row (of keys, in the cache) of 16 keys.
+  __device__ __forceinline__ int64_t first_row(const Block& b, int id, int key) const {
+    return (((int64_t)(id < 0 ? 0 : id) * a.Hkv + b.h) << a.log2_page) + (key & ((1 << a.log2_page) - 1));
+  }
+
+  __device__ __forceinline__ void load(const Block& b, int tile, int ids, int first_id, Raw& x) const {
+#pragma unroll
+    for (int p = 0; p < KP; ++p) {
+      const int at = wave * KP + p;
+      const int per = F8 ? COLS : 2 * COLS;        // pieces of 64 bytes in a key
+      const int s = at / per, col = at % per;
+      const int id = __builtin_amdgcn_readlane(ids, first_id + s);
+      const auto r = make_rsrc(a.kc + first_row(b, id, tile * KT + 16 * s) * (D * ES), 16 * D * ES);
+      x.k[p] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+          r, n * (D * ES) + 64 * col + 16 * g, 0, 0));
+    }
+    const int s32 = wave / COLS, col = wave % COLS;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int id = __builtin_amdgcn_readlane(ids, first_id + 2 * s32 + h);
+      const auto r = make_rsrc(a.vc + first_row(b, id, tile * KT + 32 * s32 + 16 * h) * (D * ES), 16 * D * ES);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = (4 * g + j) * (D * ES) + (64 * col + 4 * n) * ES;
+        if constexpr (F8) x.v[4 * h + j].x = __builtin_amdgcn_raw_buffer_load_b32(r, p, 0, 0);
+        else x.v[4 * h + j] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, p, 0, 0));
+      }
+    }
+    const int s = (threadIdx.x >> 4) % SUBS;
+    const int id = __shfl(ids, first_id + s);
+    x.id = id;
+    if (threadIdx.x < KT) {
+      const int64_t row = first_row(b, id, tile * KT + 16 * s) + n;
+      if constexpr (KV == kKvFloat) {
+        x.ks = *(const uint32_t*)(a.ks + 4 * row);
+        x.vs = *(const uint32_t*)(a.vs + 4 * row);
+      } else if constexpr (KV == kKvUe8m0) {
+        x.ks = a.ks[row];
+        x.vs = a.vs[row];
+      }
+    }
+  }
+
+  // A tile's values from registers to LDS.
+  __device__ __forceinline__ void stage(int tile, int buf, int ids, int first_id, Raw& x) const {
+#pragma unroll
+    for (int p = 0; p < KP; ++p) {
+      const int at = wave * KP + p;
+      if constexpr (F8) {
+        const int s = at / COLS, col = at % COLS;
+        uint4* to = sh.k[buf] + (s * (D / 32) + 2 * col + (g >> 1)) * 64 + 32 * (g & 1) + n;
+        to[0] = __builtin_bit_cast(uint4, Wave<KV, D, 1>::key_operand(make_uint2(x.k[p].x, x.k[p].y)));
+        to[16] = __builtin_bit_cast(uint4, Wave<KV, D, 1>::key_operand(make_uint2(x.k[p].z, x.k[p].w)));
+      } else {
+        sh.k[buf][at * 64 + lane] = x.k[p];
+      }
+    }
+    const int s32 = wave / COLS, col = wave % COLS;
+    const int key0 = tile * KT + 32 * s32;
+    const int id0 = __builtin_amdgcn_readlane(ids, first_id + 2 * s32);
+    const int id1 = __builtin_amdgcn_readlane(ids, first_id + 2 * s32 + 1);
+    const bool whole = uniform(id0 >= 0 && id1 >= 0 && key0 >= lo_most && key0 + 32 <= hi_least);
+    uint32_t marks = 0;
+    if (!whole) {
+      // keys that no row of the workgroup sees may hold anything; what is
+      // not finite elsewhere reaches only the rows that see it
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
+        const bool ok = ((j >> 2) ? id1 : id0) >= 0 && key >= lo_least && key < hi_most;
+#pragma unroll
+        for (int i = 0; i < ES; ++i) {
+          uint32_t v = ok ? x.v[j][i] : 0;
+          const uint32_t m = Wave<KV, D, 1>::odd_marks(v);
+          marks |= m;
+          x.v[j][i] = v & ~((m >> (F8 ? 7 : 15)) * (F8 ? 0xffu : 0xffffu));
+        }
+      }
+    }
+    const bool odd = __any(marks != 0);
+    if (lane == 0) sh.odd[buf][wave] = odd;
+    uint4* to = sh.v[buf] + (s32 * NO + 4 * col) * 64 + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (F8)
+          c[j] = __builtin_bit_cast(uint32_t, h ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.v[j].x, 1.0f, true)
+                                                : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.v[j].x, 1.0f, false));
+        else
+          c[j] = x.v[j][h];
+      }
+      u32x4 e, f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        e[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x05040100u);
+        f[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x07060302u);
+      }
+      to[(2 * h) * 64] = __builtin_bit_cast(uint4, e);
+      to[(2 * h + 1) * 64] = __builtin_bit_cast(uint4, f);
+    }
+    if (threadIdx.x < KT) {
+      if constexpr (F8) {
+        const float ks = KV == kKvFloat ? __uint_as_float(x.ks) : e8m0_f32(x.ks);
+        const float vs = KV == kKvFloat ? __uint_as_float(x.vs) : e8m0_f32(x.vs);
+        sh.ks[buf][threadIdx.x] = ks * a.scale_log2;
+        sh.vs[buf][threadIdx.x] = vs;
+      }
+      if (n == 0) sh.there[buf][threadIdx.x >> 4] = x.id >= 0;
+    }
+  }
+
+  __device__ __forceinline__ void odd_values(const Block& b, int key0, const float (&w)[RT][8],
+                                             const uint32_t (&seen)[RT]) {
+    for (int k = 0; k < 32; ++k) {
+      const int id = page_of(b, key0 + k);
+      if (id < 0) continue;
+      const int j = 4 * (k >> 4) + (k & 3), from = ((k >> 2) & 3) * 16 + n;
+      const int64_t row = first_row(b, id, key0 + k);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        float mine = w[rt][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mine = i == j ? w[rt][i] : mine;
+        const float wk = __shfl(mine, from);
+        const bool sees = (__shfl((int)seen[rt], from) >> j) & 1;
+#pragma unroll
+        for (int t = 0; t < NO; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int64_t at = row * D + 64 * (t >> 2) + 16 * g + 4 * r + (t & 3);
+            float val = 0.0f;
+            bool odd;
+            if (F8) {
+              odd = (a.vc[at] & 0x7fu) == 0x7fu;
+              if (odd) val = __uint_as_float(0x7fc00000u);
+            } else {
+              const uint32_t bits = ((const uint16_t*)a.vc)[at];
+              odd = (bits & 0x7f80u) == 0x7f80u;
+              val = __uint_as_float(bits << 16);
+            }
+            if (sees && odd) o[rt][t][r] += wk * val;
+          }
+      }
+    }
+  }
+  __device__ __forceinline__ int page_of(const Block& b, int key) const {
+    if (key >= b.keys) return -1;
+    const int id = b.table[key >> a.log2_page];
+    return id < 0 || id >= a.num_pages ? -1 : id;
+  }
+
+  // 32 keys of a tile.
+  __device__ __forceinline__ void compute(const Block& b, int key0, int buf, int u) {
+    v4f s[RT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) s[rt][h] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const bf16x8 k = __builtin_bit_cast(bf16x8, sh.k[buf][((2 * u + h) * (D / 32) + i) * 64 + lane]);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[rt][i], s[rt][h], 0, 0, 0);
+      }
+    }
+    const bool whole = uniform(key0 >= wlo_most && key0 + 32 <= whi_least &&
+                               sh.there[buf][2 * u] && sh.there[buf][2 * u + 1]);
+    float ksl[8], vs[8];
+    float vmost = 1.0f;
+    if constexpr (F8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 e = *(const float4*)(sh.ks[buf] + 32 * u + 16 * h + 4 * g);
+        const float4 f = *(const float4*)(sh.vs[buf] + 32 * u + 16 * h + 4 * g);
+        ksl[4 * h] = e.x; ksl[4 * h + 1] = e.y; ksl[4 * h + 2] = e.z; ksl[4 * h + 3] = e.w;
+        vs[4 * h] = f.x; vs[4 * h + 1] = f.y; vs[4 * h + 2] = f.z; vs[4 * h + 3] = f.w;
+      }
+      vmost = vs[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) vmost = fmaxf(vmost, vs[j]);
+    }
+    uint32_t seen[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      seen[rt] = 0xffu;
+      if (!whole) {
+        seen[rt] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
+          const bool ok = sh.there[buf][2 * u + (j >> 2)] && key >= lo[rt] && key < hi[rt];
+          seen[rt] |= (uint32_t)ok << j;
+        }
+      }
+    }
+    float w[RT][8];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float add;
+      auto weigh = [&]() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[rt][j] = __builtin_amdgcn_exp2f(fmaf(s[rt][j >> 2][j & 3], F8 ? ksl[j] : a.scale_log2, -ref[rt]));
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[rt][j] = (seen[rt] >> j) & 1 ? w[rt][j] : 0.0f;
+        }
+        add = ((w[rt][0] + w[rt][1]) + (w[rt][2] + w[rt][3])) + ((w[rt][4] + w[rt][5]) + (w[rt][6] + w[rt][7]));
+      };
+      weigh();
+      // the sum of p bounds every p; a scale that nobody uses may hold anything
+      if (__any(!(add * vmost <= kMostSum))) {
+        float top = kLowest;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float e = s[rt][j >> 2][j & 3] * (F8 ? ksl[j] : a.scale_log2);
+          if (F8) e += __builtin_amdgcn_logf(fmaxf(vs[j], kLeastScale));
+          if ((seen[rt] >> j) & 1) top = fmaxf(top, e);
+        }
+        top = fmaxf(ref[rt], group_max(top));
+        const float down = __builtin_amdgcn_exp2f(ref[rt] - top);
+        ref[rt] = top;
+        sum[rt] *= down;
+#pragma unroll
+        for (int t = 0; t < NO; ++t) o[rt][t] *= down;
+        weigh();
+      }
+      sum[rt] += add;
+      if constexpr (F8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[rt][j] *= vs[j];
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[rt][j] = (seen[rt] >> j) & 1 ? w[rt][j] : 0.0f;
+        }
+      }
+    }
+    if (uniform(sh.odd[buf][0] | sh.odd[buf][1] | sh.odd[buf][2] | sh.odd[buf][3]))
+      odd_values(b, key0, w, seen);
+
+    u32x4 wq[RT], wl[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const f32x2 v{w[rt][j], w[rt][j + 1]};
+        if constexpr (F8) {
+          wq[rt][j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+        } else {
+          const bf16x2 c = __builtin_convertvector(v, bf16x2);
+          wq[rt][j / 2] = __builtin_bit_cast(uint32_t, c);
+          wl[rt][j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
+              (f32x2{v.x - (float)c[0], v.y - (float)c[1]}), bf16x2));
+        }
+      }
+#pragma unroll
+    for (int t = 0; t < NO; ++t) {
+      const uint4 v = sh.v[buf][(u * NO + t) * 64 + lane];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if constexpr (F8) {
+          o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              __builtin_bit_cast(f16x8, v), __builtin_bit_cast(f16x8, wq[rt]), o[rt][t], 0, 0, 0);
+        } else {
+          o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, wq[rt]), o[rt][t], 0, 0, 0);
+          o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, wl[rt]), o[rt][t], 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  // Tiles first .. end of the block's keys, all waves together.
+  __device__ __forceinline__ void walk(const Block& b, int first, int end) {
+    end = min(end, (hi_most + KT - 1) / KT);
+    first = max(first, lo_least / KT);
+    if (first < end) {
+      Raw x;
+      int ids = page_ids(b, first), next = page_ids(b, first + kIdTiles);
+      load(b, first, ids, 0, x);
+      stage(first, 0, ids, 0, x);
+      int at = 0;                                  // of the tile in x among the ids' tiles
+      // x has tile i + 1 while tile i is computed
+      auto fetch = [&](int tile) {
+        if (tile >= end) return;
+        if (++at == kIdTiles) at = 0;
+        if (at == 0) {
+          ids = next;
+          next = page_ids(b, tile + kIdTiles);
+        }
+        load(b, tile, ids, at * SUBS, x);
+      };
+      fetch(first + 1);
+      __syncthreads();
+      for (int i = first; i < end; ++i) {
+        const int buf = (i - first) & 1;
+        if (i + 1 < end) {
+          stage(i + 1, buf ^ 1, ids, at * SUBS, x);
+          fetch(i + 2);
+        }
+#pragma unroll
+        for (int u = 0; u < NS; ++u) compute(b, i * KT + 32 * u, buf, u);
+        __syncthreads();
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) sum[rt] = group_sum(sum[rt]);
+  }
+
+  __device__ __forceinline__ void out_row(const Block& b, int row0, int rt, int64_t slot, int block_rows,
+                                          bool direct) const {
+    const int r = row0 + 16 * rt + n;
+    if (r >= b.rows) return;
+    if (direct) {
+      const int i = (b.row0 + r) / a.G;
+      const int head = b.h * a.G + (b.row0 + r - i * a.G);
+      const float f = sum[rt] == 0.0f ? 0.0f : 1.0f / sum[rt];
+      uint16_t* y = a.y + ((int64_t)(b.q0 + i) * a.Hq + head) * D + 16 * g;
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        uint32_t p[8];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int t = 0; t < 4; t += 2)
+            p[2 * m + t / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
+                (f32x2{o[rt][4 * c + t][m] * f, o[rt][4 * c + t + 1][m] * f}), bf16x2));
+        *(uint4*)(y + 64 * c) = make_uint4(p[0], p[1], p[2], p[3]);
+        *(uint4*)(y + 64 * c + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+      }
+    } else {
+      const int64_t at = slot * block_rows + r;
+      if (g == 0) a.ml[at] = make_float2(ref[rt], sum[rt]);
+      float* p = a.part + at * D + 16 * g;
+#pragma unroll
+      for (int c = 0; c < COLS; ++c)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          *(float4*)(p + 64 * c + 4 * m) =
+              make_float4(o[rt][4 * c][m], o[rt][4 * c + 1][m], o[rt][4 * c + 2][m], o[rt][4 * c + 3][m]);
+    }
+  }
+};
+
 // A workgroup takes 64 RT rows of a block and key head; every wave walks all of
 // its split of the keys.  PRE: the blocks are of all tokens, the keys the
 // prefix's.
 template <int KV, int D, int RT, bool PRE>
-__global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
   constexpr int ROWS = 64 * RT;
-  __shared__ int found[4];
+  using R = Rows<KV, D, RT>;
+  constexpr int KT = R::KT;
+  __shared__ typename R::Shared sh;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int splits = PRE ? a.plan.pre_splits : a.plan.own_splits;
   const int blocks = PRE ? a.plan.pre_blocks : a.plan.own_blocks;
@@ -768,7 +1229,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
     k.keys = a.prefix_len;
     k.pre = 1;
     k.n = k.len = 0;
-    end = (k.keys + kTile - 1) / kTile;
+    end = (k.keys + KT - 1) / KT;
   } else {
     int count = 0;                     // sequences whose blocks begin at or before this one
     for (int b = threadIdx.x; b < a.B; b += 256) {
@@ -777,11 +1238,15 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d);
-    if (lane == 0) found[wave] = count;
+    if (lane == 0) sh.range[wave][0] = count;
     __syncthreads();
-    const int b = uniform(found[0] + found[1] + found[2] + found[3]) - 1;
+    const int b = uniform(sh.range[0][0] + sh.range[1][0] + sh.range[2][0] + sh.range[3][0]) - 1;
+    __syncthreads();
     if (b < 0) return;
     Seq s = seq_of(a, b);
+    s.q0 = uniform(s.q0);
+    s.n = uniform(s.n);
+    s.len = uniform(s.len);
     const int j = blk - block_base(a, b, s.q0, ROWS);
     if (j < 0 || (int64_t)j * ROWS >= (int64_t)s.n * a.G) return;
     k.q0 = s.q0;
@@ -793,8 +1258,8 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
     k.n = s.n;
     k.len = s.len;
     const int pos0 = s.len - s.n + k.row0 / a.G, pos1 = s.len - s.n + (k.row0 + k.rows - 1) / a.G;
-    end = (clampi(pos1 + 1, 0, s.len) + kTile - 1) / kTile;
-    if (a.window) first = (int)(max((int64_t)pos0 - a.window + 1, (int64_t)0) / kTile);
+    end = (clampi(pos1 + 1, 0, s.len) + KT - 1) / KT;
+    if (a.window) first = (int)(max((int64_t)pos0 - a.window + 1, (int64_t)0) / KT);
   }
   const int tiles = max(end - first, 0);
   const int per = (tiles + splits - 1) / splits;
@@ -806,10 +1271,9 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
     a.meta[id] = make_int2((int)slot, direct ? -1 : parts);
   if (split >= parts && !(direct && split == 0)) return;
   const int row0 = wave * 16 * RT;
-  if (row0 >= k.rows) return;
-  Wave<KV, D, RT> w(a);
+  R w(a, sh);
   w.begin(k, row0);
-  w.walk(k, first + split * per, min(first + (split + 1) * per, end), 1);
+  w.walk(k, first + split * per, min(first + (split + 1) * per, end));
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) w.out_row(k, row0, rt, slot, ROWS, direct);
 }
@@ -960,7 +1424,7 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
     const int64_t own = up(keys, kUnit) * (rows / 16 + B) * Hkv;
     const int64_t pre = p.pre_wide ? 0 : up(prefix_len, kUnit) * p.pre_blocks * Hkv;
     const int64_t most = own + pre > 0 ? own + pre : 1;
-    p.own_groups = (int)(most < 768 ? most : 768);
+    p.own_groups = (int)(most < 512 ? most : 512);
     p.own_slots = p.own_groups + (int64_t)(p.own_blocks + (p.pre_wide ? 0 : p.pre_blocks)) * Hkv;
   }
   if (p.pre_wide) {
