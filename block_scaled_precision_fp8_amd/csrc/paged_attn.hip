@@ -38,7 +38,7 @@ constexpr int kUnit = 4 * kTile;       // keys of a step of four waves that spli
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kMostW = 1024.0f;      // a larger w raises the reference exponent
 constexpr float kMostSum = 8192.0f;    // the same of a bound of 8 of them
-constexpr float kLeastScale = 0x1p-100f;
+constexpr float kLeastScale = -100.0f;  // log2 of the least value scale that the reference goes by
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) {
   return v < lo ? lo : (v > hi ? hi : v);
@@ -313,6 +313,8 @@ struct Wave {
         const uint32_t m = odd_marks(x.v[j][i]);
         x.v[j][i] &= ~((m >> (F8 ? 7 : 15)) * (F8 ? 0xffu : 0xffffu));
       }
+    int g = this->g, n = this->n;      // not to be prepared before it is known that they are needed
+    asm volatile("" : "+v"(g), "+v"(n));
     const int in_page = (1 << a.log2_page) - 1;
     for (int k = 0; k < kTile; ++k) {
       const int s = k >> 4, j = (k & 3) + 4 * s, from = ((k >> 2) & 3) * 16 + n;
@@ -387,6 +389,8 @@ struct Wave {
     for (int rt = 0; rt < RT; ++rt) {
       seen[rt] = 0xffu;
       if (!whole) {
+        int g = this->g;               // as above
+        asm volatile("" : "+v"(g));
         seen[rt] = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -423,7 +427,7 @@ struct Wave {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float e = s[rt][j >> 2][j & 3] * ksl[j];
-          if (F8) e += __builtin_amdgcn_logf(fmaxf(x.vs[j], kLeastScale));
+          if (F8) e += fmaxf(__builtin_amdgcn_logf(x.vs[j]), kLeastScale);
           if ((seen[rt] >> j) & 1) top = fmaxf(top, e);
         }
         top = fmaxf(ref[rt], group_max(top));
@@ -768,7 +772,7 @@ struct Rows {
     uint4 k[2][SUBS * (D / 32) * 64];
     uint4 v[2][NS * NO * 64];
     float ks[2][KT], vs[2][KT];
-    int there[2][SUBS];      // whether the 16 keys have a page
+    float vmost[2][SUBS];    // the largest of 16 vs
     int odd[2][4];           // values that are not finite were taken out
     int range[4][4];
   };
@@ -776,7 +780,6 @@ struct Rows {
     uint4 k[KP];
     u32x2 v[8];              // E4M3: the first dword
     uint32_t ks, vs;
-    int id;                  // of the 16 keys whose scales the thread has
   };
 
   const AttnArgs& a;
@@ -786,7 +789,6 @@ struct Rows {
   float ref[RT], sum[RT];
   int lo[RT], hi[RT];
   int lo_most, lo_least, hi_least, hi_most;        // of the workgroup's rows
-  int wlo_most, whi_least;                         // of the wave's rows
   int wave, lane, n, g;
 
   __device__ __forceinline__ Rows(const AttnArgs& args, Shared& shared) : a(args), sh(shared) {
@@ -824,16 +826,14 @@ struct Rows {
       ref[rt] = kLowest;
       sum[rt] = 0.0f;
     }
-    wlo_most = uniform(row16_max(lom));
-    whi_least = -uniform(row16_max(-hil));
-    if (lane == 0) {
-      sh.range[wave][0] = wlo_most;
-      sh.range[wave][2] = whi_least;
-    }
+    lom = row16_max(lom);
     lol = -row16_max(-lol);
+    hil = -row16_max(-hil);
     him = row16_max(him);
     if (lane == 0) {
+      sh.range[wave][0] = lom;
       sh.range[wave][1] = lol;
+      sh.range[wave][2] = hil;
       sh.range[wave][3] = him;
     }
     __syncthreads();
@@ -852,6 +852,9 @@ struct Rows {
       if (id < 0 || id >= a.num_pages) id = -1;
     }
     return id;
+  }
+  __device__ __forceinline__ static uint32_t pages_there(int ids, int first_id) {
+    return (uint32_t)(__ballot(ids >= 0) >> first_id) & ((1u << SUBS) - 1);
   }
   // The first row (of keys, in the cache) of 16 keys.
   __device__ __forceinline__ int64_t first_row(const Block& b, int id, int key) const {
@@ -883,7 +886,6 @@ struct Rows {
     }
     const int s = (threadIdx.x >> 4) % SUBS;
     const int id = __shfl(ids, first_id + s);
-    x.id = id;
     if (threadIdx.x < KT) {
       const int64_t row = first_row(b, id, tile * KT + 16 * s) + n;
       if constexpr (KV == kKvFloat) {
@@ -961,13 +963,17 @@ struct Rows {
         const float vs = KV == kKvFloat ? __uint_as_float(x.vs) : e8m0_f32(x.vs);
         sh.ks[buf][threadIdx.x] = ks * a.scale_log2;
         sh.vs[buf][threadIdx.x] = vs;
+        // sizes compare as whole numbers, NaN above all
+        const uint32_t most = row16_max(__float_as_uint(vs) & 0x7fffffffu);
+        if (n == 0) sh.vmost[buf][threadIdx.x >> 4] = __uint_as_float(most);
       }
-      if (n == 0) sh.there[buf][threadIdx.x >> 4] = x.id >= 0;
     }
   }
 
   __device__ __forceinline__ void odd_values(const Block& b, int key0, const float (&w)[RT][8],
                                              const uint32_t (&seen)[RT]) {
+    int g = this->g, n = this->n;      // not to be prepared before it is known that they are needed
+    asm volatile("" : "+v"(g), "+v"(n));
     for (int k = 0; k < 32; ++k) {
       const int id = page_of(b, key0 + k);
       if (id < 0) continue;
@@ -1006,47 +1012,54 @@ struct Rows {
     return id < 0 || id >= a.num_pages ? -1 : id;
   }
 
-  // 32 keys of a tile.
-  __device__ __forceinline__ void compute(const Block& b, int key0, int buf, int u) {
-    v4f s[RT][2];
+  // 32 keys of a tile.  EDGE: some of them may be hidden from some row;
+  // `there`: bit h, whether the 16 keys 16 h .. have a page.
+  __device__ __forceinline__ void compute(const Block& b, int key0, int buf, int u, uint32_t there, const bool EDGE) {
+    uint4 f[2][D / 32];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s[rt][h] = v4f{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const bf16x8 k = __builtin_bit_cast(bf16x8, sh.k[buf][((2 * u + h) * (D / 32) + i) * 64 + lane]);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[rt][i], s[rt][h], 0, 0, 0);
-      }
-    }
-    const bool whole = uniform(key0 >= wlo_most && key0 + 32 <= whi_least &&
-                               sh.there[buf][2 * u] && sh.there[buf][2 * u + 1]);
+      for (int i = 0; i < D / 32; ++i) f[h][i] = sh.k[buf][((2 * u + h) * (D / 32) + i) * 64 + lane];
+    __builtin_amdgcn_sched_barrier(0);
     float ksl[8], vs[8];
     float vmost = 1.0f;
     if constexpr (F8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float4 e = *(const float4*)(sh.ks[buf] + 32 * u + 16 * h + 4 * g);
-        const float4 f = *(const float4*)(sh.vs[buf] + 32 * u + 16 * h + 4 * g);
-        ksl[4 * h] = e.x; ksl[4 * h + 1] = e.y; ksl[4 * h + 2] = e.z; ksl[4 * h + 3] = e.w;
-        vs[4 * h] = f.x; vs[4 * h + 1] = f.y; vs[4 * h + 2] = f.z; vs[4 * h + 3] = f.w;
+        const float4 c = *(const float4*)(sh.ks[buf] + 32 * u + 16 * h + 4 * g);
+        const float4 d = *(const float4*)(sh.vs[buf] + 32 * u + 16 * h + 4 * g);
+        ksl[4 * h] = c.x; ksl[4 * h + 1] = c.y; ksl[4 * h + 2] = c.z; ksl[4 * h + 3] = c.w;
+        vs[4 * h] = d.x; vs[4 * h + 1] = d.y; vs[4 * h + 2] = d.z; vs[4 * h + 3] = d.w;
       }
-      vmost = vs[0];
-#pragma unroll
-      for (int j = 1; j < 8; ++j) vmost = fmaxf(vmost, vs[j]);
+      const float2 m = *(const float2*)(sh.vmost[buf] + 2 * u);
+      vmost = __uint_as_float(max(__float_as_uint(m.x), __float_as_uint(m.y)));
     }
+    v4f s[RT][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f[h][i]), q[rt][i],
+                                                             s[rt][h], 0, 0, 0);
+    uint4 v[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = sh.v[buf][(u * NO + t) * 64 + lane];
     uint32_t seen[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       seen[rt] = 0xffu;
-      if (!whole) {
+      if (EDGE) {
+        int g = this->g;               // as above
+        asm volatile("" : "+v"(g));
         seen[rt] = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
-          const bool ok = sh.there[buf][2 * u + (j >> 2)] && key >= lo[rt] && key < hi[rt];
+          const bool ok = ((there >> (j >> 2)) & 1) && key >= lo[rt] && key < hi[rt];
           seen[rt] |= (uint32_t)ok << j;
         }
       }
@@ -1059,7 +1072,7 @@ struct Rows {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           w[rt][j] = __builtin_amdgcn_exp2f(fmaf(s[rt][j >> 2][j & 3], F8 ? ksl[j] : a.scale_log2, -ref[rt]));
-        if (!whole) {
+        if (EDGE) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[rt][j] = (seen[rt] >> j) & 1 ? w[rt][j] : 0.0f;
         }
@@ -1067,12 +1080,12 @@ struct Rows {
       };
       weigh();
       // the sum of p bounds every p; a scale that nobody uses may hold anything
-      if (__any(!(add * vmost <= kMostSum))) {
+      if (__builtin_expect(__any(!(add * vmost <= kMostSum)), 0)) {
         float top = kLowest;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float e = s[rt][j >> 2][j & 3] * (F8 ? ksl[j] : a.scale_log2);
-          if (F8) e += __builtin_amdgcn_logf(fmaxf(vs[j], kLeastScale));
+          if (F8) e += fmaxf(__builtin_amdgcn_logf(vs[j]), kLeastScale);
           if ((seen[rt] >> j) & 1) top = fmaxf(top, e);
         }
         top = fmaxf(ref[rt], group_max(top));
@@ -1087,45 +1100,57 @@ struct Rows {
       if constexpr (F8) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[rt][j] *= vs[j];
-        if (!whole) {
+        if (EDGE) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[rt][j] = (seen[rt] >> j) & 1 ? w[rt][j] : 0.0f;
         }
       }
     }
-    if (uniform(sh.odd[buf][0] | sh.odd[buf][1] | sh.odd[buf][2] | sh.odd[buf][3]))
-      odd_values(b, key0, w, seen);
+    if (EDGE) {
+      if (uniform(sh.odd[buf][0] | sh.odd[buf][1] | sh.odd[buf][2] | sh.odd[buf][3]))
+        odd_values(b, key0, w, seen);
+    }
 
     u32x4 wq[RT], wl[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        const f32x2 v{w[rt][j], w[rt][j + 1]};
+        const f32x2 p{w[rt][j], w[rt][j + 1]};
         if constexpr (F8) {
-          wq[rt][j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+          wq[rt][j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, f16x2));
         } else {
-          const bf16x2 c = __builtin_convertvector(v, bf16x2);
+          const bf16x2 c = __builtin_convertvector(p, bf16x2);
           wq[rt][j / 2] = __builtin_bit_cast(uint32_t, c);
           wl[rt][j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
-              (f32x2{v.x - (float)c[0], v.y - (float)c[1]}), bf16x2));
+              (f32x2{p.x - (float)c[0], p.y - (float)c[1]}), bf16x2));
         }
       }
-#pragma unroll
-    for (int t = 0; t < NO; ++t) {
-      const uint4 v = sh.v[buf][(u * NO + t) * 64 + lane];
+    auto add_values = [&](const uint4& x, int t) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         if constexpr (F8) {
           o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              __builtin_bit_cast(f16x8, v), __builtin_bit_cast(f16x8, wq[rt]), o[rt][t], 0, 0, 0);
+              __builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, wq[rt]), o[rt][t], 0, 0, 0);
         } else {
           o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, wq[rt]), o[rt][t], 0, 0, 0);
+              __builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, wq[rt]), o[rt][t], 0, 0, 0);
           o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, wl[rt]), o[rt][t], 0, 0, 0);
+              __builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, wl[rt]), o[rt][t], 0, 0, 0);
         }
       }
+    };
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) {
+      uint4 z[4];
+      if (c + 1 < COLS) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) z[t] = sh.v[buf][(u * NO + 4 * c + 4 + t) * 64 + lane];
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) add_values(v[t], 4 * c + t);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) v[t] = z[t];
     }
   }
 
@@ -1139,6 +1164,7 @@ struct Rows {
       load(b, first, ids, 0, x);
       stage(first, 0, ids, 0, x);
       int at = 0;                                  // of the tile in x among the ids' tiles
+      uint32_t there = pages_there(ids, 0), there_next = 0;
       // x has tile i + 1 while tile i is computed
       auto fetch = [&](int tile) {
         if (tile >= end) return;
@@ -1155,10 +1181,14 @@ struct Rows {
         const int buf = (i - first) & 1;
         if (i + 1 < end) {
           stage(i + 1, buf ^ 1, ids, at * SUBS, x);
+          there_next = pages_there(ids, at * SUBS);
           fetch(i + 2);
         }
+        constexpr uint32_t kAll = (1u << SUBS) - 1;
+        const bool edge = !(there == kAll && i * KT >= lo_most && i * KT + KT <= hi_least);
 #pragma unroll
-        for (int u = 0; u < NS; ++u) compute(b, i * KT + 32 * u, buf, u);
+        for (int u = 0; u < NS; ++u) compute(b, i * KT + 32 * u, buf, u, there >> (2 * u), edge);
+        there = there_next;
         __syncthreads();
       }
     }
