@@ -74,7 +74,12 @@ __device__ __forceinline__ int row16_max(int v) {
 
 struct Seq { int q0, n, len; };        // first token, tokens, own cached tokens
 
-__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+__device__ __forceinline__ int len_of(const AttnArgs& a, int b) {
+  const int64_t room = (int64_t)a.max_pages << a.log2_page;
+  const int len = a.kv_len[b];
+  return len < 0 ? 0 : (len > room ? (int)room : len);
+}
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b, int len) {
   Seq s;
   s.q0 = b;
   s.n = 1;
@@ -82,11 +87,10 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
     s.q0 = clampi(a.q_start[b], 0, a.T);
     s.n = clampi(a.q_start[b + 1], s.q0, a.T) - s.q0;
   }
-  const int64_t room = (int64_t)a.max_pages << a.log2_page;
-  const int len = a.kv_len[b];
-  s.len = len < 0 ? 0 : (len > room ? (int)room : len);
+  s.len = len;
   return s;
 }
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) { return seq_of(a, b, len_of(a, b)); }
 
 // Own keys that the sequence's first and last token bound: [first, len).
 __device__ __forceinline__ int first_key(const AttnArgs& a, const Seq& s) {
@@ -149,13 +153,15 @@ __device__ __forceinline__ void row_range(const AttnArgs& a, const Block& b, int
 
 // ----------------------------------------------------------- a wave's rows
 
-template <int KV, int D, int RT>
+template <int KV, int D, int RT, bool STREAM = false>
 struct Wave {
   static constexpr bool F8 = KV != kKvBf16;
   static constexpr int ES = F8 ? 1 : 2;            // bytes of a cached value
   static constexpr int KQ = D * 16 * ES / 1024;    // 16-byte pieces of a lane's 16-key part
   static constexpr int DPL = D / 16;               // values of a key that a lane holds
   static constexpr int VW = DPL * ES / 4;          // dwords of them
+  static constexpr int AUX = STREAM ? 2 : 0;       // non-temporal
+  static constexpr bool AHEAD = D * ES <= 128;     // a second tile fits the registers of two waves
 
   struct Raw {
     uint4 k[2][KQ];
@@ -241,7 +247,7 @@ struct Wave {
 #pragma unroll
       for (int i = 0; i < KQ; ++i)
         x.k[s][i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-            kr, n * (D * ES) + 16 * g + 64 * i, 0, 0));
+            kr, n * (D * ES) + 16 * g + 64 * i, 0, AUX));
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -265,15 +271,15 @@ struct Wave {
         const int p = (4 * g + j) * (D * ES) + n * (DPL * ES);
         uint32_t* v = x.v[4 * s + j];
         if constexpr (VW == 1) {
-          v[0] = __builtin_amdgcn_raw_buffer_load_b32(vr, p, 0, 0);
+          v[0] = __builtin_amdgcn_raw_buffer_load_b32(vr, p, 0, AUX);
         } else if constexpr (VW == 2) {
-          const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vr, p, 0, 0));
+          const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vr, p, 0, AUX));
           v[0] = w.x;
           v[1] = w.y;
         } else {
 #pragma unroll
           for (int i = 0; i < VW; i += 4) {
-            const uint4 w = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(vr, p + 4 * i, 0, 0));
+            const uint4 w = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(vr, p + 4 * i, 0, AUX));
             v[i] = w.x;
             v[i + 1] = w.y;
             v[i + 2] = w.z;
@@ -538,7 +544,7 @@ struct Wave {
     if (lo_least >= (first + 1) * kTile) first += (lo_least / kTile - first + step - 1) / step * step;
     if (first >= end) return;
     const int count = (end - first + step - 1) / step;
-    Raw x, z;
+    Raw x;
     int ids = 0;
     auto fetch = [&](int i, Raw& r) {
       if (i < count && i % 32 == 0) ids = page_ids(b, first + i * step, step);
@@ -546,14 +552,22 @@ struct Wave {
       load(b, first + c * step, __builtin_amdgcn_readlane(ids, at),
            __builtin_amdgcn_readlane(ids, at + 1), r);
     };
-    fetch(0, x);
-    for (int i = 0;;) {
-      fetch(i + 1, z);
-      tile(b, first + i * step, x);
-      if (++i >= count) break;
-      fetch(i + 1, x);
-      tile(b, first + i * step, z);
-      if (++i >= count) break;
+    if constexpr (AHEAD) {
+      Raw z;
+      fetch(0, x);
+      for (int i = 0;;) {
+        fetch(i + 1, z);
+        tile(b, first + i * step, x);
+        if (++i >= count) break;
+        fetch(i + 1, x);
+        tile(b, first + i * step, z);
+        if (++i >= count) break;
+      }
+    } else {
+      for (int i = 0; i < count; ++i) {
+        fetch(i, x);
+        tile(b, first + i * step, x);
+      }
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) sum[rt] = group_sum(sum[rt]);
@@ -602,10 +616,10 @@ struct Wave {
 // lengths are read from the device, so that one launch shape (and one graph)
 // serves them all.  The prefix, where its rows are few too, comes last, as a
 // sequence of its own whose rows are all tokens'.
-template <int KV, int D>
-__global__ __launch_bounds__(256, D * (KV == kKvBf16 ? 2 : 1) >= 256 ? 1 : 2) void attn_split_kernel(AttnArgs a) {
+template <int KV, int D, bool STREAM>
+__global__ __launch_bounds__(256, KV == kKvBf16 && D == 256 ? 1 : 2) void attn_split_kernel(AttnArgs a) {
   constexpr int DPL = D / 16;
-  __shared__ int before[kAttnMaxSeqs + 2];
+  __shared__ int before[kAttnMaxSeqs + 2], lens[kAttnMaxSeqs + 1];
   __shared__ int wave_total[4];
   __shared__ float merge[2][16][D + 4];
   __shared__ float2 merge_ml[2][16];
@@ -618,9 +632,10 @@ __global__ __launch_bounds__(256, D * (KV == kKvBf16 ? 2 : 1) >= 256 ? 1 : 2) vo
   int total = 0;
   for (int base = 0; base < items; base += 256) {
     const int b = base + tid;
-    int v = 0;
+    int v = 0, len = 0;
     if (b < a.B) {
-      const Seq s = seq_of(a, b);
+      len = len_of(a, b);
+      const Seq s = seq_of(a, b, len);
       v = units_of(a, s) * ((s.n * a.G + 15) / 16) * a.Hkv;
     } else if (b < items) {
       v = pre_units * pre_blocks * a.Hkv;
@@ -636,6 +651,7 @@ __global__ __launch_bounds__(256, D * (KV == kKvBf16 ? 2 : 1) >= 256 ? 1 : 2) vo
     int add = total;
     for (int i = 0; i < wave; ++i) add += wave_total[i];
     if (b < items) before[b] = add + incl - v;
+    if (b < a.B) lens[b] = len;
     total += wave_total[0] + wave_total[1] + wave_total[2] + wave_total[3];
     __syncthreads();
   }
@@ -660,7 +676,7 @@ __global__ __launch_bounds__(256, D * (KV == kKvBf16 ? 2 : 1) >= 256 ? 1 : 2) vo
     b = uniform(b);
   }
 
-  Wave<KV, D, 1> w(a);
+  Wave<KV, D, 1, STREAM> w(a);
   while (x < xe) {
     while (b + 1 < items && uniform(before[b + 1]) <= x) ++b;
     Block k;
@@ -668,10 +684,9 @@ __global__ __launch_bounds__(256, D * (KV == kKvBf16 ? 2 : 1) >= 256 ? 1 : 2) vo
     const int rel = x - uniform(before[b]);
     int part;
     if (b < a.B) {
-      Seq s = seq_of(a, b);
+      Seq s = seq_of(a, b, uniform(lens[b]));
       s.q0 = uniform(s.q0);
       s.n = uniform(s.n);
-      s.len = uniform(s.len);
       units = units_of(a, s);
       unit0 = first_key(a, s) / kUnit;
       part = rel / units;
@@ -1317,7 +1332,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int LPR = D / 4, SUB = 64 / LPR;       // lanes of a partial row, rows at once
   constexpr int RPB = 4 / WPR;
   __shared__ float4 acc[4][64];
-  __shared__ float accl[4][64];
+  __shared__ float accl[4][64], acct[4];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t row = grid_row() * RPB + wave / WPR;
   if (row >= (int64_t)a.T * a.Hq) return;          // WPR = 4: the whole workgroup
@@ -1336,40 +1351,78 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   if (t >= s.q0 + s.n) return;
   const int local = (t - s.q0) * a.G + gq;
   const int orows = a.plan.own_rows, prows = a.plan.pre_rows;
+  // what is of no use (no keys: nobody wrote it) is loaded all the same, not
+  // behind the lengths
+  const int2 m0 = a.meta[(block_base(a, b, s.q0, orows) + local / orows) * a.Hkv + h];
   int c0 = 0, c1 = 0;
   int64_t f0 = 0, f1 = 0;              // the first partial's rows
-  if (s.len > 0) {
-    const int id = (block_base(a, b, s.q0, orows) + local / orows) * a.Hkv + h;
-    const int2 m = a.meta[id];
-    if (m.y < 0) return;               // written already
-    c0 = uniform(m.y);
-    f0 = (int64_t)uniform(m.x) * orows + local % orows;
-  }
   if (a.prefix_len > 0) {
     const int64_t all = (int64_t)t * a.G + gq;
-    const int2 m = a.meta[(a.plan.own_blocks + (int)(all / prows)) * a.Hkv + h];
-    c1 = uniform(m.y);
-    f1 = (int64_t)uniform(m.x) * prows + all % prows;
+    const int2 m1 = a.meta[(a.plan.own_blocks + (int)(all / prows)) * a.Hkv + h];
+    c1 = uniform(m1.y);
+    f1 = (int64_t)uniform(m1.x) * prows + all % prows;
+  }
+  if (uniform(s.len) > 0) {
+    if (uniform(m0.y) < 0) return;     // written already
+    c0 = uniform(m0.y);
+    f0 = (int64_t)uniform(m0.x) * orows + local % orows;
   }
   const int count = c0 + c1;
   auto place = [&](int i) { return i < c0 ? f0 + (int64_t)i * orows : f1 + (int64_t)(i - c0) * prows; };
-  float top = kLowest;
-  for (int i = lane; i < count; i += 64) top = fmaxf(top, a.ml[place(i)].x);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
   const int sub = lane / LPR + SUB * (wave % WPR), d4 = lane % LPR;
+  constexpr int STEP = SUB * WPR, NL = 4;          // rows at once, loads under way
   float4 o = make_float4(0, 0, 0, 0);
-  float l = 0.0f;
-  for (int i = sub; i < count; i += SUB * WPR) {
-    const int64_t at = place(i);
-    const float2 e = a.ml[at];
-    const float4 c = *(const float4*)(a.part + at * D + 4 * d4);
-    const float f = __builtin_amdgcn_exp2f(e.x - top);
-    l += e.y * f;
-    o.x += c.x * f;
-    o.y += c.y * f;
-    o.z += c.z * f;
-    o.w += c.w * f;
+  float l = 0.0f, top = kLowest;
+  for (int i0 = sub; i0 < count; i0 += NL * STEP) {
+    float2 e[NL];
+    float4 c[NL];
+#pragma unroll
+    for (int u = 0; u < NL; ++u) {
+      const int i = i0 + u * STEP;
+      e[u] = make_float2(kLowest, 0.0f);
+      c[u] = make_float4(0, 0, 0, 0);
+      if (i < count) {
+        const int64_t at = place(i);
+        e[u] = a.ml[at];
+        c[u] = *(const float4*)(a.part + at * D + 4 * d4);
+      }
+    }
+    float high = top;
+#pragma unroll
+    for (int u = 0; u < NL; ++u) high = fmaxf(high, e[u].x);
+    const float down = __builtin_amdgcn_exp2f(top - high);
+    top = high;
+    l *= down;
+    o.x *= down;
+    o.y *= down;
+    o.z *= down;
+    o.w *= down;
+#pragma unroll
+    for (int u = 0; u < NL; ++u) {
+      const float f = __builtin_amdgcn_exp2f(e[u].x - top);
+      l += e[u].y * f;
+      o.x += c[u].x * f;
+      o.y += c[u].y * f;
+      o.z += c[u].z * f;
+      o.w += c[u].w * f;
+    }
+  }
+  // the lanes' sums, each to its own reference
+  float all = top;
+#pragma unroll
+  for (int d = LPR; d < 64; d <<= 1) all = fmaxf(all, __shfl_xor(all, d));
+  if constexpr (WPR > 1) {
+    if (lane == 0) acct[wave] = all;
+    __syncthreads();
+    all = fmaxf(fmaxf(acct[0], acct[1]), fmaxf(acct[2], acct[3]));
+  }
+  {
+    const float down = __builtin_amdgcn_exp2f(top - all);
+    l *= down;
+    o.x *= down;
+    o.y *= down;
+    o.z *= down;
+    o.w *= down;
   }
 #pragma unroll
   for (int d = LPR; d < 64; d <<= 1) {
@@ -1405,14 +1458,21 @@ template <int KV, int D>
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
   constexpr int RT = attn_row_tiles(D);
   const AttnPlan& p = a.plan;
+  // What a call reads is left in the last-level cache where it fits there (256
+  // MiB), and passes it by where it does not.
+  const int64_t room = (int64_t)a.max_pages << a.log2_page;
+  const int64_t keys = a.window && a.window < room ? a.window : room;
+  const bool stream = keys * a.B * a.Hkv * 2 * (KV == kKvBf16 ? 2 * D : D + 4) > (int64_t(1) << 28);
   if (p.pre_wide)
     hipLaunchKernelGGL((attn_rows_kernel<KV, D, RT, true>),
                        row_grid((int64_t)p.pre_blocks * p.pre_splits * a.Hkv), dim3(256), 0, s, a);
   if (p.own_wide)
     hipLaunchKernelGGL((attn_rows_kernel<KV, D, RT, false>),
                        row_grid((int64_t)p.own_blocks * p.own_splits * a.Hkv), dim3(256), 0, s, a);
+  else if (stream)
+    hipLaunchKernelGGL((attn_split_kernel<KV, D, true>), dim3(p.own_groups), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((attn_split_kernel<KV, D>), dim3(p.own_groups), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attn_split_kernel<KV, D, false>), dim3(p.own_groups), dim3(256), 0, s, a);
   if (p.own_wide && p.own_splits == 1 && a.prefix_len == 0) return hipGetLastError();   // y is complete
   const int64_t rows = (int64_t)a.T * a.Hq;
   if (rows <= 2048)
@@ -1436,13 +1496,15 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
   AttnPlan p{};
   const int64_t G = Hq / Hkv, rows = T * G;
   const int wide = 64 * attn_row_tiles(D);
+  constexpr int64_t kAttnPreUnits = 1024;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   auto splits = [&](int64_t blocks, int64_t most) {
-    const int64_t want = up(1024, blocks * Hkv), tiles = up(most, 8 * kTile);
+    const int64_t want = up(512, blocks * Hkv), tiles = up(most, 8 * kTile);
     return (int)(want < tiles ? want : (tiles > 1 ? tiles : 1));
   };
   p.own_wide = rows > 32 * B;
-  p.pre_wide = prefix_len > 0 && (p.own_wide || rows > 32);
+  p.pre_wide = prefix_len > 0 &&
+               (p.own_wide || up(prefix_len, kUnit) * up(rows, 16) * Hkv > kAttnPreUnits);
   p.own_rows = p.own_wide ? wide : 16;
   p.pre_rows = p.pre_wide ? wide : 16;
   p.own_blocks = (int)(rows / p.own_rows + B);
