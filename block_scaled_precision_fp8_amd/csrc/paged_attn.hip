@@ -161,7 +161,6 @@ struct Wave {
   static constexpr int DPL = D / 16;               // values of a key that a lane holds
   static constexpr int VW = DPL * ES / 4;          // dwords of them
   static constexpr int AUX = STREAM ? 2 : 0;       // non-temporal
-  static constexpr bool AHEAD = D * ES <= 128;     // a second tile fits the registers of two waves
 
   struct Raw {
     uint4 k[2][KQ];
@@ -535,9 +534,10 @@ struct Wave {
     }
   }
 
-  // Tiles first, first + step, .. below end.  The next tile's loads go out
-  // before a tile is computed, without a branch around them (the last tile's
-  // go out again at the end): behind one the compiler waits for all of them.
+  // Tiles first, first + step, .. below end.  What hides a tile's loads is the
+  // other waves: a second tile in registers costs every third wave, and code
+  // that is twice as long (64 x 8192 ragged 121 us with it, 115 without; 1 x
+  // 700 8.5 and 7.8).
   __device__ __forceinline__ void walk(const Block& b, int first, int end, int step) {
     // those that some row sees
     end = min(end, (hi_most + kTile - 1) / kTile);
@@ -546,28 +546,12 @@ struct Wave {
     const int count = (end - first + step - 1) / step;
     Raw x;
     int ids = 0;
-    auto fetch = [&](int i, Raw& r) {
-      if (i < count && i % 32 == 0) ids = page_ids(b, first + i * step, step);
-      const int c = min(i, count - 1), at = 2 * (c % 32);
-      load(b, first + c * step, __builtin_amdgcn_readlane(ids, at),
-           __builtin_amdgcn_readlane(ids, at + 1), r);
-    };
-    if constexpr (AHEAD) {
-      Raw z;
-      fetch(0, x);
-      for (int i = 0;;) {
-        fetch(i + 1, z);
-        tile(b, first + i * step, x);
-        if (++i >= count) break;
-        fetch(i + 1, x);
-        tile(b, first + i * step, z);
-        if (++i >= count) break;
-      }
-    } else {
-      for (int i = 0; i < count; ++i) {
-        fetch(i, x);
-        tile(b, first + i * step, x);
-      }
+    for (int i = 0; i < count; ++i) {
+      if (i % 32 == 0) ids = page_ids(b, first + i * step, step);
+      const int at = 2 * (i % 32);
+      load(b, first + i * step, __builtin_amdgcn_readlane(ids, at),
+           __builtin_amdgcn_readlane(ids, at + 1), x);
+      tile(b, first + i * step, x);
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) sum[rt] = group_sum(sum[rt]);
@@ -616,8 +600,11 @@ struct Wave {
 // lengths are read from the device, so that one launch shape (and one graph)
 // serves them all.  The prefix, where its rows are few too, comes last, as a
 // sequence of its own whose rows are all tokens'.
+constexpr int split_resident(int kv, int D) {      // workgroups that a CU's registers hold
+  return D == 256 ? (kv == kKvBf16 ? 1 : 2) : (kv == kKvBf16 && D == 128 ? 2 : 3);
+}
 template <int KV, int D, bool STREAM>
-__global__ __launch_bounds__(256, KV == kKvBf16 && D == 256 ? 1 : 2) void attn_split_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, split_resident(KV, D)) void attn_split_kernel(AttnArgs a) {
   constexpr int DPL = D / 16;
   __shared__ int before[kAttnMaxSeqs + 2], lens[kAttnMaxSeqs + 1];
   __shared__ int wave_total[4];
@@ -1455,9 +1442,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 }
 
 template <int KV, int D>
-hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
+hipError_t launch_attn(AttnArgs a, hipStream_t s) {
   constexpr int RT = attn_row_tiles(D);
-  const AttnPlan& p = a.plan;
+  AttnPlan& p = a.plan;
+  // all at once, so that equal shares end together
+  if (p.own_groups > 256 * split_resident(KV, D)) p.own_groups = 256 * split_resident(KV, D);
   // What a call reads is left in the last-level cache where it fits there (256
   // MiB), and passes it by where it does not.
   const int64_t room = (int64_t)a.max_pages << a.log2_page;
@@ -1516,7 +1505,7 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
     const int64_t own = up(keys, kUnit) * (rows / 16 + B) * Hkv;
     const int64_t pre = p.pre_wide ? 0 : up(prefix_len, kUnit) * p.pre_blocks * Hkv;
     const int64_t most = own + pre > 0 ? own + pre : 1;
-    p.own_groups = (int)(most < 512 ? most : 512);
+    p.own_groups = (int)(most < 768 ? most : 768);
     p.own_slots = p.own_groups + (int64_t)(p.own_blocks + (p.pre_wide ? 0 : p.pre_blocks)) * Hkv;
   }
   if (p.pre_wide) {
