@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvArgs a, int per_wave
   const int64_t page = slot >> a.log2_page;
   const int64_t at = slot & ((int64_t(1) << a.log2_page) - 1);
 
-  const double pos = (double)a.positions[t];
+  const double pos = half ? (double)a.positions[t] : 0.0;   // without a rotation there may be none
   for (int i = lane; i < half; i += 64) {
     const double turns = pos * (double)a.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
     float s, c;
