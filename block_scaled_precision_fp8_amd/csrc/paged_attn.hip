@@ -1464,7 +1464,9 @@ hipError_t launch_attn(AttnArgs a, hipStream_t s) {
     hipLaunchKernelGGL((attn_split_kernel<KV, D, false>), dim3(p.own_groups), dim3(256), 0, s, a);
   if (p.own_wide && p.own_splits == 1 && a.prefix_len == 0) return hipGetLastError();   // y is complete
   const int64_t rows = (int64_t)a.T * a.Hq;
-  if (rows <= 2048)
+  // four waves a row, or one: 256 rows of 4096 keys 25.0 us and 25.6, one row in
+  // a hundred partial results 32.6 and 37.3; 2048 rows 34.7 and 33.2, 16384 85 and 74
+  if (rows <= 1024)
     hipLaunchKernelGGL((attn_join_kernel<D, 4>), row_grid(rows), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((attn_join_kernel<D, 1>), row_grid((rows + 3) / 4), dim3(256), 0, s, a);
@@ -1485,15 +1487,21 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
   AttnPlan p{};
   const int64_t G = Hq / Hkv, rows = T * G;
   const int wide = 64 * attn_row_tiles(D);
-  constexpr int64_t kAttnPreUnits = 1024;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   auto splits = [&](int64_t blocks, int64_t most) {
     const int64_t want = up(512, blocks * Hkv), tiles = up(most, 8 * kTile);
     return (int)(want < tiles ? want : (tiles > 1 ? tiles : 1));
   };
-  p.own_wide = rows > 32 * B;
-  p.pre_wide = prefix_len > 0 &&
-               (p.own_wide || up(prefix_len, kUnit) * up(rows, 16) * Hkv > kAttnPreUnits);
+  // Few rows: four waves share a block's keys, a step of 128 keys is a unit, and
+  // every block reads the keys anew.  Many: a wave has its own rows.  Behind
+  // 4096 keys with 8 key heads, us, many-row launch and the other:
+  //   1 sequence,  128 rows of it (2048 units)  26.2  26.0;  256 (4096)  33.1  34.1
+  //   8 sequences,  48 rows of each (6144)  45.9  34.6;  64 (8192)  47.7  55.2
+  //   32 sequences, 16 (one block)  106  65;  32 (16384)  108  116;  64  115  218
+  p.own_wide = rows > 16 * B && up(keys, kUnit) * up(rows, 16) * Hkv > 6144;
+  // The same for the prefix: 64 rows on 4096 keys (1024 units) 28  19, on 16384
+  // (4096) 38  38; 256 rows on 16384 (16384 units) 59  116.
+  p.pre_wide = prefix_len > 0 && (p.own_wide || up(prefix_len, kUnit) * up(rows, 16) * Hkv > 2048);
   p.own_rows = p.own_wide ? wide : 16;
   p.pre_rows = p.pre_wide ? wide : 16;
   p.own_blocks = (int)(rows / p.own_rows + B);
