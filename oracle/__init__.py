@@ -18,6 +18,8 @@ numpy with fp64 arithmetic wherever the pages do not fix a precision:
   scales, fp32 tensor scale) and its GEMM.
 * ``layer``   -- residual addition + RMS norm + quantization, a router's
   top-k choice, and a whole MoE layer from the tokens' expert ids.
+* ``attn``    -- rotary positions, a paged key/value cache and attention over
+  it.
 
 Page citations use the page titles:
   [FG-FP8]  "Transformers 中的细粒度 FP8 量化：配置、DeepGEMM 加速路径与 UE8M0
