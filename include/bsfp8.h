@@ -540,7 +540,9 @@ BSFP8_API int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_
  *   prefix_table  DEVICE int32 [ceil(prefix_len / page_size)], the same for
  *               the prefix; own keys begin on a page of their own.  Not
  *               looked at for prefix_len 0.
- *   k_cache .. kv_fmt, num_pages, page_size   as rope_kv_append writes them.
+ *   k_cache .. kv_fmt, num_pages, page_size   as rope_kv_append writes them;
+ *               value scales beyond 2^100 are outside the contract, those
+ *               below 2^-100 lose precision.
  *               What they hold behind a sequence's or the prefix's last key,
  *               or before the window, reaches no result, NaN and infinities
  *               included.
