@@ -37,6 +37,7 @@ struct AttnPlan {
   int own_rows, pre_rows;    // rows of a block: of one sequence, of the prefix launch
   bool own_wide, pre_wide;   // which launch computes them (pre_wide false: with the sequences)
   int own_blocks, pre_blocks;            // bounds of their numbers (own: also ids between)
+  int own_waves, pre_waves;              // of a wide launch's workgroups
   int own_splits, pre_splits;            // of a wide block's keys
   int own_groups;                        // workgroups of the launch that splits keys evenly
   int64_t own_slots, pre_slots;          // partial results

@@ -10,14 +10,14 @@
 // the row's largest log2 w_j only when some w_j passes 2^10, which the first
 // tile does and few others: the sums are rescaled then, and not at every tile.
 // E4M3 codes are exact in bf16 (keys, beside the bf16 query) and in fp16
-// (values); w_j is rounded to fp16, 2^-12 of itself, where a bf16 w_j would lose
+// (values); w_j is rounded to fp16, 2^-11 of itself, where a bf16 w_j would lose
 // as much as rounding the output does.  A bf16 value keeps its type, and w_j is
-// the sum of two bf16 numbers then (2^-17 of it lost).
+// the sum of two bf16 numbers then (2^-16 of it lost).
 //
 // Layout.  The score tile is computed transposed, keys x rows: a lane then
 // holds 8 keys of one row, which is what the second product wants of it as an
-// operand once the values' order of summation is that same order.  Nothing
-// goes through LDS, and a row's statistics are exchanged between four lanes.
+// operand once the values' order of summation is that same order, and a row's
+// statistics are exchanged between four lanes.
 // The values' transposition is a byte permutation of what a lane itself loads
 // (8 keys x D/16 values).  Few rows (attn_split_kernel): nothing goes through
 // LDS on the way from memory to the matrix cores, bound by HBM: 64 sequences
@@ -767,11 +767,11 @@ __global__ __launch_bounds__(256, split_resident(KV, D)) void attn_split_kernel(
 // matrix product reads it: lanes read and write consecutive pieces.  While a
 // tile is computed the next but one is on its way in registers and the next
 // one in the other half of LDS; one barrier per tile.
-template <int KV, int D, int RT>
+template <int KV, int D, int RT, int W>
 struct Rows {
   static constexpr bool F8 = KV != kKvBf16;
   static constexpr int ES = F8 ? 1 : 2;
-  static constexpr int KT = 8192 / D;              // keys of a tile: 32, 64 or 128
+  static constexpr int KT = 2048 * W / D;          // keys of a tile
   static constexpr int SUBS = KT / 16, NS = KT / 32;
   static constexpr int COLS = D / 64;              // 64-value columns
   static constexpr int KP = 2 * ES;                // 16-byte pieces of keys of a thread
@@ -783,8 +783,8 @@ struct Rows {
     uint4 v[2][NS * NO * 64];
     float ks[2][KT], vs[2][KT];
     float vmost[2][SUBS];    // the largest of 16 vs
-    int odd[2][4];           // values that are not finite were taken out
-    int range[4][4];
+    int odd[2][W];           // values that are not finite were taken out
+    int range[W][4];
   };
   struct Raw {
     uint4 k[KP];
@@ -847,10 +847,21 @@ struct Rows {
       sh.range[wave][3] = him;
     }
     __syncthreads();
-    lo_most = uniform(max(max(sh.range[0][0], sh.range[1][0]), max(sh.range[2][0], sh.range[3][0])));
-    lo_least = uniform(min(min(sh.range[0][1], sh.range[1][1]), min(sh.range[2][1], sh.range[3][1])));
-    hi_least = uniform(min(min(sh.range[0][2], sh.range[1][2]), min(sh.range[2][2], sh.range[3][2])));
-    hi_most = uniform(max(max(sh.range[0][3], sh.range[1][3]), max(sh.range[2][3], sh.range[3][3])));
+    lo_most = sh.range[0][0];
+    lo_least = sh.range[0][1];
+    hi_least = sh.range[0][2];
+    hi_most = sh.range[0][3];
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      lo_most = max(lo_most, sh.range[i][0]);
+      lo_least = min(lo_least, sh.range[i][1]);
+      hi_least = min(hi_least, sh.range[i][2]);
+      hi_most = max(hi_most, sh.range[i][3]);
+    }
+    lo_most = uniform(lo_most);
+    lo_least = uniform(lo_least);
+    hi_least = uniform(hi_least);
+    hi_most = uniform(hi_most);
   }
 
   // Page ids of 64 times 16 keys from tile on.
@@ -1117,8 +1128,10 @@ struct Rows {
       }
     }
     if (EDGE) {
-      if (uniform(sh.odd[buf][0] | sh.odd[buf][1] | sh.odd[buf][2] | sh.odd[buf][3]))
-        odd_values(b, key0, w, seen);
+      int odd = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) odd |= sh.odd[buf][i];
+      if (uniform(odd)) odd_values(b, key0, w, seen);
     }
 
     u32x4 wq[RT], wl[RT];
@@ -1241,22 +1254,23 @@ struct Rows {
   }
 };
 
-// A workgroup takes 64 RT rows of a block and key head; every wave walks all of
-// its split of the keys.  PRE: the blocks are of all tokens, the keys the
-// prefix's.  Two workgroups a CU (66 KB of LDS, 256 registers): one's products
-// run beside the other's weights.  Measured at 2 x 2048 over 6000 keys: matrix
-// cores busy 28% of the time, vector issue 50%, LDS 27%.  32 rows a wave share
-// an operand read from LDS (16 would double LDS's share to where it bounds;
-// 64 leave one wave a SIMD, 689 us against 516).
-template <int KV, int D, int RT, bool PRE>
-__global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
-  constexpr int ROWS = 64 * RT;
-  using R = Rows<KV, D, RT>;
+// A workgroup takes 16 W RT rows of a block and key head; every wave walks all of
+// its split of the keys.  pre: the blocks are of all tokens, the keys the
+// prefix's.  Eight waves a CU (132 KB of LDS, 256 registers), in one workgroup
+// or two: one wave's products run beside another's weights.  Four waves a
+// workgroup at 2 x 2048 over 6000 keys: matrix cores busy 28% of the time,
+// vector issue 50%, LDS 27%; eight convert and store a tile once for twice the
+// rows.  32 rows a wave share an operand read from LDS (16 would double LDS's
+// share to where it bounds; 64 leave one wave a SIMD, 689 us against 516).
+template <int KV, int D, int RT, int W>
+__global__ __launch_bounds__(64 * W, 8 / W) void attn_rows_kernel(AttnArgs a, const int pre) {
+  constexpr int ROWS = 16 * W * RT;
+  using R = Rows<KV, D, RT, W>;
   constexpr int KT = R::KT;
   __shared__ typename R::Shared sh;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int splits = PRE ? a.plan.pre_splits : a.plan.own_splits;
-  const int blocks = PRE ? a.plan.pre_blocks : a.plan.own_blocks;
+  const int splits = pre ? a.plan.pre_splits : a.plan.own_splits;
+  const int blocks = pre ? a.plan.pre_blocks : a.plan.own_blocks;
   const int64_t wg = grid_row();
   if (wg >= (int64_t)blocks * splits * a.Hkv) return;
   Block k;
@@ -1265,7 +1279,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
   const int split = (int)(rest % splits);
   const int blk = blocks - 1 - (int)(rest / splits);   // a sequence's last block has the most keys
   int first = 0, end;
-  if constexpr (PRE) {
+  if (pre) {
     k.q0 = 0;
     k.row0 = blk * ROWS;
     k.rows = (int)min((int64_t)ROWS, (int64_t)a.T * a.G - k.row0);
@@ -1276,7 +1290,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
     end = (k.keys + KT - 1) / KT;
   } else {
     int count = 0;                     // sequences whose blocks begin at or before this one
-    for (int b = threadIdx.x; b < a.B; b += 256) {
+    for (int b = threadIdx.x; b < a.B; b += 64 * W) {
       const int q0 = a.q_start ? clampi(a.q_start[b], 0, a.T) : b;
       count += block_base(a, b, q0, ROWS) <= blk;
     }
@@ -1284,7 +1298,10 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
     for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d);
     if (lane == 0) sh.range[wave][0] = count;
     __syncthreads();
-    const int b = uniform(sh.range[0][0] + sh.range[1][0] + sh.range[2][0] + sh.range[3][0]) - 1;
+    count = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) count += sh.range[i][0];
+    const int b = uniform(count) - 1;
     __syncthreads();
     if (b < 0) return;
     Seq s = seq_of(a, b);
@@ -1308,9 +1325,9 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
   const int tiles = max(end - first, 0);
   const int per = (tiles + splits - 1) / splits;
   const int parts = per ? (tiles + per - 1) / per : 0;
-  const int id = (PRE ? a.plan.own_blocks + blk : blk) * a.Hkv + k.h;
-  const int64_t slot = ((int64_t)blk * a.Hkv + k.h) * splits + split + (PRE ? a.plan.own_slots * a.plan.own_rows / ROWS : 0);
-  const bool direct = !PRE && parts <= 1 && a.prefix_len == 0;
+  const int id = (pre ? a.plan.own_blocks + blk : blk) * a.Hkv + k.h;
+  const int64_t slot = ((int64_t)blk * a.Hkv + k.h) * splits + split + (pre ? a.plan.own_slots * a.plan.own_rows / ROWS : 0);
+  const bool direct = !pre && parts <= 1 && a.prefix_len == 0;
   if (split == 0 && threadIdx.x == 0)
     a.meta[id] = make_int2((int)slot, direct ? -1 : parts);
   if (split >= parts && !(direct && split == 0)) return;
@@ -1464,12 +1481,14 @@ hipError_t launch_attn(AttnArgs a, hipStream_t s) {
   const int64_t room = (int64_t)a.max_pages << a.log2_page;
   const int64_t keys = a.window && a.window < room ? a.window : room;
   const bool stream = keys * a.B * a.Hkv * 2 * (KV == kKvBf16 ? 2 * D : D + 4) > (int64_t(1) << 28);
-  if (p.pre_wide)
-    hipLaunchKernelGGL((attn_rows_kernel<KV, D, RT, true>),
-                       row_grid((int64_t)p.pre_blocks * p.pre_splits * a.Hkv), dim3(256), 0, s, a);
-  if (p.own_wide)
-    hipLaunchKernelGGL((attn_rows_kernel<KV, D, RT, false>),
-                       row_grid((int64_t)p.own_blocks * p.own_splits * a.Hkv), dim3(256), 0, s, a);
+  auto rows_launch = [&](int waves, int64_t workgroups, int pre) {
+    if (waves == 8)
+      hipLaunchKernelGGL((attn_rows_kernel<KV, D, RT, 8>), row_grid(workgroups), dim3(512), 0, s, a, pre);
+    else
+      hipLaunchKernelGGL((attn_rows_kernel<KV, D, RT, 4>), row_grid(workgroups), dim3(256), 0, s, a, pre);
+  };
+  if (p.pre_wide) rows_launch(p.pre_waves, (int64_t)p.pre_blocks * p.pre_splits * a.Hkv, 1);
+  if (p.own_wide) rows_launch(p.own_waves, (int64_t)p.own_blocks * p.own_splits * a.Hkv, 0);
   else if (stream)
     hipLaunchKernelGGL((attn_split_kernel<KV, D, true>), dim3(p.own_groups), dim3(256), 0, s, a);
   else
@@ -1498,10 +1517,10 @@ using namespace detail;
 AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, int64_t prefix_len) {
   AttnPlan p{};
   const int64_t G = Hq / Hkv, rows = T * G;
-  const int wide = 64 * attn_row_tiles(D);
+  const int wide = 16 * attn_row_tiles(D);           // of a wave
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  auto splits = [&](int64_t blocks, int64_t most) {
-    const int64_t want = up(512, blocks * Hkv), tiles = up(most, 8 * kTile);
+  auto splits = [&](int64_t blocks, int waves, int64_t most) {
+    const int64_t want = up(2048 / waves, blocks * Hkv), tiles = up(most, 8 * kTile);
     return (int)(want < tiles ? want : (tiles > 1 ? tiles : 1));
   };
   // Few rows: four waves share a block's keys, a step of 128 keys is a unit, and
@@ -1514,12 +1533,18 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
   // The same for the prefix: 64 rows on 4096 keys (1024 units) 28  19, on 16384
   // (4096) 38  38; 256 rows on 16384 (16384 units) 59  116.
   p.pre_wide = prefix_len > 0 && (p.own_wide || up(prefix_len, kUnit) * up(rows, 16) * Hkv > 2048);
-  p.own_rows = p.own_wide ? wide : 16;
-  p.pre_rows = p.pre_wide ? wide : 16;
+  // Workgroups of eight waves where their 256 rows are mostly there.  Behind 4096
+  // keys, four waves and eight, us: 1 sequence of 512 rows 36  38, of 2048 71  66; 2
+  // of 1024 73  66; 8 of 128 66  67, of 256 86  99, of 512 123  109, of 1024 192  159; 2 of
+  // 8192 over 6000 keys 470  387.
+  p.own_waves = rows >= 1024 * B ? 8 : 4;
+  p.pre_waves = rows >= 1024 ? 8 : 4;
+  p.own_rows = p.own_wide ? wide * p.own_waves : 16;
+  p.pre_rows = p.pre_wide ? wide * p.pre_waves : 16;
   p.own_blocks = (int)(rows / p.own_rows + B);
   p.pre_blocks = prefix_len > 0 ? (int)up(rows, p.pre_rows) : 0;
   if (p.own_wide) {
-    p.own_splits = splits(p.own_blocks, keys);
+    p.own_splits = splits(p.own_blocks, p.own_waves, keys);
     p.own_slots = (int64_t)p.own_blocks * Hkv * p.own_splits;
   } else {
     const int64_t own = up(keys, kUnit) * (rows / 16 + B) * Hkv;
@@ -1529,7 +1554,7 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
     p.own_slots = p.own_groups + (int64_t)(p.own_blocks + (p.pre_wide ? 0 : p.pre_blocks)) * Hkv;
   }
   if (p.pre_wide) {
-    p.pre_splits = splits(p.pre_blocks, prefix_len);
+    p.pre_splits = splits(p.pre_blocks, p.pre_waves, prefix_len);
     p.pre_slots = (int64_t)p.pre_blocks * Hkv * p.pre_splits;
     // the prefix's partials begin at a whole block of theirs
     p.own_slots = up(p.own_slots * p.own_rows, p.pre_rows) * p.pre_rows / p.own_rows;

@@ -155,31 +155,73 @@ def test_shapes(case):
     run(cache, q, new, cached, table, ptable, hidden, prefix, window, pad=24)
 
 
+ROOM = 1 << 14     # pages of a table that may be used: the many-row launch goes by what may come
+
+
+@pytest.mark.parametrize("case", [i for i, c in enumerate(SHAPES) if sum(c[0]) * c[2] // c[3] > 16 * len(c[0])])
+def test_shapes_with_room(case):
+    """The same with tables so wide that blocks of many rows are launched."""
+    new, cached, Hq, Hkv, D, fmt, page, prefix, window = SHAPES[case]
+    say("room", case, SHAPES[case])
+    rng = np.random.default_rng(case + 101)
+    cache, q, table, ptable, hidden = setup(rng, new, cached, Hq, Hkv, D, fmt, page, prefix, extra=ROOM)
+    run(cache, q, new, cached, table, ptable, hidden, prefix, window, pad=24)
+
+
+MANY = [
+    # rows by the thousand: workgroups of eight waves
+    ([300], [300], 4, 1, 64, FLOAT, 16, 0, 0),
+    ([270], [1111], 4, 1, 128, FLOAT, 64, 0, 0),
+    ([150], [777], 8, 1, 256, UE8M0, 32, 0, 300),
+    ([257], [600], 8, 2, 128, BF16, 16, 77, 0),
+    ([260, 300], [700, 301], 8, 1, 64, BF16, 128, 200, 250),
+    ([140], [140], 16, 2, 256, BF16, 16, 0, 0),
+    ([600, 3, 0, 500], [650, 3, 9, 900], 8, 1, 64, UE8M0, 16, 0, 0),
+    # single tokens, and a prefix for the many-row launch (four waves, eight)
+    ([1] * 64, [1 + 3 * i % 50 for i in range(64)], 8, 2, 64, FLOAT, 64, 8400, 0),
+    ([1] * 150, [1 + 7 * i % 60 for i in range(150)], 16, 2, 64, UE8M0, 64, 3500, 3000),
+    ([1, 2, 0, 1] * 20, [2, 30, 4, 1] * 20, 8, 2, 128, BF16, 16, 6700, 0),
+    ([1] * 40, [9] * 40, 16, 2, 256, FLOAT, 32, 7000, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_rows(case):
+    new, cached, Hq, Hkv, D, fmt, page, prefix, window = MANY[case]
+    say("many", case, new[:4], cached[:4], MANY[case][2:])
+    rng = np.random.default_rng(case + 201)
+    cache, q, table, ptable, hidden = setup(rng, new, cached, Hq, Hkv, D, fmt, page, prefix,
+                                            extra=ROOM if max(new) > 2 else 2)
+    run(cache, q, new, cached, table, ptable, hidden, prefix, window, pad=8)
+
+
+@pytest.mark.parametrize("room", [2, ROOM])
 @pytest.mark.parametrize("fmt", [FLOAT, UE8M0, BF16])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("new,cached,prefix", [([1], [300], 0), ([1, 1], [40, 700], 70), ([40], [90], 0),
                                                ([20, 30], [20, 45], 50)])
-def test_types_and_heads(fmt, D, new, cached, prefix):
-    say("types", fmt, D, new, cached, prefix)
+def test_types_and_heads(fmt, D, new, cached, prefix, room):
+    say("types", fmt, D, new, cached, prefix, room)
     rng = np.random.default_rng(D + fmt)
-    cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 2, D, fmt, 16, prefix)
+    cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 2, D, fmt, 16, prefix, extra=room)
     run(cache, q, new, cached, table, ptable, hidden, prefix)
 
 
 def test_tokens_of_no_sequence_stay():
     rng = np.random.default_rng(3)
-    for new, cached in (([2, 1], [20, 40]), ([80, 90], [80, 100])):
-        cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 2, 128, FLOAT, 16, 30)
+    for new, cached, room in (([2, 1], [20, 40], 2), ([80, 90], [80, 100], 2), ([80, 90], [80, 100], ROOM)):
+        cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 2, 128, FLOAT, 16, 30, extra=room)
         run(cache, q, new, cached, table, ptable, hidden, 30, tail=5)
         run(cache, q, new, cached, table, ptable, hidden, 0, tail=5)
 
 
 @pytest.mark.parametrize("fmt", [FLOAT, BF16])
-@pytest.mark.parametrize("new,cached", [([1, 1], [200, 90]), ([70, 3], [200, 90])])
-def test_bad_pages_are_hidden(fmt, new, cached):
+@pytest.mark.parametrize("new,cached,room", [([1, 1], [200, 90], 2), ([70, 3], [200, 90], 2),
+                                             ([70, 3], [200, 90], ROOM)])
+def test_bad_pages_are_hidden(fmt, new, cached, room):
     """Pages outside the cache in the middle of a sequence and of the prefix."""
     rng = np.random.default_rng(11)
-    cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 1, 64, fmt, 16, 100)
+    cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 1, 64, fmt, 16, 100, extra=room)
     table[0, 2], table[1, 0], ptable[3] = -1, 1 << 29, -(1 << 31)
     run(cache, q, new, cached, table, ptable, hidden, 100)
     table[1, :] = -1                                          # nothing of its own left
@@ -194,8 +236,8 @@ def test_values_only_later_tokens_see(fmt, D):
     """NaN and infinities of a later token's value reach that token and the
     later ones, and no earlier one."""
     rng = np.random.default_rng(12)
-    for n, length in ((4, 50), (60, 170)):
-        cache, q, table, ptable, hidden = setup(rng, [n], [length], 4, 2, D, fmt, 16)
+    for n, length, room in ((4, 50, 2), (60, 170, 2), (60, 170, ROOM)):
+        cache, q, table, ptable, hidden = setup(rng, [n], [length], 4, 2, D, fmt, 16, extra=room)
         t = cache.tensors()
         poison(t, cache, hidden)
         key = length - 2                                      # the last but one token's
@@ -248,9 +290,10 @@ def test_value_scales_of_all_sizes(fmt):
     """Value scales that differ by 2^40 from token to token and are all tiny
     or all large: the weights keep their precision."""
     rng = np.random.default_rng(14)
-    for lo, hi in ((87, 127), (30, 34), (200, 204)):
-        new, cached = [1, 3], [600, 200]
-        cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 2, 128, fmt, 16)
+    for lo, hi, new, room in ((87, 127, [1, 3], 2), (30, 34, [1, 3], 2), (200, 204, [1, 3], 2),
+                              (87, 127, [40, 9], ROOM), (200, 204, [40, 9], ROOM)):
+        cached = [600, 200]
+        cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 2, 128, fmt, 16, extra=room)
         codes, _ = cache.parts[1]
         e = rng.integers(lo, hi, codes.shape[:3]).astype(np.uint8)
         cache.parts[1] = (codes, e if fmt == UE8M0 else (2.0 ** (e.astype(np.float64) - 127)).astype(np.float32))
@@ -262,12 +305,13 @@ def test_one_dominant_value_scale():
     """The largest value belongs to a key of almost no weight: the others'
     weights are small beside it and must not be lost."""
     rng = np.random.default_rng(15)
-    cache, q, table, ptable, hidden = setup(rng, [1], [256], 4, 1, 64, FLOAT, 16)
-    codes, scale = cache.parts[1]
-    scale[table[0, 0], :, 0] = 2.0 ** 20
-    cache.parts[0][1][table[0, 0], :, 0] = 0.0               # its score is 0, the others' large
-    cache.k, cache.v = (A.cache_values(c, s, FLOAT) for c, s in cache.parts)
-    run(cache, q, [1], [256], table, ptable, hidden)
+    for new, room in (([1], 2), ([30], ROOM)):
+        cache, q, table, ptable, hidden = setup(rng, new, [256], 4, 1, 64, FLOAT, 16, extra=room)
+        codes, scale = cache.parts[1]
+        scale[table[0, 0], :, 0] = 2.0 ** 20
+        cache.parts[0][1][table[0, 0], :, 0] = 0.0           # its score is 0, the others' large
+        cache.k, cache.v = (A.cache_values(c, s, FLOAT) for c, s in cache.parts)
+        run(cache, q, new, [256], table, ptable, hidden)
 
 
 def test_same_bits_again_and_on_another_stream():
