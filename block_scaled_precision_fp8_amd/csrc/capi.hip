@@ -81,8 +81,9 @@ int32_t check_cache(int32_t fmt, int64_t num_pages, int32_t page_size, const voi
   return BSFP8_OK;
 }
 
+// *plan: that of sizes that are accepted and not empty
 int32_t check_attn_sizes(int64_t T, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
-                         int64_t max_pages, int32_t page_size, int64_t prefix_len) {
+                         int64_t max_pages, int32_t page_size, int64_t prefix_len, AttnPlan* plan) {
   if (T < 0 || B < 0 || !fits_i32(T) || !fits_i32(B)) return BSFP8_EINVAL;
   if (Hkv < 1 || Hq < Hkv || Hq > kAttnMaxHeads || Hq % Hkv != 0 || D <= 0) return BSFP8_EINVAL;
   int32_t r = check_page_size(page_size);
@@ -96,7 +97,7 @@ int32_t check_attn_sizes(int64_t T, int64_t B, int32_t Hq, int32_t Hkv, int32_t 
   const int64_t blocks = T * (Hq / Hkv) / 16 + B + 1;
   if ((double)blocks * Hkv * (((double)max_pages * page_size + prefix_len) / 128 + 2) > 2e9)
     return BSFP8_ENOTSUP;
-  const AttnPlan p = attn_plan(T, B, Hq, Hkv, D, max_pages * page_size, prefix_len);
+  const AttnPlan p = *plan = attn_plan(T, B, Hq, Hkv, D, max_pages * page_size, prefix_len);
   if (p.own_slots * p.own_rows + p.pre_slots * p.pre_rows > 0x7fffffffLL) return BSFP8_ENOTSUP;
   return BSFP8_OK;
 }
@@ -426,10 +427,10 @@ int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, co
 
 size_t paged_attn_workspace_size(int64_t T, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
                                  int64_t max_pages, int32_t page_size, int64_t prefix_len) {
-  if (check_attn_sizes(T, B, Hq, Hkv, D, max_pages, page_size, prefix_len) != BSFP8_OK)
+  AttnPlan p{};
+  if (check_attn_sizes(T, B, Hq, Hkv, D, max_pages, page_size, prefix_len, &p) != BSFP8_OK)
     return (size_t)-1;
-  if (T == 0 || B == 0) return 0;
-  return attn_plan(T, B, Hq, Hkv, D, max_pages * page_size, prefix_len).bytes;
+  return p.bytes;
 }
 
 int32_t paged_attn(const void* q, int64_t ldq, const int32_t* q_start, const int32_t* kv_len,
@@ -439,7 +440,8 @@ int32_t paged_attn(const void* q, int64_t ldq, const int32_t* q_start, const int
                    int32_t page_size, int64_t T, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
                    float scale, int64_t window, void* y, void* workspace, size_t workspace_bytes,
                    void* stream) {
-  int32_t r = check_attn_sizes(T, B, Hq, Hkv, D, max_pages, page_size, prefix_len);
+  AttnPlan p{};
+  int32_t r = check_attn_sizes(T, B, Hq, Hkv, D, max_pages, page_size, prefix_len, &p);
   if (r != BSFP8_OK) return r;
   if (!(scale > 0.0f) || !(scale <= 1e30f)) return BSFP8_EINVAL;
   if (window < 0 || !fits_i32(window)) return BSFP8_EINVAL;
@@ -453,7 +455,6 @@ int32_t paged_attn(const void* q, int64_t ldq, const int32_t* q_start, const int
   if (!al16(q) || !al16(y) || ((uintptr_t)q_start & 3u) || ((uintptr_t)kv_len & 3u) ||
       ((uintptr_t)page_table & 3u) || ((uintptr_t)prefix_table & 3u))
     return BSFP8_EINVAL;
-  const AttnPlan p = attn_plan(T, B, Hq, Hkv, D, max_pages * page_size, prefix_len);
   if (!workspace || ((uintptr_t)workspace & 15u)) return BSFP8_EINVAL;
   if (workspace_bytes < p.bytes) return BSFP8_ENOSPC;
   r = check_device(stream);

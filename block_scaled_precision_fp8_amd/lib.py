@@ -51,6 +51,7 @@ _F64 = ctypes.c_double
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
+_REFUSED = ctypes.c_size_t(-1).value
 
 _SIGS = {
     "bsfp8_version": (_I32, []),
@@ -112,9 +113,9 @@ def load(path=None):
     global _device, _raw_stream
     _device = getattr(torch._C, "_cuda_getDevice", _device)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-    global _BF16, _FP32, _INT32, _BF16S, _FP32S, _BYTES, _CODES, _SCALES, _INT32S, _INT64S, _CACHES
+    global _BF16, _FP32, _INT32, _BF16S, _FP32S, _BYTES, _CODES, _SCALES, _INT32S, _INT64S, _CACHES, _empty
     _BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
-    _INT32S, _INT64S = (_INT32,), (torch.int64,)
+    _INT32S, _INT64S, _empty = (_INT32,), (torch.int64,), torch.empty
     _BF16S, _FP32S, _BYTES = (_BF16,), (_FP32,), (torch.uint8,)
     _CODES = (torch.uint8, torch.float8_e4m3fn)
     _SCALES = (_FP32S, (torch.uint8, torch.float8_e8m0fnu))             # by scale_fmt
@@ -189,39 +190,42 @@ def _operand(name, t, dtypes, shape, dev):
 def _heads(name, t, T, dev):
     """(address, row stride, heads, head size) of a bf16 (T, heads, size)
     tensor whose rows are dense; any row stride for a single row."""
-    if t.dtype is not _BF16 or t.dim() != 3 or t.get_device() != dev:
-        raise ValueError(f"{name} must be bf16 (T, heads, size) on device {dev}")
-    n, H, D = t.shape
+    n, H, D = t.shape                      # ValueError for another number of dimensions
     ld, lh, one = t.stride()
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        raise ValueError(f"{name} must be bf16 on device {dev}")
     if n != T or (one != 1 and D != 1) or (lh != D and H != 1):
         raise ValueError(f"rows of {name} must be contiguous, and {T} of them")
     return t.data_ptr(), (H * D if n <= 1 else ld), H, D
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, kv_fmt, Hkv, D, dev):
-    """(pages, page size) of a paged cache, its tensors checked."""
+    """(pages, page size, addresses of keys, values and their scales) of a
+    paged cache, its tensors checked."""
     if kv_fmt not in (KV_FP8_FLOAT, KV_FP8_UE8M0, KV_BF16):
         raise ValueError("kv_fmt must be one of KV_FP8_FLOAT, KV_FP8_UE8M0, KV_BF16")
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[1] != Hkv or shape[3] != D:
+    pages, heads, page, size = shape = k_cache.shape
+    if heads != Hkv or size != D:
         raise ValueError("caches must be (pages, key heads, page size, head size)")
-    _operand("k_cache", k_cache, _CACHES[kv_fmt], shape, dev)
-    _operand("v_cache", v_cache, _CACHES[kv_fmt], shape, dev)
-    if kv_fmt != KV_BF16:
-        if k_scale is None or v_scale is None:
-            raise ValueError("FP8 caches need k_scale and v_scale")
-        _operand("k_scale", k_scale, _SCALES[kv_fmt], shape[:3], dev)
-        _operand("v_scale", v_scale, _SCALES[kv_fmt], shape[:3], dev)
-    return shape[0], shape[2]
+    kinds = _CACHES[kv_fmt]
+    pk = _operand("k_cache", k_cache, kinds, shape, dev)
+    pv = _operand("v_cache", v_cache, kinds, shape, dev)
+    if kv_fmt == KV_BF16:
+        return pages, page, pk, pv, None, None
+    if k_scale is None or v_scale is None:
+        raise ValueError("FP8 caches need k_scale and v_scale")
+    kinds, shape = _SCALES[kv_fmt], (pages, heads, page)
+    return (pages, page, pk, pv, _operand("k_scale", k_scale, kinds, shape, dev),
+            _operand("v_scale", v_scale, kinds, shape, dev))
 
 
 def _launch_workspace(need, device, stream):
     """Workspace for one launch, from that launch's stream: memory of the
     current one may still be in use there, and is given out again while the
     launch runs."""
-    import torch
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return _empty(need, dtype=_BYTES[0], device=device)
+    import torch
     st = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     with torch.cuda.stream(st):
         return torch.empty(need, dtype=torch.uint8, device=device)
@@ -559,10 +563,8 @@ def rope_kv_append(positions, inv_freq, q=None, q_out=None, k=None, v=None, slot
         if slots is None or k_cache is None or v_cache is None:
             raise ValueError("k and v need slots, k_cache and v_cache")
         psl = _operand("slots", slots, _INT64S, (T,), dev)
-        pages, page = _cache(k_cache, v_cache, k_scale, v_scale, kv_fmt, Hkv, D, dev)
-        pkc, pvc = k_cache.data_ptr(), v_cache.data_ptr()
-        if kv_fmt != KV_BF16:
-            pks, pvs = k_scale.data_ptr(), v_scale.data_ptr()
+        pages, page, pkc, pvc, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale, kv_fmt, Hkv, D,
+                                                 dev)
     _check("rope_kv_append", lib.rope_kv_append(
         pq, ldq, po, ldo, pk, ldk, pv, ldv, pp, pf, rot, int(interleaved), mscale, psl, T, Hq, Hkv,
         D, kv_fmt, pages, page, pkc, pvc, pks, pvs,
@@ -588,16 +590,11 @@ def paged_attn(q, k_cache, v_cache, kv_len, page_table, y, k_scale=None, v_scale
     T = q.shape[0]
     pq, ldq, Hq, D = _heads("q", q, T, dev)
     py = _operand("y", y, _BF16S, (T, Hq, D), dev)
-    if k_cache.dim() != 4:
-        raise ValueError("caches must be (pages, key heads, page size, head size)")
-    Hkv = k_cache.shape[1]
-    pages, page = _cache(k_cache, v_cache, k_scale, v_scale, kv_fmt, Hkv, D, dev)
-    pks, pvs = (None, None) if kv_fmt == KV_BF16 else (k_scale.data_ptr(), v_scale.data_ptr())
-    if kv_len.dim() != 1 or page_table.dim() != 2:
-        raise ValueError("kv_len must be (B,) and page_table (B, max_pages)")
-    B, most = page_table.shape
+    _, Hkv, _, _ = k_cache.shape
+    pages, page, pkc, pvc, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale, kv_fmt, Hkv, D, dev)
+    B, most = shape = page_table.shape
     pl = _operand("kv_len", kv_len, _INT32S, (B,), dev)
-    pt = _operand("page_table", page_table, _INT32S, (B, most), dev)
+    pt = _operand("page_table", page_table, _INT32S, shape, dev)
     if q_start is None and T != B:
         raise ValueError("q_start is needed where sequences have other than one token")
     ps = None if q_start is None else _operand("q_start", q_start, _INT32S, (B + 1,), dev)
@@ -608,7 +605,7 @@ def paged_attn(q, k_cache, v_cache, kv_len, page_table, y, k_scale=None, v_scale
             raise ValueError("prefix_table must be (>= ceil(prefix_len / page size),)")
         pp = _operand("prefix_table", prefix_table, _INT32S, prefix_table.shape, dev)
     need = lib.paged_attn_workspace_size(T, B, Hq, Hkv, D, most, page, prefix_len)
-    if need == ctypes.c_size_t(-1).value:  # sizes that the library refuses by a status
+    if need == _REFUSED:                   # sizes that the library refuses by a status
         need = 0
     if workspace is None:
         workspace = _launch_workspace(need, q.device, stream) if need else None
@@ -618,6 +615,6 @@ def paged_attn(q, k_cache, v_cache, kv_len, page_table, y, k_scale=None, v_scale
         if wsb >= need and not (workspace.get_device() == dev and workspace.is_contiguous()):
             raise ValueError("the workspace must be contiguous, on the device of q")
     _check("paged_attn", lib.paged_attn(
-        pq, ldq, ps, pl, pt, most, pp, prefix_len, k_cache.data_ptr(), v_cache.data_ptr(), pks, pvs,
+        pq, ldq, ps, pl, pt, most, pp, prefix_len, pkc, pvc, pks, pvs,
         kv_fmt, pages, page, T, B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, py,
         _ptr(workspace), wsb, _raw_stream(dev) if stream is None else stream))
