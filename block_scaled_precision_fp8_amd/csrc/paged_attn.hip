@@ -1529,7 +1529,12 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
   //   1 sequence,  128 rows of it (2048 units)  26.2  26.0;  256 (4096)  33.1  34.1
   //   8 sequences,  48 rows of each (6144)  45.9  34.6;  64 (8192)  47.7  55.2
   //   32 sequences, 16 (one block)  106  65;  32 (16384)  108  116;  64  115  218
-  p.own_wide = rows > 16 * B && up(keys, kUnit) * up(rows, 16) * Hkv > 6144;
+  // Behind few keys it is the blocks that count, each with its own latencies; behind
+  // 256:  8 sequences, 64 rows of each (256 blocks and key heads)  16.7  16.3;  16 (512)
+  // 17.0  16.7;  32 (1024)  21  31;  64 (2048)  34  43;  behind 64 keys 9.8  11.6,  10.0  13.8,
+  // 12  21,  19  33.
+  const int64_t blocks = up(rows, 16) * Hkv;
+  p.own_wide = rows > 16 * B && (blocks > 512 || up(keys, kUnit) * blocks > 6144);
   // The same for the prefix: 64 rows on 4096 keys (1024 units) 28  19, on 16384
   // (4096) 38  38; 256 rows on 16384 (16384 units) 59  116.
   p.pre_wide = prefix_len > 0 && (p.own_wide || up(prefix_len, kUnit) * up(rows, 16) * Hkv > 2048);
