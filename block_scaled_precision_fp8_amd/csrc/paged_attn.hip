@@ -642,7 +642,12 @@ __global__ __launch_bounds__(256, split_resident(KV, D)) void attn_split_kernel(
       if (lane >= d) incl += u;
     }
     if (lane == 63) wave_total[wave] = incl;
-    __syncthreads();
+    // sequences in another order would count rows twice, past what has a place
+    if (a.q_start) {
+      if (__syncthreads_or(b < a.B && a.q_start[b + 1] < a.q_start[b])) return;
+    } else {
+      __syncthreads();
+    }
     int add = total;
     for (int i = 0; i < wave; ++i) add += wave_total[i];
     if (b < items) before[b] = add + incl - v;
@@ -762,8 +767,8 @@ __global__ __launch_bounds__(256, split_resident(KV, D)) void attn_split_kernel(
 
 // --------------------------------------------- many rows: a wave has its own
 
-// Keys and values of KT = 8192 / D keys at a time go through LDS, converted
-// once for the workgroup's 64 RT rows, each 16-byte piece where a lane of the
+// Keys and values of KT = 2048 W / D keys at a time go through LDS, converted
+// once for the workgroup's 16 W RT rows, each 16-byte piece where a lane of the
 // matrix product reads it: lanes read and write consecutive pieces.  While a
 // tile is computed the next but one is on its way in registers and the next
 // one in the other half of LDS; one barrier per tile.
@@ -1290,10 +1295,13 @@ __global__ __launch_bounds__(64 * W, 8 / W) void attn_rows_kernel(AttnArgs a, co
     end = (k.keys + KT - 1) / KT;
   } else {
     int count = 0;                     // sequences whose blocks begin at or before this one
+    bool falls = false;
     for (int b = threadIdx.x; b < a.B; b += 64 * W) {
       const int q0 = a.q_start ? clampi(a.q_start[b], 0, a.T) : b;
       count += block_base(a, b, q0, ROWS) <= blk;
+      falls |= a.q_start && a.q_start[b + 1] < a.q_start[b];
     }
+    if (__syncthreads_or(falls)) return;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d);
     if (lane == 0) sh.range[wave][0] = count;
@@ -1357,7 +1365,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   int b = t;
   if (a.q_start) {
     int count = 0;                     // sequences that end at or before the token
-    for (int i = lane; i < a.B; i += 64) count += a.q_start[i + 1] <= t;
+    bool falls = false;
+    for (int i = lane; i < a.B; i += 64) {
+      const int next = a.q_start[i + 1];
+      count += next <= t;
+      falls |= next < a.q_start[i];
+    }
+    if (__any(falls)) return;          // nothing was computed
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d);
     b = uniform(count);

@@ -529,9 +529,10 @@ BSFP8_API int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_
  * sequence.  Deterministic: the same call gives the same bits.
  *
  *   q           bf16 [T][Hq][D], row stride ldq (ldq % 8 == 0).
- *   q_start     DEVICE int32 [B+1], not decreasing, or NULL: one token per
- *               sequence (T == B).  Rows of y before q_start[0] and from
- *               q_start[B] on stay as they are.
+ *   q_start     DEVICE int32 [B+1], not decreasing (else y stays as it is),
+ *               or NULL: one token per sequence (T == B).  Rows of y before
+ *               q_start[0] and from q_start[B] on stay as they are; what is
+ *               outside [0, T] counts as its nearer end.
  *   kv_len      DEVICE int32 [B]; negative counts as 0, more than
  *               max_pages * page_size as that.
  *   page_table  DEVICE int32 [B][max_pages]: pages of the own keys in order.

@@ -215,6 +215,28 @@ def test_tokens_of_no_sequence_stay():
         run(cache, q, new, cached, table, ptable, hidden, 0, tail=5)
 
 
+@pytest.mark.parametrize("room,prefix", [(2, 0), (ROOM, 0), (2, 30), (ROOM, 30)])
+def test_starts_out_of_order_or_range(room, prefix):
+    rng = np.random.default_rng(4)
+    new, cached = [30, 25, 40], [40, 25, 77]
+    cache, q, table, ptable, hidden = setup(rng, new, cached, 4, 1, 64, FLOAT, 16, prefix, extra=room)
+    t = cache.tensors()
+
+    def call(starts):
+        y = torch.full((95, 4, 64), 7.0, dtype=torch.bfloat16, device=dev())
+        L.paged_attn(on_dev(q), kv_len=to_dev(np.array(cached, np.int32)), page_table=to_dev(table), y=y,
+                     q_start=to_dev(np.array(starts, np.int32)), prefix_len=prefix,
+                     prefix_table=to_dev(ptable) if prefix else None, **t)
+        torch.cuda.synchronize()
+        return y
+
+    for starts in ([0, 60, 30, 95], [95, 50, 20, 0], [0, 95, 0, 95]):
+        assert torch.all(call(starts) == 7.0)
+    # ends beyond the tokens count as the last one's
+    inside, outside = call([0, 30, 55, 95]), call([-5, 30, 55, 1000])
+    assert torch.equal(inside, outside) and not torch.any(torch.all(inside.view(95, -1) == 7.0, 1))
+
+
 @pytest.mark.parametrize("fmt", [FLOAT, BF16])
 @pytest.mark.parametrize("new,cached,room", [([1, 1], [200, 90], 2), ([70, 3], [200, 90], 2),
                                              ([70, 3], [200, 90], ROOM)])
@@ -391,6 +413,13 @@ def test_many_sequences():
     cached = [int(v) for v in rng.integers(0, 40, 700)]
     cache, q, table, ptable, hidden = setup(rng, [1] * 700, cached, 2, 1, 64, UE8M0, 16)
     run(cache, q, [1] * 700, cached, table, ptable, hidden)
+
+
+def test_as_many_sequences_as_there_may_be():
+    rng = np.random.default_rng(23)
+    cached = [int(v) for v in rng.integers(0, 20, 4096)]
+    cache, q, table, ptable, hidden = setup(rng, [1] * 4096, cached, 1, 1, 64, FLOAT, 16, extra=0)
+    run(cache, q, [1] * 4096, cached, table, ptable, hidden)
 
 
 def test_long_sequence():
