@@ -25,7 +25,7 @@
 // 5.8 TB/s; 131072 keys of one 277 MB in 50.5 us, 5.5; a large copy runs at
 // 5.1.  Many rows (attn_rows_kernel): conversions and transpositions are shared
 // through LDS, bound by issue and latency: 2 x 2048 tokens over 6000 keys 334
-// GFLOP in 471 to 520 us.
+// GFLOP in 382 to 455 us, 730 to 875 TFLOP/s; a large bf16 product runs at 1415.
 #include "bsfp8_attn.h"
 
 namespace bsfp8 {
