@@ -3,8 +3,8 @@
 Argument marshalling only: every function here takes torch device tensors,
 passes their data pointers, sizes and torch's current HIP stream to the
 C entry point of the same name, and raises ``BsFp8Error`` on a non-OK
-status.  The norm, router and MoE layer's functions check every tensor's
-type, shape, order and device first (ValueError).  Nothing is computed in
+status.  The norm, router, MoE layer's and attention's functions check every
+tensor's type, shape, order and device first (ValueError).  Nothing is computed in
 Python.  The library is loaded from the package directory; if it is missing,
 every call raises (there is no fallback path).
 """
