@@ -9,10 +9,14 @@
 // p_j in fp32, and sums of w_j (v's codes) on the matrix cores.  r is raised to
 // the row's largest log2 w_j only when some w_j passes 2^10, which the first
 // tile does and few others: the sums are rescaled then, and not at every tile.
-// E4M3 codes are exact in bf16 (keys, beside the bf16 query) and in fp16
-// (values); w_j is rounded to fp16, 2^-11 of itself, where a bf16 w_j would lose
-// as much as rounding the output does.  A bf16 value keeps its type, and w_j is
-// the sum of two bf16 numbers then (2^-16 of it lost).
+// E4M3 codes, keys' and values', are exact in bf16.  w_j is the sum of two bf16
+// numbers (2^-16 of it lost, whatever its size), and the second product is
+// taken for both: one bf16 number would lose as much as rounding the output
+// does, one of fp16 every weight that is small beside a heavier key's, which an
+// element to which that key's value adds nothing consists of (a value row of
+// zeros has the scale 1).  The second half of the products costs few rows
+// nothing (64 x 8192 112 us, 113 with it), many rows a quarter (2 x 2048 over
+// 6000 keys 385 us, 480).
 //
 // Layout.  The score tile is computed transposed, keys x rows: a lane then
 // holds 8 keys of one row, which is what the second product wants of it as an
@@ -33,8 +37,6 @@ namespace detail {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -294,15 +296,14 @@ struct Wave {
     }
   }
 
+  // The bf16 numbers of a dword's lower or upper two codes.
+  template <bool UPPER>
+  __device__ __forceinline__ static uint32_t two_codes(uint32_t c) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, UPPER));
+  }
   __device__ __forceinline__ static bf16x8 key_operand(uint2 c) {
-    if constexpr (F8) {
-      const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, 1.0f, false);
-      const bf16x2 f = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, 1.0f, true);
-      const bf16x2 i = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, false);
-      const bf16x2 j = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, true);
-      return bf16x8{e[0], e[1], f[0], f[1], i[0], i[1], j[0], j[1]};
-    }
-    return bf16x8{};
+    return __builtin_bit_cast(bf16x8, u32x4{two_codes<false>(c.x), two_codes<true>(c.x),
+                                            two_codes<false>(c.y), two_codes<true>(c.y)});
   }
 
   // A code or value that is not finite: its mark in each byte or half.
@@ -471,70 +472,51 @@ struct Wave {
       }
     }
 
-    if constexpr (F8) {
-      f16x8 wq[RT];
+    bf16x8 wh[RT], wl[RT];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
+    for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const f16x2 c = __builtin_convertvector((f32x2{w[rt][j], w[rt][j + 1]}), f16x2);
-          wq[rt][j] = c[0];
-          wq[rt][j + 1] = c[1];
-        }
+      for (int j = 0; j < 8; j += 2) {
+        const bf16x2 c = __builtin_convertvector((f32x2{w[rt][j], w[rt][j + 1]}), bf16x2);
+        const bf16x2 d = __builtin_convertvector((f32x2{w[rt][j] - (float)c[0], w[rt][j + 1] - (float)c[1]}), bf16x2);
+        wh[rt][j] = c[0];
+        wh[rt][j + 1] = c[1];
+        wl[rt][j] = d[0];
+        wl[rt][j + 1] = d[1];
+      }
+    }
+    // two values of a lane's eight keys, as the first and second operand's rows
+    auto add_values = [&](const uint32_t (&c)[8], int t) {
+      u32x4 e, f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        e[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x05040100u);
+        f[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x07060302u);
       }
 #pragma unroll
-      for (int i = 0; i < VW; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t c[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            c[j] = __builtin_bit_cast(uint32_t, h ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.v[j][i], 1.0f, true)
-                                                  : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.v[j][i], 1.0f, false));
-          u32x4 e, f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            e[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x05040100u);
-            f[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x07060302u);
-          }
-          const int t = 4 * i + 2 * h;
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, e), wq[rt], o[rt][t], 0, 0, 0);
-            o[rt][t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, f), wq[rt], o[rt][t + 1], 0, 0, 0);
-          }
-        }
-    } else {
-      bf16x8 wh[RT], wl[RT];
-#pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const bf16x2 c = __builtin_convertvector((f32x2{w[rt][j], w[rt][j + 1]}), bf16x2);
-          const bf16x2 d = __builtin_convertvector((f32x2{w[rt][j] - (float)c[0], w[rt][j + 1] - (float)c[1]}), bf16x2);
-          wh[rt][j] = c[0];
-          wh[rt][j + 1] = c[1];
-          wl[rt][j] = d[0];
-          wl[rt][j + 1] = d[1];
-        }
+        v4f& u = o[rt][t];
+        v4f& v = o[rt][t + 1];
+        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wh[rt], u, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wh[rt], v, 0, 0, 0);
+        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wl[rt], u, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wl[rt], v, 0, 0, 0);
       }
+    };
 #pragma unroll
-      for (int i = 0; i < VW; ++i) {
-        u32x4 e, f;
+    for (int i = 0; i < VW; ++i) {
+      uint32_t c[8];
+      if constexpr (F8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          e[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][i], x.v[2 * j][i], 0x05040100u);
-          f[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][i], x.v[2 * j][i], 0x07060302u);
-        }
+        for (int j = 0; j < 8; ++j) c[j] = two_codes<false>(x.v[j][i]);
+        add_values(c, 4 * i);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          v4f& u = o[rt][2 * i];
-          v4f& v = o[rt][2 * i + 1];
-          u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wh[rt], u, 0, 0, 0);
-          v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wh[rt], v, 0, 0, 0);
-          u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wl[rt], u, 0, 0, 0);
-          v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wl[rt], v, 0, 0, 0);
-        }
+        for (int j = 0; j < 8; ++j) c[j] = two_codes<true>(x.v[j][i]);
+        add_values(c, 4 * i + 2);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = x.v[j][i];
+        add_values(c, 2 * i);
       }
     }
   }
@@ -968,11 +950,9 @@ struct Rows {
       uint32_t c[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if constexpr (F8)
-          c[j] = __builtin_bit_cast(uint32_t, h ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.v[j].x, 1.0f, true)
-                                                : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.v[j].x, 1.0f, false));
-        else
-          c[j] = x.v[j][h];
+        if constexpr (F8) c[j] = h ? Wave<KV, D, 1>::template two_codes<true>(x.v[j].x)
+                                   : Wave<KV, D, 1>::template two_codes<false>(x.v[j].x);
+        else c[j] = x.v[j][h];
       }
       u32x4 e, f;
 #pragma unroll
@@ -1139,34 +1119,28 @@ struct Rows {
       if (uniform(odd)) odd_values(b, key0, w, seen);
     }
 
-    u32x4 wq[RT], wl[RT];
+    u32x4 wh[RT], wl[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const f32x2 p{w[rt][j], w[rt][j + 1]};
-        if constexpr (F8) {
-          wq[rt][j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, f16x2));
-        } else {
-          const bf16x2 c = __builtin_convertvector(p, bf16x2);
-          wq[rt][j / 2] = __builtin_bit_cast(uint32_t, c);
-          wl[rt][j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
-              (f32x2{p.x - (float)c[0], p.y - (float)c[1]}), bf16x2));
-        }
+        const bf16x2 c = __builtin_convertvector(p, bf16x2);
+        wh[rt][j / 2] = __builtin_bit_cast(uint32_t, c);
+        wl[rt][j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
+            (f32x2{p.x - (float)c[0], p.y - (float)c[1]}), bf16x2));
       }
-    auto add_values = [&](const uint4& x, int t) {
+    // four registers of sums, the weights' upper parts before the lower ones
+    auto add_values = [&](const uint4 (&x)[4], int t0) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if constexpr (F8) {
-          o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              __builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, wq[rt]), o[rt][t], 0, 0, 0);
-        } else {
-          o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, wq[rt]), o[rt][t], 0, 0, 0);
-          o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, wl[rt]), o[rt][t], 0, 0, 0);
-        }
-      }
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            o[rt][t0 + t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, x[t]), __builtin_bit_cast(bf16x8, part ? wl[rt] : wh[rt]),
+                o[rt][t0 + t], 0, 0, 0);
     };
 #pragma unroll
     for (int c = 0; c < COLS; ++c) {
@@ -1175,8 +1149,7 @@ struct Rows {
 #pragma unroll
         for (int t = 0; t < 4; ++t) z[t] = sh.v[buf][(u * NO + 4 * c + 4 + t) * 64 + lane];
       }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) add_values(v[t], 4 * c + t);
+      add_values(v, 4 * c);
 #pragma unroll
       for (int t = 0; t < 4; ++t) v[t] = z[t];
     }

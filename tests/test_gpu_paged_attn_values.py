@@ -1,0 +1,130 @@
+"""paged_attn where values, scales and scores differ widely from key to key:
+every weight keeps its precision whatever the others are."""
+
+import numpy as np
+import pytest
+import torch
+
+import attn_value_bounds as bounds
+import test_gpu_paged_attn as P
+from block_scaled_precision_fp8_amd import lib as L
+from gpu_util import bf16_bits, dev, say, to_dev
+from oracle import attn as A, formats as F
+
+pytestmark = pytest.mark.gpu
+
+FLOAT, UE8M0, BF16 = L.KV_FP8_FLOAT, L.KV_FP8_UE8M0, L.KV_BF16
+ROOM = P.ROOM
+
+
+def held(y, k, v, q, cached, table, scale, **kw):
+    """y (tensor) within its bound of the oracle's attention over the pages k, v."""
+    want, spread, reach, keys = A.attention(q, k, v, cached, table, scale, **kw)
+    live = ~np.isnan(want[:, 0, 0])
+    got = F.bf16_decode(bf16_bits(y))[live]
+    room = bounds.attention(want[live], spread[live], reach[live], keys[live], q.shape[2], np.abs(v).max())
+    off = np.abs(got - want[live])
+    assert np.all(np.isfinite(got))
+    worst = float((off / room).max())
+    say("  worst share of the bound", round(worst, 3))
+    assert worst <= 1.0
+
+
+def appended(k, v, fmt, page, spare=2, rng=None):
+    """A cache that rope_kv_append wrote (keys n, heads, D on random pages):
+    its tensors, its pages' float64 values and the table."""
+    n, H, D = k.shape
+    pages = -(-n // page) + spare
+    order = rng.permutation(pages)[:-(-n // page)].astype(np.int32)
+    slots = order[np.arange(n) // page].astype(np.int64) * page + np.arange(n) % page
+    cdt = torch.bfloat16 if fmt == BF16 else torch.uint8
+    c = lambda: torch.zeros(pages, H, page, D, dtype=cdt, device=dev())
+    s = lambda: None if fmt == BF16 else torch.zeros(
+        pages, H, page, dtype=torch.uint8 if fmt == UE8M0 else torch.float32, device=dev())
+    t = dict(k_cache=c(), v_cache=c(), k_scale=s(), v_scale=s(), kv_fmt=fmt)
+    L.rope_kv_append(None, None, k=P.on_dev(k), v=P.on_dev(v), slots=to_dev(slots), **t)
+    host = lambda x: None if x is None else (F.bf16_decode(bf16_bits(x)) if x.dtype == torch.bfloat16 else
+                                             x.cpu().numpy())
+    values = [A.cache_values(host(t[m + "_cache"]), host(t[m + "_scale"]), fmt) for m in "kv"]
+    return t, values, order
+
+
+def attend(q, t, n, order, room, **kw):
+    """The last tokens of a sequence of n keys; room: what its table has room for."""
+    T = q.shape[0]
+    table = np.full((1, len(order) + room), -1, np.int32)
+    table[0, :len(order)] = order
+    y = torch.empty(q.shape, dtype=torch.bfloat16, device=dev())
+    L.paged_attn(P.on_dev(q), kv_len=to_dev(np.array([n], np.int32)), page_table=to_dev(table), y=y,
+                 q_start=to_dev(np.array([0, T], np.int32)), **t, **kw)
+    return y, table
+
+
+def under_one_key(rng, n, T, Hq, Hkv, D, where, gap):
+    """Queries near one direction, and keys of which `where` stands some `gap` above the others."""
+    u = rng.standard_normal(D)
+    q = F.bf16_round(u + 0.2 * rng.standard_normal((T, Hq, D)))
+    k = 0.3 * rng.standard_normal((n, Hkv, D))
+    k[where] = gap * D ** 0.5 / (u @ u) * u
+    return q, F.bf16_round(k)
+
+
+@pytest.mark.parametrize("fmt", [FLOAT, UE8M0, BF16])
+@pytest.mark.parametrize("size", [1.0, 0.1, 0.03, 0.01])
+@pytest.mark.parametrize("T,room", [(1, 2), (3, 2), (48, ROOM)])
+def test_zero_value_under_the_top_score(fmt, size, T, room):
+    """A key that takes most of the weight and has a value of zeros, which the
+    codec gives the scale 1: what the others add is all of y."""
+    for D, where in ((64, 0), (128, 200), (256, 250)):
+        say("zero value", fmt, size, T, room, D, where)
+        rng = np.random.default_rng(D + T)
+        n = 300
+        q, k = under_one_key(rng, n, T, 4, 1, D, where, 10.0)
+        v = F.bf16_round(size * rng.standard_normal((n, 1, D)))
+        v[where] = 0.0
+        t, (kv, vv), order = appended(k, v, fmt, 16, rng=rng)
+        y, table = attend(q, t, n, order, room)
+        held(y, kv, vv, q, [n], table, D ** -0.5, q_start=[0, T])
+
+
+@pytest.mark.parametrize("T,room,n,gap", [(1, 0, 4096, 12.0), (12, ROOM, 4096, 12.0), (12, ROOM, 40000, 12.0)])
+def test_thousands_of_keys_under_a_zero_value(T, room, n, gap):
+    """Each of them has little weight, all together much of it."""
+    rng = np.random.default_rng(n + T)
+    D = 64
+    q, k = under_one_key(rng, n, T, 4, 1, D, 7, gap)
+    v = F.bf16_round(1.0 + 0.3 * rng.standard_normal((n, 1, D)))
+    v[7] = 0.0
+    t, (kv, vv), order = appended(k, v, FLOAT, 64, rng=rng)
+    y, table = attend(q, t, n, order, room)
+    held(y, kv, vv, q, [n], table, D ** -0.5, q_start=[0, T])
+
+
+@pytest.mark.parametrize("fmt", [FLOAT, UE8M0])
+@pytest.mark.parametrize("T,room", [(1, 2), (30, ROOM)])
+def test_elements_that_a_large_value_leaves_out(fmt, T, room):
+    """A value of far larger scale whose codes are 0 in half of the elements:
+    those are the other keys'."""
+    rng = np.random.default_rng(31)
+    for e in (20, 30, 40):
+        cache, q, table, ptable, hidden = P.setup(rng, [T], [256], 4, 1, 64, fmt, 16, extra=room)
+        codes, scale = cache.parts[1]
+        p, at = table[0, 2], 5
+        codes[p, :, at, ::2] = 0
+        scale[p, :, at] = 127 + e if fmt == UE8M0 else 2.0 ** e
+        cache.v = A.cache_values(codes, scale, fmt)
+        y = P.run(cache, q, [T], [256], table, ptable, hidden)
+        held(y, cache.k, cache.v, q, [256], table, 64 ** -0.5, q_start=[0, T])
+
+
+@pytest.mark.parametrize("case", [0, 1, 3, 4, 6, 7, 9, 10, 12, 13, 16, 17, 18, 20, 21])
+@pytest.mark.parametrize("room", [2, ROOM])
+def test_ordinary_caches(case, room):
+    """Sequences, prefixes and windows of FP8 caches within the same bound."""
+    new, cached, Hq, Hkv, D, fmt, page, prefix, window = P.SHAPES[case]
+    say("held", case, room, P.SHAPES[case])
+    rng = np.random.default_rng(case + 301)
+    cache, q, table, ptable, hidden = P.setup(rng, new, cached, Hq, Hkv, D, fmt, page, prefix, extra=room)
+    y = P.run(cache, q, new, cached, table, ptable, hidden, prefix, window)
+    held(y, cache.k, cache.v, q, cached, table, D ** -0.5, q_start=np.concatenate([[0], np.cumsum(new)]),
+         prefix_table=ptable, prefix_len=prefix, window=window)
