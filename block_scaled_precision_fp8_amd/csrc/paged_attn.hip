@@ -7,8 +7,11 @@
 // Arithmetic.  One pass over the keys in tiles of 32 with a reference
 // exponent r per row: p_j = 2^(s_j log2 e - r), w_j = p_j (v's scale), sums of
 // p_j in fp32, and sums of w_j (v's codes) on the matrix cores.  r is raised to
-// the row's largest log2 w_j only when some w_j passes 2^10, which the first
-// tile does and few others: the sums are rescaled then, and not at every tile.
+// the row's largest score only when some p_j passes 2^10, which the first tile
+// does and few others: the sums are rescaled then, and not at every tile.  It
+// goes by the scores alone: with the values' scales in it, sums of p_j over keys
+// whose scales differ by more than fp32's range would be lost, and a scale of 0
+// has no exponent.
 // E4M3 codes, keys' and values', are exact in bf16.  w_j is the sum of two bf16
 // numbers (2^-16 of it lost, whatever its size), and the second product is
 // taken for both: one bf16 number would lose as much as rounding the output
@@ -43,9 +46,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;              // keys of a wave's step
 constexpr int kUnit = 4 * kTile;       // keys of a step of four waves that split them
 constexpr float kLowest = -3.4028234663852886e38f;
-constexpr float kMostW = 1024.0f;      // a larger w raises the reference exponent
-constexpr float kMostSum = 8192.0f;    // the same of a bound of 8 of them
-constexpr float kLeastScale = -100.0f;  // log2 of the least value scale that the reference goes by
+constexpr float kMostP = 1024.0f;      // a larger p raises the reference exponent
+constexpr float kMostSum = 8192.0f;    // the same of the sum of 8 of them
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) {
   return v < lo ? lo : (v > hi ? hi : v);
@@ -416,29 +418,22 @@ struct Wave {
       float p[8];
       auto weigh = [&]() {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8; ++j)
           p[j] = __builtin_amdgcn_exp2f(fmaf(s[rt][j >> 2][j & 3], ksl[j], -ref[rt]));
-          w[rt][j] = F8 ? p[j] * x.vs[j] : p[j];
-        }
         if (!whole) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const bool ok = (seen[rt] >> j) & 1;
-            p[j] = ok ? p[j] : 0.0f;
-            w[rt][j] = ok ? w[rt][j] : 0.0f;
-          }
+          for (int j = 0; j < 8; ++j) p[j] = (seen[rt] >> j) & 1 ? p[j] : 0.0f;
         }
       };
       weigh();
-      float most = w[rt][0];
+      float most = p[0];
 #pragma unroll
-      for (int j = 1; j < 8; ++j) most = fmaxf(most, w[rt][j]);
-      if (__any(!(most <= kMostW))) {
+      for (int j = 1; j < 8; ++j) most = fmaxf(most, p[j]);
+      if (__any(!(most <= kMostP))) {
         float top = kLowest;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float e = s[rt][j >> 2][j & 3] * ksl[j];
-          if (F8) e += fmaxf(__builtin_amdgcn_logf(x.vs[j]), kLeastScale);
+          const float e = s[rt][j >> 2][j & 3] * ksl[j];
           if ((seen[rt] >> j) & 1) top = fmaxf(top, e);
         }
         top = fmaxf(ref[rt], group_max(top));
@@ -450,7 +445,12 @@ struct Wave {
         weigh();
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[rt] += p[j];
+      for (int j = 0; j < 8; ++j) {
+        sum[rt] += p[j];
+        w[rt][j] = F8 ? p[j] * x.vs[j] : p[j];
+        // a scale that the row does not use may hold anything
+        if (F8 && !whole) w[rt][j] = (seen[rt] >> j) & 1 ? w[rt][j] : 0.0f;
+      }
     }
 
     if (!whole) {
@@ -769,7 +769,6 @@ struct Rows {
     uint4 k[2][SUBS * (D / 32) * 64];
     uint4 v[2][NS * NO * 64];
     float ks[2][KT], vs[2][KT];
-    float vmost[2][SUBS];    // the largest of 16 vs
     int odd[2][W];           // values that are not finite were taken out
     int range[W][4];
   };
@@ -969,9 +968,6 @@ struct Rows {
         const float vs = KV == kKvFloat ? __uint_as_float(x.vs) : e8m0_f32(x.vs);
         sh.ks[buf][threadIdx.x] = ks * a.scale_log2;
         sh.vs[buf][threadIdx.x] = vs;
-        // sizes compare as whole numbers, NaN above all
-        const uint32_t most = row16_max(__float_as_uint(vs) & 0x7fffffffu);
-        if (n == 0) sh.vmost[buf][threadIdx.x >> 4] = __uint_as_float(most);
       }
     }
   }
@@ -1028,7 +1024,6 @@ struct Rows {
       for (int i = 0; i < D / 32; ++i) f[h][i] = sh.k[buf][((2 * u + h) * (D / 32) + i) * 64 + lane];
     __builtin_amdgcn_sched_barrier(0);
     float ksl[8], vs[8];
-    float vmost = 1.0f;
     if constexpr (F8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -1037,8 +1032,6 @@ struct Rows {
         ksl[4 * h] = c.x; ksl[4 * h + 1] = c.y; ksl[4 * h + 2] = c.z; ksl[4 * h + 3] = c.w;
         vs[4 * h] = d.x; vs[4 * h + 1] = d.y; vs[4 * h + 2] = d.z; vs[4 * h + 3] = d.w;
       }
-      const float2 m = *(const float2*)(sh.vmost[buf] + 2 * u);
-      vmost = __uint_as_float(max(__float_as_uint(m.x), __float_as_uint(m.y)));
     }
     v4f s[RT][2];
 #pragma unroll
@@ -1085,13 +1078,12 @@ struct Rows {
         add = ((w[rt][0] + w[rt][1]) + (w[rt][2] + w[rt][3])) + ((w[rt][4] + w[rt][5]) + (w[rt][6] + w[rt][7]));
       };
       weigh();
-      // the sum of p bounds every p; a scale that nobody uses may hold anything
-      if (__builtin_expect(__any(!(add * vmost <= kMostSum)), 0)) {
+      // the sum of p bounds every p
+      if (__builtin_expect(__any(!(add <= kMostSum)), 0)) {
         float top = kLowest;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float e = s[rt][j >> 2][j & 3] * (F8 ? ksl[j] : a.scale_log2);
-          if (F8) e += fmaxf(__builtin_amdgcn_logf(vs[j]), kLeastScale);
+          const float e = s[rt][j >> 2][j & 3] * (F8 ? ksl[j] : a.scale_log2);
           if ((seen[rt] >> j) & 1) top = fmaxf(top, e);
         }
         top = fmaxf(ref[rt], group_max(top));

@@ -542,8 +542,9 @@ BSFP8_API int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_
  *               the prefix; own keys begin on a page of their own.  Not
  *               looked at for prefix_len 0.
  *   k_cache .. kv_fmt, num_pages, page_size   as rope_kv_append writes them;
- *               value scales beyond 2^100 are outside the contract, those
- *               below 2^-100 lose precision.
+ *               value scales beyond 2^75 are outside the contract, those
+ *               below 2^-85 lose precision; 0 is a value of zeros.  A key
+ *               whose e^(s_j) is below 2^-126 of the largest adds nothing.
  *               What they hold behind a sequence's or the prefix's last key,
  *               or before the window, reaches no result, NaN and infinities
  *               included.

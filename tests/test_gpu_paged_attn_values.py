@@ -128,3 +128,44 @@ def test_ordinary_caches(case, room):
     y = P.run(cache, q, new, cached, table, ptable, hidden, prefix, window)
     held(y, cache.k, cache.v, q, cached, table, D ** -0.5, q_start=np.concatenate([[0], np.cumsum(new)]),
          prefix_table=ptable, prefix_len=prefix, window=window)
+
+
+@pytest.mark.parametrize("fmt", [FLOAT, UE8M0])
+@pytest.mark.parametrize("T,room", [(1, 2), (40, ROOM)])
+@pytest.mark.parametrize("first,then", [(2.0 ** -85, 2.0 ** 75), (2.0 ** 75, 2.0 ** -85), (2.0 ** -60, 2.0 ** 70)])
+def test_scales_of_both_ends_in_one_sequence(fmt, T, room, first, then):
+    """Keys of equal scores and of value scales from both ends of their range: the
+    weights' sum keeps the share of either half."""
+    rng = np.random.default_rng(41)
+    n = 1500
+    cache, q, table, ptable, hidden = P.setup(rng, [T], [n], 4, 1, 64, fmt, 16, extra=room)
+    cache.parts[0][0][:] = 0                                  # scores of 0
+    cache.k = np.zeros_like(cache.k)
+    codes, scale = cache.parts[1]
+    for j in range(n):
+        e = first if j < n // 2 else then
+        scale[table[0, j // 16], :, j % 16] = 127 + int(np.log2(e)) if fmt == UE8M0 else e
+    cache.v = A.cache_values(codes, scale, fmt)
+    t = cache.tensors()
+    P.poison(t, cache, hidden)
+    y = torch.empty(T, 4, 64, dtype=torch.bfloat16, device=dev())
+    L.paged_attn(P.on_dev(q), kv_len=to_dev(np.array([n], np.int32)), page_table=to_dev(table), y=y,
+                 q_start=to_dev(np.array([0, T], np.int32)), **t)
+    held(y, cache.k, cache.v, q, [n], table, 0.125, q_start=[0, T])
+
+
+@pytest.mark.parametrize("T,room", [(1, 2), (2, 2), (40, ROOM)])
+@pytest.mark.parametrize("D", [64, 256])
+def test_value_scales_of_zero(T, room, D):
+    """Keys whose value scales are 0 add nothing, alone in a tile or among
+    others, whatever their codes."""
+    for n, zeros in ((T, T), (T + 1, T + 1), (T + 32, T + 32), (T + 200, T), (T + 200, 60)):
+        say("zero scales", T, room, D, n, zeros)
+        rng = np.random.default_rng(n)
+        cache, q, table, ptable, hidden = P.setup(rng, [T], [n], 4, 1, D, FLOAT, 16, extra=room)
+        codes, scale = cache.parts[1]
+        for j in range(zeros):
+            scale[table[0, j // 16], :, j % 16] = 0.0
+        cache.v = A.cache_values(codes, scale, FLOAT)
+        y = P.run(cache, q, [T], [n], table, ptable, hidden)
+        held(y, cache.k, cache.v, q, [n], table, D ** -0.5, q_start=[0, T])
