@@ -33,6 +33,8 @@
 // 5.1.  Many rows (attn_rows_kernel): conversions and transpositions are shared
 // through LDS, bound by issue and latency: 2 x 2048 tokens over 6000 keys 334
 // GFLOP in 382 to 455 us, 730 to 875 TFLOP/s; a large bf16 product runs at 1415.
+#include <type_traits>
+
 #include "bsfp8_attn.h"
 
 namespace bsfp8 {
@@ -48,11 +50,30 @@ constexpr int kUnit = 4 * kTile;       // keys of a step of four waves that spli
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kMostP = 1024.0f;      // a larger p raises the reference exponent
 constexpr float kMostSum = 8192.0f;    // the same of the sum of 8 of them
+constexpr float kMostRef = 4096.0f;    // beyond: scores are rounded before the difference
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) {
   return v < lo ? lo : (v > hi ? hi : v);
 }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// 2^(s k - ref).  One fused operation where the reference is at most kMostRef
+// in size.  From there on the score is rounded first, as the reference was: of
+// scores from 2^30 on the last place is a whole power of two of the weight, and
+// 2^x of what the rounding took off passes fp32's range.  Rounded everywhere it
+// costs 3% (2 x 2048 over 6000 keys 470 us, 483), so that such rows take the
+// rare path that raises the reference at every tile instead.
+template <bool ROUNDED>
+__device__ __forceinline__ float weight(float s, float k, float ref) {
+#pragma clang fp contract(off)
+  if (!ROUNDED) return __builtin_amdgcn_exp2f(fmaf(s, k, -ref));
+  const float e = s * k;
+  return __builtin_amdgcn_exp2f(e - ref);
+}
+// What `most` may be before the raising path is taken, for a row's reference.
+__device__ __forceinline__ float limit_of(float ref, float most) {
+  return fabsf(ref) > kMostRef && ref != kLowest ? -1.0f : most;
+}
 
 // The maximum over the four lanes that share lane % 16.
 __device__ __forceinline__ float group_max(float v) {
@@ -183,6 +204,7 @@ struct Wave {
   bf16x8 q[RT][D / 32];
   v4f o[RT][DPL];
   float ref[RT], sum[RT];
+  float most_p[RT];          // a larger p, and the reference is looked at
   int lo[RT], hi[RT];        // the lane's row's visible keys
   int lo_most, lo_least, hi_least, hi_most;        // over the wave's rows
   int lane, n, g;
@@ -222,6 +244,7 @@ struct Wave {
       for (int t = 0; t < DPL; ++t) o[rt][t] = v4f{0, 0, 0, 0};
       ref[rt] = kLowest;
       sum[rt] = 0.0f;
+      most_p[rt] = kMostP;
     }
     lo_most = uniform(row16_max(lom));
     lo_least = -uniform(row16_max(-lol));
@@ -416,20 +439,20 @@ struct Wave {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float p[8];
-      auto weigh = [&]() {
+      auto weigh = [&](auto rounded) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          p[j] = __builtin_amdgcn_exp2f(fmaf(s[rt][j >> 2][j & 3], ksl[j], -ref[rt]));
+          p[j] = weight<decltype(rounded)::value>(s[rt][j >> 2][j & 3], ksl[j], ref[rt]);
         if (!whole) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) p[j] = (seen[rt] >> j) & 1 ? p[j] : 0.0f;
         }
       };
-      weigh();
+      weigh(std::false_type());
       float most = p[0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) most = fmaxf(most, p[j]);
-      if (__any(!(most <= kMostP))) {
+      if (__any(!(most <= most_p[rt]))) {
         float top = kLowest;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -442,7 +465,8 @@ struct Wave {
         sum[rt] *= down;
 #pragma unroll
         for (int t = 0; t < DPL; ++t) o[rt][t] *= down;
-        weigh();
+        most_p[rt] = limit_of(top, kMostP);
+        weigh(std::true_type());
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -783,6 +807,7 @@ struct Rows {
   bf16x8 q[RT][D / 32];
   v4f o[RT][NO];             // o[4 i + t][r]: value 64 i + 16 g + 4 r + t
   float ref[RT], sum[RT];
+  float most_sum[RT];        // a larger sum of p, and the reference is looked at
   int lo[RT], hi[RT];
   int lo_most, lo_least, hi_least, hi_most;        // of the workgroup's rows
   int wave, lane, n, g;
@@ -821,6 +846,7 @@ struct Rows {
       for (int t = 0; t < NO; ++t) o[rt][t] = v4f{0, 0, 0, 0};
       ref[rt] = kLowest;
       sum[rt] = 0.0f;
+      most_sum[rt] = kMostSum;
     }
     lom = row16_max(lom);
     lol = -row16_max(-lol);
@@ -1067,19 +1093,19 @@ struct Rows {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float add;
-      auto weigh = [&]() {
+      auto weigh = [&](auto rounded) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          w[rt][j] = __builtin_amdgcn_exp2f(fmaf(s[rt][j >> 2][j & 3], F8 ? ksl[j] : a.scale_log2, -ref[rt]));
+          w[rt][j] = weight<decltype(rounded)::value>(s[rt][j >> 2][j & 3], F8 ? ksl[j] : a.scale_log2, ref[rt]);
         if (EDGE) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[rt][j] = (seen[rt] >> j) & 1 ? w[rt][j] : 0.0f;
         }
         add = ((w[rt][0] + w[rt][1]) + (w[rt][2] + w[rt][3])) + ((w[rt][4] + w[rt][5]) + (w[rt][6] + w[rt][7]));
       };
-      weigh();
+      weigh(std::false_type());
       // the sum of p bounds every p
-      if (__builtin_expect(__any(!(add <= kMostSum)), 0)) {
+      if (__builtin_expect(__any(!(add <= most_sum[rt])), 0)) {
         float top = kLowest;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -1092,7 +1118,8 @@ struct Rows {
         sum[rt] *= down;
 #pragma unroll
         for (int t = 0; t < NO; ++t) o[rt][t] *= down;
-        weigh();
+        most_sum[rt] = limit_of(top, kMostSum);
+        weigh(std::true_type());
       }
       sum[rt] += add;
       if constexpr (F8) {

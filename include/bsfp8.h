@@ -548,7 +548,8 @@ BSFP8_API int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_
  *               What they hold behind a sequence's or the prefix's last key,
  *               or before the window, reaches no result, NaN and infinities
  *               included.
- *   scale       > 0.  window  0: none.
+ *   scale       > 0; scores beyond fp32's range are outside the contract.
+ *   window      0: none.
  *   y           out, bf16 [T][Hq][D] (dense); must not overlap an input.
  *   workspace   >= paged_attn_workspace_size(...) bytes, 16-byte aligned;
  *               nothing in it is kept from one call to the next.  Calls that

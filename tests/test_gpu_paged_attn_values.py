@@ -169,3 +169,52 @@ def test_value_scales_of_zero(T, room, D):
         cache.v = A.cache_values(codes, scale, FLOAT)
         y = P.run(cache, q, [T], [n], table, ptable, hidden)
         held(y, cache.k, cache.v, q, [n], table, D ** -0.5, q_start=[0, T])
+
+
+@pytest.mark.parametrize("fmt", [FLOAT, UE8M0, BF16])
+@pytest.mark.parametrize("T,room", [(1, 2), (40, ROOM)])
+@pytest.mark.parametrize("scale", [1e5, 1e8, 1e11, 1e15, 1e30])
+def test_scores_that_only_one_key_survives(fmt, T, room, scale):
+    """Scores so large that their own rounding is whole exponents: the key
+    with the largest has all the weight."""
+    rng = np.random.default_rng(51)
+    n, D = 700, 64
+    for where in (0, 333, n - T):
+        u = np.ones(D)
+        u[::2] = -1.0
+        q = F.bf16_round(u * (1.0 + rng.random((T, 4, 1))))
+        k = rng.standard_normal((n, 1, D)) * 0.1
+        k[where] = 1.5 * u                                    # by far the largest score of every row
+        v = F.bf16_round(rng.standard_normal((n, 1, D)))
+        t, (kv, vv), order = appended(F.bf16_round(k), v, fmt, 16, rng=rng)
+        y, table = attend(q, t, n, order, room, scale=scale)
+        at = vv[order[where // 16], 0, where % 16]
+        got = F.bf16_decode(bf16_bits(y))
+        assert np.all(np.isfinite(got))
+        # the weight is 2^0 or, before a reference that rises, at most 2^10 of its own reference; the sums
+        # are of one term: two roundings of 2^-16 and one to bf16
+        assert np.all(np.abs(got - at) <= (bounds.BF16 * 1.01 + 2.0 ** -14) * np.abs(at))
+
+
+@pytest.mark.parametrize("T,room", [(1, 2), (40, ROOM)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_equal_scores_of_any_size(T, room, sign):
+    """Equal keys have equal weights, however large their scores are."""
+    n, D = 700, 64
+    rng = np.random.default_rng(52)
+    q = F.bf16_round(1.0 + rng.random((T, 4, D)))
+    k = np.full((n, 1, D), sign * 1.234)
+    v = F.bf16_round(rng.standard_normal((n, 1, D)))
+    for fmt in (FLOAT, BF16):
+        t, (kv, vv), order = appended(F.bf16_round(k), v, fmt, 16, rng=rng)
+        at = vv[order[np.arange(n) // 16], 0, np.arange(n) % 16]
+        for scale in (1.0, 1e4, 1e8, 1e11, 1e15, 1e30):
+            y, table = attend(q, t, n, order, room, scale=scale)
+            got = F.bf16_decode(bf16_bits(y))
+            assert np.all(np.isfinite(got)), (fmt, scale)
+            for i in range(T):
+                see = at[:n - T + 1 + i]
+                want, spread = see.mean(0), np.abs(see).mean(0)
+                # equal products and sums: no error in the scores; weights 2^-16, fp32 sums 2^-24 a key
+                room_ = bounds.BF16 * np.abs(want) + 1.01 * spread * (2.0 ** -15 + 2 * n * 2.0 ** -24)
+                assert np.all(np.abs(got[i] - want) <= room_), (fmt, scale)
