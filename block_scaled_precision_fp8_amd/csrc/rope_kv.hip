@@ -188,13 +188,14 @@ hipError_t launch_rope_kv(const RopeKvArgs& a, hipStream_t s) {
 __global__ void inv_freq_kernel(int scaling, int rot, double base, double factor, double low,
                                 double high, double orig_len, float* out) {
   for (int i = threadIdx.x; i < rot / 2; i += blockDim.x) {
-    double f = pow(base, -2.0 * i / rot);
+    const double f = pow(base, -2.0 * i / rot);
     double keep = scaling == 0 ? 1.0 : 0.0;
     if (scaling == 2) {
       const double r = orig_len * f * 0.15915494309189533577;
       keep = fmin(fmax((r - low) / (high - low), 0.0), 1.0);
     }
-    out[i] = (float)(f * keep + f / factor * (1.0 - keep));
+    // a factor that nothing is divided by may be anything
+    out[i] = (float)(keep == 1.0 ? f : f * keep + f / factor * (1.0 - keep));
   }
 }
 

@@ -194,3 +194,15 @@ def test_inv_freq(scaling, kw, rot):
     want = A.inv_freq(rot, 500000.0, scaling, **kw).astype(np.float64)
     # both round a 64-bit value that pow() may have off by some 2^-50
     assert np.all(np.abs(out.cpu().numpy() - want) <= 2.0 ** -23 * want)
+
+
+@pytest.mark.parametrize("scaling,kw", [
+    (0, dict(factor=0.0)), (0, dict(factor=float("nan"))),
+    (0, dict(factor=-1.0, low=float("nan"), high=float("nan"), orig_len=float("nan"))),
+    (1, dict(factor=4.0, low=float("nan"), high=float("nan"), orig_len=float("nan"))),
+    (2, dict(factor=5e-324, low=1.0, high=1.5, orig_len=1e30))])          # every angle keeps its own
+def test_inv_freq_looks_at_what_its_scaling_uses(scaling, kw):
+    out = torch.empty(64, device=dev())
+    L.rope_inv_freq(out, base=500000.0, scaling=scaling, **kw)
+    want = A.inv_freq(128, 500000.0, 1 if scaling == 1 else 0, factor=4.0).astype(np.float64)
+    assert np.all(np.abs(out.cpu().numpy() - want) <= 2.0 ** -23 * want)
