@@ -41,6 +41,7 @@ struct AttnPlan {
   int own_splits, pre_splits;            // of a wide block's keys
   int own_groups;                        // workgroups of the launch that splits keys evenly
   int64_t own_slots, pre_slots;          // partial results
+  bool complete;             // the one launch writes all of y, and no partial result
   size_t off_ml, off_part, bytes;
 };
 

@@ -1499,7 +1499,7 @@ hipError_t launch_attn(AttnArgs a, hipStream_t s) {
     hipLaunchKernelGGL((attn_split_kernel<KV, D, true>), dim3(p.own_groups), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((attn_split_kernel<KV, D, false>), dim3(p.own_groups), dim3(256), 0, s, a);
-  if (p.own_wide && p.own_splits == 1 && a.prefix_len == 0) return hipGetLastError();   // y is complete
+  if (p.complete) return hipGetLastError();
   const int64_t rows = (int64_t)a.T * a.Hq;
   // four waves a row, or one: 256 rows of 4096 keys 25.0 us and 25.6, one row in
   // a hundred partial results 32.6 and 37.3; 2048 rows 34.7 and 33.2, 16384 85 and 74
@@ -1556,6 +1556,7 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
   p.pre_blocks = prefix_len > 0 ? (int)up(rows, p.pre_rows) : 0;
   if (p.own_wide) {
     p.own_splits = splits(p.own_blocks, p.own_waves, keys);
+    p.complete = p.own_splits == 1 && prefix_len == 0;   // rows in one piece, and nothing to join them with
     p.own_slots = (int64_t)p.own_blocks * Hkv * p.own_splits;
   } else {
     const int64_t own = up(keys, kUnit) * (rows / 16 + B) * Hkv;
@@ -1574,7 +1575,8 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
   const int64_t prow = p.own_slots * p.own_rows + p.pre_slots * p.pre_rows;
   p.off_ml = aligned((size_t)(p.own_blocks + p.pre_blocks) * Hkv * sizeof(int2));
   p.off_part = p.off_ml + aligned((size_t)prow * sizeof(float2));
-  p.bytes = p.off_part + (size_t)prow * D * sizeof(float);
+  // complete rows leave no partial sums (1.1 GB for 32768 tokens of 64 heads of 128)
+  p.bytes = p.off_part + (p.complete ? 0 : (size_t)prow * D * sizeof(float));
   return p;
 }
 

@@ -160,3 +160,16 @@ def test_workspace_holds_what_the_kernels_write():
                     # at least one partial result for every row of one source, with its head's copies
                     assert need < 2**63 and need >= rows * Hkv * 8
     assert _need(T=0) == 0 and _need(B=0, T=0) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=32768, B=8, Hq=64, Hkv=8, most=2048, page=16, pre=0), dict(T=8192, B=1, Hq=32, Hkv=8, most=512, pre=0),
+    dict(T=576, B=64, Hq=16, Hkv=4, D=64, most=4, pre=0), dict(T=4096, B=2, Hq=16, Hkv=16, D=256, most=256, pre=0)])
+def test_workspace_of_complete_rows(kw):
+    """Where no row's keys are split and no prefix is there, y is written at
+    once: a pair of numbers per block and per row (in blocks of up to 256) of
+    each key head, no partial sums of D values."""
+    a = dict(SIZES, **kw)
+    rows = a["T"] * (a["Hq"] // a["Hkv"])
+    assert 0 < _need(**kw) <= (rows + 256 * a["B"] + rows // 64 + a["B"]) * a["Hkv"] * 8 + 4096
+    assert _need(**{**kw, "pre": 16}) > rows * a["Hkv"] * a["D"] * 4            # the prefix's and their own

@@ -218,3 +218,25 @@ def test_equal_scores_of_any_size(T, room, sign):
                 # equal products and sums: no error in the scores; weights 2^-16, fp32 sums 2^-24 a key
                 room_ = bounds.BF16 * np.abs(want) + 1.01 * spread * (2.0 ** -15 + 2 * n * 2.0 ** -24)
                 assert np.all(np.abs(got[i] - want) <= room_), (fmt, scale)
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_rows_that_need_no_partial_sums(D):
+    """Many short sequences, each row's keys in one piece: a workspace without
+    partial sums, and nothing behind it is touched."""
+    rng = np.random.default_rng(61)
+    B, n, Hq, Hkv = 64, 9, 16, 4
+    cached = [int(v) for v in rng.integers(0, 60, B)]
+    cache, q, table, ptable, hidden = P.setup(rng, [n] * B, cached, Hq, Hkv, D, FLOAT, 16, extra=0)
+    need = L.paged_attn_workspace_size(B * n, B, Hq, Hkv, D, table.shape[1], 16)
+    assert need < B * n * Hq * D * 4                          # a partial sum per row would be more
+    t = cache.tensors()
+    P.poison(t, cache, hidden)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=dev())
+    y = torch.empty(B * n, Hq, D, dtype=torch.bfloat16, device=dev())
+    start = np.arange(B + 1) * n
+    L.paged_attn(P.on_dev(q), kv_len=to_dev(np.array(cached, np.int32)), page_table=to_dev(table), y=y,
+                 q_start=to_dev(start.astype(np.int32)), workspace=ws[:need], **t)
+    torch.cuda.synchronize()
+    assert torch.all(ws[need:] == 0xA5)
+    held(y, cache.k, cache.v, q, cached, table, D ** -0.5, q_start=start)
