@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import attn_value_bounds as bounds
+import test_gpu_attn_layer as layers
 import test_gpu_paged_attn as P
 from block_scaled_precision_fp8_amd import lib as L
 from gpu_util import bf16_bits, dev, say, to_dev
@@ -240,3 +241,26 @@ def test_rows_that_need_no_partial_sums(D):
     torch.cuda.synchronize()
     assert torch.all(ws[need:] == 0xA5)
     held(y, cache.k, cache.v, q, cached, table, D ** -0.5, q_start=start)
+
+
+@pytest.mark.parametrize("fmt", [FLOAT, UE8M0, BF16])
+def test_a_layers_attention_within_its_roundings(fmt):
+    """Norm to output linear: two prompts, then a token each, y within the
+    attention's own roundings of what the cache holds."""
+    rng = np.random.default_rng(70 + fmt)
+    layer = layers.Layer(rng, fmt)
+    table = rng.permutation(layers.PAGES)[:12].reshape(2, 6)
+    td = layers.i32(table.tolist())
+    slot = lambda b, j: int(table[b, j // layers.PAGE]) * layers.PAGE + j % layers.PAGE
+    lens, new = [0, 0], [50, 21]
+    for _ in range(3):
+        at = [(b, lens[b] + j) for b in range(2) for j in range(new[b])]
+        lens = [l + n for l, n in zip(lens, new)]
+        start = np.concatenate([[0], np.cumsum(new)])
+        x = P.on_dev(rng.standard_normal((len(at), layers.H)))
+        q, y, _ = layer.step(x, layers.i32([j for _, j in at]),
+                             torch.tensor([slot(b, j) for b, j in at], device=dev()), kv_len=layers.i32(lens),
+                             page_table=td, q_start=layers.i32(start.tolist()))
+        k, v = layer.values()
+        held(y, k, v, F.bf16_decode(bf16_bits(q.contiguous())), lens, table, layers.D ** -0.5, q_start=start)
+        new = [1, 1]
