@@ -183,7 +183,7 @@ __device__ __forceinline__ void row_range(const AttnArgs& a, const Block& b, int
 
 // ----------------------------------------------------------- a wave's rows
 
-template <int KV, int D, int RT, bool STREAM = false>
+template <int KV, int D, bool STREAM = false>
 struct Wave {
   static constexpr bool F8 = KV != kKvBf16;
   static constexpr int ES = F8 ? 1 : 2;            // bytes of a cached value
@@ -201,11 +201,11 @@ struct Wave {
   };
 
   const AttnArgs& a;
-  bf16x8 q[RT][D / 32];
-  v4f o[RT][DPL];
-  float ref[RT], sum[RT];
-  float most_p[RT];          // a larger p, and the reference is looked at
-  int lo[RT], hi[RT];        // the lane's row's visible keys
+  bf16x8 q[D / 32];
+  v4f o[DPL];
+  float ref, sum;
+  float most_p;              // a larger p, and the reference is looked at
+  int lo, hi;                // the lane's row's visible keys
   int lo_most, lo_least, hi_least, hi_most;        // over the wave's rows
   int lane, n, g;
 
@@ -215,41 +215,30 @@ struct Wave {
     g = lane >> 4;
   }
 
-  // Queries and visible keys of rows row0 + 16 rt + n of the block.
-  __device__ __forceinline__ void begin(const Block& b, int row0) {
-    int lom = 0, lol = 0x7fffffff, hil = 0x7fffffff, him = 0;
+  // Query and visible keys of row n of the block.
+  __device__ __forceinline__ void begin(const Block& b) {
+    const bool live = n < b.rows;
+    const int i = live ? (b.row0 + n) / a.G : 0;
+    const int head = b.h * a.G + (b.row0 + n - i * a.G);
+    lo = hi = 0;
+    if (live) row_range(a, b, n, &lo, &hi);
+    const uint16_t* src = a.q + (int64_t)(b.q0 + i) * a.ldq + (int64_t)head * D;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = row0 + 16 * rt + n;
-      const bool live = r < b.rows;
-      const int i = live ? (b.row0 + r) / a.G : 0;
-      const int head = b.h * a.G + (b.row0 + r - i * a.G);
-      lo[rt] = hi[rt] = 0;
-      if (live) {
-        row_range(a, b, r, &lo[rt], &hi[rt]);
-        lom = max(lom, lo[rt]);
-        lol = min(lol, lo[rt]);
-        hil = min(hil, hi[rt]);
-        him = max(him, hi[rt]);
-      }
-      const uint16_t* src = a.q + (int64_t)(b.q0 + i) * a.ldq + (int64_t)head * D;
-#pragma unroll
-      for (int s = 0; s < D / 32; ++s) {
-        const int d = F8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) v = *(const uint4*)(src + d);
-        q[rt][s] = __builtin_bit_cast(bf16x8, v);
-      }
-#pragma unroll
-      for (int t = 0; t < DPL; ++t) o[rt][t] = v4f{0, 0, 0, 0};
-      ref[rt] = kLowest;
-      sum[rt] = 0.0f;
-      most_p[rt] = kMostP;
+    for (int s = 0; s < D / 32; ++s) {
+      const int d = F8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (live) v = *(const uint4*)(src + d);
+      q[s] = __builtin_bit_cast(bf16x8, v);
     }
-    lo_most = uniform(row16_max(lom));
-    lo_least = -uniform(row16_max(-lol));
-    hi_least = -uniform(row16_max(-hil));
-    hi_most = uniform(row16_max(him));
+#pragma unroll
+    for (int t = 0; t < DPL; ++t) o[t] = v4f{0, 0, 0, 0};
+    ref = kLowest;
+    sum = 0.0f;
+    most_p = kMostP;
+    lo_most = uniform(row16_max(lo));
+    lo_least = -uniform(row16_max(live ? -lo : -0x7fffffff));
+    hi_least = -uniform(row16_max(live ? -hi : -0x7fffffff));
+    hi_most = uniform(row16_max(hi));
   }
 
   // Page ids of the 32 tiles tile0, tile0 + step, ..: lane 2 i + s has that
@@ -341,7 +330,7 @@ struct Wave {
   // they are taken out of the tile (0 w would not be 0) and added, one by one,
   // to the rows that see them.
   __device__ __forceinline__ void odd_values(const Block& b, int tile, Raw& x,
-                                             const float (&w)[RT][8], const uint32_t (&seen)[RT]) {
+                                             const float (&w)[8], uint32_t seen) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -357,31 +346,28 @@ struct Wave {
       const int id = s ? x.id[1] : x.id[0];
       if (id < 0) continue;
       const int64_t row = (((int64_t)id * a.Hkv + b.h) << a.log2_page) + ((tile * kTile + k) & in_page);
+      float mine = w[0];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        float mine = w[rt][0];
+      for (int i = 1; i < 8; ++i) mine = i == j ? w[i] : mine;
+      const float wk = __shfl(mine, from);
+      const bool sees = (__shfl((int)seen, from) >> j) & 1;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) mine = i == j ? w[rt][i] : mine;
-        const float wk = __shfl(mine, from);
-        const bool sees = (__shfl((int)seen[rt], from) >> j) & 1;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int t = 0; t < DPL; ++t) {
-            const int64_t at = row * D + DPL * (4 * g + i) + t;
-            float val = 0.0f;
-            bool odd;
-            if (F8) {
-              odd = (a.vc[at] & 0x7fu) == 0x7fu;
-              if (odd) val = __uint_as_float(0x7fc00000u);
-            } else {
-              const uint32_t bits = ((const uint16_t*)a.vc)[at];
-              odd = (bits & 0x7f80u) == 0x7f80u;
-              val = __uint_as_float(bits << 16);
-            }
-            if (sees && odd) o[rt][t][i] += wk * val;
+        for (int t = 0; t < DPL; ++t) {
+          const int64_t at = row * D + DPL * (4 * g + i) + t;
+          float val = 0.0f;
+          bool odd;
+          if (F8) {
+            odd = (a.vc[at] & 0x7fu) == 0x7fu;
+            if (odd) val = __uint_as_float(0x7fc00000u);
+          } else {
+            const uint32_t bits = ((const uint16_t*)a.vc)[at];
+            odd = (bits & 0x7f80u) == 0x7f80u;
+            val = __uint_as_float(bits << 16);
           }
-      }
+          if (sees && odd) o[t][i] += wk * val;
+        }
     }
   }
 
@@ -389,9 +375,7 @@ struct Wave {
     const int key0 = tile * kTile;
     const bool whole = uniform(x.id[0] >= 0 && x.id[1] >= 0 && key0 >= lo_most && key0 + kTile <= hi_least);
 
-    v4f s[RT][2];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = v4f{0, 0, 0, 0};
+    v4f s[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -403,9 +387,7 @@ struct Wave {
         } else {
           k = __builtin_bit_cast(bf16x8, x.k[h][i]);
         }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[rt][i], s[rt][h], 0, 0, 0);
+        s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[i], s[h], 0, 0, 0);
       }
 
     if constexpr (KV == kKvUe8m0) {
@@ -419,62 +401,57 @@ struct Wave {
 #pragma unroll
     for (int j = 0; j < 8; ++j) ksl[j] = F8 ? x.ks[j] * a.scale_log2 : a.scale_log2;
 
-    float w[RT][8];
-    uint32_t seen[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      seen[rt] = 0xffu;
-      if (!whole) {
-        int g = this->g;               // as above
-        asm volatile("" : "+v"(g));
-        seen[rt] = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
-          const bool ok = x.id[j >> 2] >= 0 && key >= lo[rt] && key < hi[rt];
-          seen[rt] |= (uint32_t)ok << j;
-        }
-      }
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      float p[8];
-      auto weigh = [&](auto rounded) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          p[j] = weight<decltype(rounded)::value>(s[rt][j >> 2][j & 3], ksl[j], ref[rt]);
-        if (!whole) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] = (seen[rt] >> j) & 1 ? p[j] : 0.0f;
-        }
-      };
-      weigh(std::false_type());
-      float most = p[0];
-#pragma unroll
-      for (int j = 1; j < 8; ++j) most = fmaxf(most, p[j]);
-      if (__any(!(most <= most_p[rt]))) {
-        float top = kLowest;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float e = s[rt][j >> 2][j & 3] * ksl[j];
-          if ((seen[rt] >> j) & 1) top = fmaxf(top, e);
-        }
-        top = fmaxf(ref[rt], group_max(top));
-        const float down = __builtin_amdgcn_exp2f(ref[rt] - top);
-        ref[rt] = top;
-        sum[rt] *= down;
-#pragma unroll
-        for (int t = 0; t < DPL; ++t) o[rt][t] *= down;
-        most_p[rt] = limit_of(top, kMostP);
-        weigh(std::true_type());
-      }
+    uint32_t seen = 0xffu;
+    if (!whole) {
+      int g = this->g;                 // as above
+      asm volatile("" : "+v"(g));
+      seen = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sum[rt] += p[j];
-        w[rt][j] = F8 ? p[j] * x.vs[j] : p[j];
-        // a scale that the row does not use may hold anything
-        if (F8 && !whole) w[rt][j] = (seen[rt] >> j) & 1 ? w[rt][j] : 0.0f;
+        const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
+        const bool ok = x.id[j >> 2] >= 0 && key >= lo && key < hi;
+        seen |= (uint32_t)ok << j;
       }
+    }
+    float p[8];
+    auto weigh = [&](auto rounded) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        p[j] = weight<decltype(rounded)::value>(s[j >> 2][j & 3], ksl[j], ref);
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = (seen >> j) & 1 ? p[j] : 0.0f;
+      }
+    };
+    weigh(std::false_type());
+    float most = p[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) most = fmaxf(most, p[j]);
+    if (__any(!(most <= most_p))) {
+      float top = kLowest;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float e = s[j >> 2][j & 3] * ksl[j];
+        if ((seen >> j) & 1) top = fmaxf(top, e);
+      }
+      top = fmaxf(ref, group_max(top));
+      const float down = __builtin_amdgcn_exp2f(ref - top);
+      ref = top;
+      sum *= down;
+#pragma unroll
+      for (int t = 0; t < DPL; ++t) o[t] *= down;
+      most_p = limit_of(top, kMostP);
+      weigh(std::true_type());
+    }
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += p[j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = F8 ? p[j] * x.vs[j] : p[j];
+    // a scale that the row does not use may hold anything
+    if (F8 && !whole) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = (seen >> j) & 1 ? w[j] : 0.0f;
     }
 
     if (!whole) {
@@ -496,18 +473,15 @@ struct Wave {
       }
     }
 
-    bf16x8 wh[RT], wl[RT];
+    bf16x8 wh, wl;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const bf16x2 c = __builtin_convertvector((f32x2{w[rt][j], w[rt][j + 1]}), bf16x2);
-        const bf16x2 d = __builtin_convertvector((f32x2{w[rt][j] - (float)c[0], w[rt][j + 1] - (float)c[1]}), bf16x2);
-        wh[rt][j] = c[0];
-        wh[rt][j + 1] = c[1];
-        wl[rt][j] = d[0];
-        wl[rt][j + 1] = d[1];
-      }
+    for (int j = 0; j < 8; j += 2) {
+      const bf16x2 c = __builtin_convertvector((f32x2{w[j], w[j + 1]}), bf16x2);
+      const bf16x2 d = __builtin_convertvector((f32x2{w[j] - (float)c[0], w[j + 1] - (float)c[1]}), bf16x2);
+      wh[j] = c[0];
+      wh[j + 1] = c[1];
+      wl[j] = d[0];
+      wl[j + 1] = d[1];
     }
     // two values of a lane's eight keys, as the first and second operand's rows
     auto add_values = [&](const uint32_t (&c)[8], int t) {
@@ -517,15 +491,12 @@ struct Wave {
         e[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x05040100u);
         f[j] = __builtin_amdgcn_perm(c[2 * j + 1], c[2 * j], 0x07060302u);
       }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        v4f& u = o[rt][t];
-        v4f& v = o[rt][t + 1];
-        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wh[rt], u, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wh[rt], v, 0, 0, 0);
-        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wl[rt], u, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wl[rt], v, 0, 0, 0);
-      }
+      v4f& u = o[t];
+      v4f& v = o[t + 1];
+      u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wh, u, 0, 0, 0);
+      v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wh, v, 0, 0, 0);
+      u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e), wl, u, 0, 0, 0);
+      v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), wl, v, 0, 0, 0);
     };
 #pragma unroll
     for (int i = 0; i < VW; ++i) {
@@ -564,19 +535,16 @@ struct Wave {
            __builtin_amdgcn_readlane(ids, at + 1), x);
       tile(b, first + i * step, x);
     }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) sum[rt] = group_sum(sum[rt]);
+    sum = group_sum(sum);
   }
 
   // The lane's 4 DPL values of a row: y, or a partial result.
-  __device__ __forceinline__ void out_row(const Block& b, int row0, int rt, int64_t slot,
-                                          int block_rows, bool direct) const {
-    const int r = row0 + 16 * rt + n;
-    if (r >= b.rows) return;
+  __device__ __forceinline__ void out_row(const Block& b, int64_t slot, bool direct) const {
+    if (n >= b.rows) return;
     if (direct) {
-      const int i = (b.row0 + r) / a.G;
-      const int head = b.h * a.G + (b.row0 + r - i * a.G);
-      const float f = sum[rt] == 0.0f ? 0.0f : 1.0f / sum[rt];
+      const int i = (b.row0 + n) / a.G;
+      const int head = b.h * a.G + (b.row0 + n - i * a.G);
+      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
       uint16_t* y = a.y + ((int64_t)(b.q0 + i) * a.Hq + head) * D + 4 * DPL * g;
 #pragma unroll
       for (int i4 = 0; i4 < 4; ++i4) {
@@ -584,7 +552,7 @@ struct Wave {
 #pragma unroll
         for (int t = 0; t < DPL; t += 2)
           c[t / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
-              (f32x2{o[rt][t][i4] * f, o[rt][t + 1][i4] * f}), bf16x2));
+              (f32x2{o[t][i4] * f, o[t + 1][i4] * f}), bf16x2));
         uint16_t* p = y + DPL * i4;
         if constexpr (DPL == 4) *(uint2*)p = make_uint2(c[0], c[1]);
         else
@@ -592,14 +560,14 @@ struct Wave {
           for (int t = 0; t < DPL / 2; t += 4) *(uint4*)(p + 2 * t) = make_uint4(c[t], c[t + 1], c[t + 2], c[t + 3]);
       }
     } else {
-      const int64_t at = slot * block_rows + r;
-      if (g == 0) a.ml[at] = make_float2(ref[rt], sum[rt]);
+      const int64_t at = slot * 16 + n;
+      if (g == 0) a.ml[at] = make_float2(ref, sum);
       float* p = a.part + at * D + 4 * DPL * g;
 #pragma unroll
       for (int i4 = 0; i4 < 4; ++i4)
 #pragma unroll
         for (int t = 0; t < DPL; t += 4)
-          *(float4*)(p + DPL * i4 + t) = make_float4(o[rt][t][i4], o[rt][t + 1][i4], o[rt][t + 2][i4], o[rt][t + 3][i4]);
+          *(float4*)(p + DPL * i4 + t) = make_float4(o[t][i4], o[t + 1][i4], o[t + 2][i4], o[t + 3][i4]);
     }
   }
 };
@@ -682,7 +650,7 @@ __global__ __launch_bounds__(256, split_resident(KV, D)) void attn_split_kernel(
     b = uniform(b);
   }
 
-  Wave<KV, D, 1, STREAM> w(a);
+  Wave<KV, D, STREAM> w(a);
   while (x < xe) {
     while (b + 1 < items && uniform(before[b + 1]) <= x) ++b;
     Block k;
@@ -729,7 +697,7 @@ __global__ __launch_bounds__(256, split_resident(KV, D)) void attn_split_kernel(
     const int64_t slot = (int64_t)blockIdx.x + id;
     if (u == 0 && tid == 0) a.meta[id] = make_int2(w0 + id, direct ? -1 : w1 - w0 + 1);
 
-    w.begin(k, 0);
+    w.begin(k);
     w.walk(k, (unit0 + u) * 4 + wave, (unit0 + ue) * 4, 4);
 
     // the waves' sums in two steps: 2 and 3 to 0 and 1, then 1 to 0
@@ -742,31 +710,31 @@ __global__ __launch_bounds__(256, split_resident(KV, D)) void attn_split_kernel(
 #pragma unroll
           for (int t = 0; t < DPL; t += 4)
             *(float4*)(m + DPL * (4 * w.g + i) + t) =
-                make_float4(w.o[0][t][i], w.o[0][t + 1][i], w.o[0][t + 2][i], w.o[0][t + 3][i]);
-        if (w.g == 0) merge_ml[wave - step][w.n] = make_float2(w.ref[0], w.sum[0]);
+                make_float4(w.o[t][i], w.o[t + 1][i], w.o[t + 2][i], w.o[t + 3][i]);
+        if (w.g == 0) merge_ml[wave - step][w.n] = make_float2(w.ref, w.sum);
       }
       __syncthreads();
       if (wave < step) {
         const float* m = merge[wave][w.n];
         const float2 e = merge_ml[wave][w.n];
-        const float top = fmaxf(w.ref[0], e.x);
-        const float f0 = __builtin_amdgcn_exp2f(w.ref[0] - top), f1 = __builtin_amdgcn_exp2f(e.x - top);
-        w.ref[0] = top;
-        w.sum[0] = w.sum[0] * f0 + e.y * f1;
+        const float top = fmaxf(w.ref, e.x);
+        const float f0 = __builtin_amdgcn_exp2f(w.ref - top), f1 = __builtin_amdgcn_exp2f(e.x - top);
+        w.ref = top;
+        w.sum = w.sum * f0 + e.y * f1;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int t = 0; t < DPL; t += 4) {
             const float4 c = *(const float4*)(m + DPL * (4 * w.g + i) + t);
-            w.o[0][t][i] = w.o[0][t][i] * f0 + c.x * f1;
-            w.o[0][t + 1][i] = w.o[0][t + 1][i] * f0 + c.y * f1;
-            w.o[0][t + 2][i] = w.o[0][t + 2][i] * f0 + c.z * f1;
-            w.o[0][t + 3][i] = w.o[0][t + 3][i] * f0 + c.w * f1;
+            w.o[t][i] = w.o[t][i] * f0 + c.x * f1;
+            w.o[t + 1][i] = w.o[t + 1][i] * f0 + c.y * f1;
+            w.o[t + 2][i] = w.o[t + 2][i] * f0 + c.z * f1;
+            w.o[t + 3][i] = w.o[t + 3][i] * f0 + c.w * f1;
           }
       }
       __syncthreads();
     }
-    if (wave == 0) w.out_row(k, 0, 0, slot, 16, direct);
+    if (wave == 0) w.out_row(k, slot, direct);
     x += ue - u;
   }
 }
@@ -939,8 +907,8 @@ struct Rows {
       if constexpr (F8) {
         const int s = at / COLS, col = at % COLS;
         uint4* to = sh.k[buf] + (s * (D / 32) + 2 * col + (g >> 1)) * 64 + 32 * (g & 1) + n;
-        to[0] = __builtin_bit_cast(uint4, Wave<KV, D, 1>::key_operand(make_uint2(x.k[p].x, x.k[p].y)));
-        to[16] = __builtin_bit_cast(uint4, Wave<KV, D, 1>::key_operand(make_uint2(x.k[p].z, x.k[p].w)));
+        to[0] = __builtin_bit_cast(uint4, Wave<KV, D>::key_operand(make_uint2(x.k[p].x, x.k[p].y)));
+        to[16] = __builtin_bit_cast(uint4, Wave<KV, D>::key_operand(make_uint2(x.k[p].z, x.k[p].w)));
       } else {
         sh.k[buf][at * 64 + lane] = x.k[p];
       }
@@ -961,7 +929,7 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < ES; ++i) {
           uint32_t v = ok ? x.v[j][i] : 0;
-          const uint32_t m = Wave<KV, D, 1>::odd_marks(v);
+          const uint32_t m = Wave<KV, D>::odd_marks(v);
           marks |= m;
           x.v[j][i] = v & ~((m >> (F8 ? 7 : 15)) * (F8 ? 0xffu : 0xffffu));
         }
@@ -975,8 +943,8 @@ struct Rows {
       uint32_t c[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if constexpr (F8) c[j] = h ? Wave<KV, D, 1>::template two_codes<true>(x.v[j].x)
-                                   : Wave<KV, D, 1>::template two_codes<false>(x.v[j].x);
+        if constexpr (F8) c[j] = h ? Wave<KV, D>::template two_codes<true>(x.v[j].x)
+                                   : Wave<KV, D>::template two_codes<false>(x.v[j].x);
         else c[j] = x.v[j][h];
       }
       u32x4 e, f;
