@@ -1498,17 +1498,23 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
     return (int)(want < tiles ? want : (tiles > 1 ? tiles : 1));
   };
   // Few rows: four waves share a block's keys, a step of 128 keys is a unit, and
-  // every block reads the keys anew.  Many: a wave has its own rows.  Behind
-  // 4096 keys with 8 key heads, us, many-row launch and the other:
-  //   1 sequence,  128 rows of it (2048 units)  26.2  26.0;  256 (4096)  33.1  34.1
-  //   8 sequences,  48 rows of each (6144)  45.9  34.6;  64 (8192)  47.7  55.2
-  //   32 sequences, 16 (one block)  106  65;  32 (16384)  108  116;  64  115  218
-  // Behind few keys it is the blocks that count, each with its own latencies; behind
-  // 256:  8 sequences, 64 rows of each (256 blocks and key heads)  16.7  16.3;  16 (512)
-  // 17.0  16.7;  32 (1024)  21  31;  64 (2048)  34  43;  behind 64 keys 9.8  11.6,  10.0  13.8,
-  // 12  21,  19  33.
+  // every block reads the keys anew.  Many: a wave has its own rows, and a
+  // workgroup 128 of a sequence or more, of which few are there where sequences
+  // bring few.  Heads of 128, 8 key heads, us, many-row launch and the other,
+  // behind 4096 keys:
+  //   1 sequence,  128 rows of it (2048 units)  27.6  26.3;  256 (4096)  27.1  33.5
+  //   8 sequences,  64 rows of each (8192)  52.6  55.7;  16 (16384)  87.8  94.4;  32  134  219
+  //   8 sequences,  48 rows of each (6144)  51.2  35.1;  16 (12288)  84.9  55.5;  32  131  121
+  //   16 sequences, 32 rows of each (8192)  68.5  55.6;  32 (16384)  126  117;  128  457  412
+  // Behind few keys it is the blocks that count, each with its own latencies; 64
+  // rows of each behind 256 keys:  8 sequences (256 blocks and key heads)  17.6  16.5;
+  // 16 (512)  17.9  17.2;  32 (1024)  22.5  31.3;  64 (2048)  36.2  44.2;  behind 64 keys 10.3
+  // 12.0,  10.6  14.4,  12.9  21.7,  20.1  33.4.  32 rows of each behind 1024 keys:  32
+  // sequences (512)  45.8  38.4;  64 (1024)  66.0  61.9;  128 (2048)  128  140;  behind 256 keys
+  // 22.3  17.0,  26.7  31.7,  46.0  46.5;  behind 64 keys 11.9  14.0,  15.3  21.8,  25.8  34.1.
   const int64_t blocks = up(rows, 16) * Hkv;
-  p.own_wide = rows > 16 * B && (blocks > 512 || up(keys, kUnit) * blocks > 6144);
+  if (rows > 48 * B) p.own_wide = blocks > 512 || up(keys, kUnit) * blocks > 6144;
+  else p.own_wide = rows > 16 * B && blocks > 512 && keys <= 256;
   // The same for the prefix: 64 rows on 4096 keys (1024 units) 28  19, on 16384
   // (4096) 38  38; 256 rows on 16384 (16384 units) 59  116.
   p.pre_wide = prefix_len > 0 && (p.own_wide || up(prefix_len, kUnit) * up(rows, 16) * Hkv > 2048);

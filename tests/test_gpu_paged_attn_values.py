@@ -88,7 +88,7 @@ def test_zero_value_under_the_top_score(fmt, size, T, room):
         held(y, kv, vv, q, [n], table, D ** -0.5, q_start=[0, T])
 
 
-@pytest.mark.parametrize("T,room,n,gap", [(1, 0, 4096, 12.0), (12, ROOM, 4096, 12.0), (12, ROOM, 40000, 12.0)])
+@pytest.mark.parametrize("T,room,n,gap", [(1, 0, 4096, 12.0), (16, ROOM, 4096, 12.0), (16, ROOM, 40000, 12.0)])
 def test_thousands_of_keys_under_a_zero_value(T, room, n, gap):
     """Each of them has little weight, all together much of it."""
     rng = np.random.default_rng(n + T)
@@ -264,3 +264,15 @@ def test_a_layers_attention_within_its_roundings(fmt):
         k, v = layer.values()
         held(y, k, v, F.bf16_decode(bf16_bits(q.contiguous())), lens, table, layers.D ** -0.5, q_start=start)
         new = [1, 1]
+
+
+@pytest.mark.parametrize("B,n,keys", [(70, 6, 40), (70, 6, 300), (3, 13, 900), (3, 12, 900), (70, 12, 250)])
+@pytest.mark.parametrize("fmt", [UE8M0, BF16])
+def test_a_few_rows_of_each_sequence(fmt, B, n, keys):
+    """24 to 52 rows of each, on either side of the borders between the launches."""
+    rng = np.random.default_rng(B + n)
+    new = [n] * B
+    cached = [keys] + [int(v) for v in rng.integers(0, keys + 1, B - 1)]
+    cache, q, table, ptable, hidden = P.setup(rng, new, cached, 8, 2, 64, fmt, 16, extra=0 if B > 3 else ROOM)
+    y = P.run(cache, q, new, cached, table, ptable, hidden)
+    held(y, cache.k, cache.v, q, cached, table, 0.125, q_start=np.arange(B + 1) * n)
