@@ -1450,8 +1450,12 @@ hipError_t launch_attn(AttnArgs a, hipStream_t s) {
   AttnPlan& p = a.plan;
   // all at once, so that equal shares end together
   if (p.own_groups > 256 * split_resident(KV, D)) p.own_groups = 256 * split_resident(KV, D);
-  // What a call reads is left in the last-level cache where it fits there (256
-  // MiB), and passes it by where it does not.
+  // What a call may read is left in the last-level cache where it fits there (256
+  // MiB), and passes it by where it does not: 64 sequences of up to 8192 keys 118 us
+  // with the cache, 106 past it.  It goes by what the tables have room for (the
+  // lengths are on the device): shorter sequences in such tables, which the cache
+  // might hold from call to call, are read past it too (64 of up to 2000 keys 37 us
+  // with it, 40 past it; of up to 600 the same).
   const int64_t room = (int64_t)a.max_pages << a.log2_page;
   const int64_t keys = a.window && a.window < room ? a.window : room;
   const bool stream = keys * a.B * a.Hkv * 2 * (KV == kKvBf16 ? 2 * D : D + 4) > (int64_t(1) << 28);
@@ -1515,13 +1519,17 @@ AttnPlan attn_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t keys, i
   const int64_t blocks = up(rows, 16) * Hkv;
   if (rows > 48 * B) p.own_wide = blocks > 512 || up(keys, kUnit) * blocks > 6144;
   else p.own_wide = rows > 16 * B && blocks > 512 && keys <= 256;
-  // The same for the prefix: 64 rows on 4096 keys (1024 units) 28  19, on 16384
-  // (4096) 38  38; 256 rows on 16384 (16384 units) 59  116.
-  p.pre_wide = prefix_len > 0 && (p.own_wide || up(prefix_len, kUnit) * up(rows, 16) * Hkv > 2048);
+  // The same for the prefix, many-row launch and with the sequences': 64 rows on
+  // 4096 keys (1024 units) 29.0  19.5, on 16384 (4096) 39.2  37.8; 256 rows on 4096 (4096)
+  // 36.3  35.6, on 16384 (16384) 61  115; 512 rows on 4096 (8192) 51  60; 1024 rows on 1024
+  // (4096) 48.5  46.3.
+  p.pre_wide = prefix_len > 0 && (p.own_wide || up(prefix_len, kUnit) * up(rows, 16) * Hkv > 4096);
   // Workgroups of eight waves where their 256 rows are mostly there.  Behind 4096
-  // keys, four waves and eight, us: 1 sequence of 512 rows 36  38, of 2048 71  66; 2
-  // of 1024 73  66; 8 of 128 66  67, of 256 86  99, of 512 123  109, of 1024 192  159; 2 of
-  // 8192 over 6000 keys 470  387.
+  // keys, four waves and eight, us: 1 sequence of 512 rows 36.0  39.5, of 1024 50.4  52.4,
+  // of 2048 76.2  75.5; 2 of 1024 78.5  75.7; 4 of 512 79.3  86.9; 8 of 256 96  117, of 512
+  // 135  127, of 1024 215  194; 16 of 512 222  374; 2 of 8192 over 6000 keys 522  476.  The
+  // prefix launch's: 512 rows on 4096 keys 51.4  53.1, on 16384 93  88; 1024 on 4096 72.2
+  // 70.8, on 16384 151  138.
   p.own_waves = rows >= 1024 * B ? 8 : 4;
   p.pre_waves = rows >= 1024 ? 8 : 4;
   p.own_rows = p.own_wide ? wide * p.own_waves : 16;

@@ -24,7 +24,7 @@ def plan(T, B, Hq, Hkv, D, keys, prefix):
         p.own_wide = blocks > 512 or up(keys, UNIT) * blocks > 6144
     else:
         p.own_wide = rows > 16 * B and blocks > 512 and keys <= 256
-    p.pre_wide = prefix > 0 and (p.own_wide or up(prefix, UNIT) * blocks > 2048)
+    p.pre_wide = prefix > 0 and (p.own_wide or up(prefix, UNIT) * blocks > 4096)
     p.own_waves, p.pre_waves = (8 if rows >= 1024 * B else 4), (8 if rows >= 1024 else 4)
     p.own_rows = wide * p.own_waves if p.own_wide else 16
     p.pre_rows = wide * p.pre_waves if p.pre_wide else 16

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import attn_plan
 import attn_value_bounds as bounds
 import test_gpu_attn_layer as layers
 import test_gpu_paged_attn as P
@@ -276,3 +277,19 @@ def test_a_few_rows_of_each_sequence(fmt, B, n, keys):
     cache, q, table, ptable, hidden = P.setup(rng, new, cached, 8, 2, 64, fmt, 16, extra=0 if B > 3 else ROOM)
     y = P.run(cache, q, new, cached, table, ptable, hidden)
     held(y, cache.k, cache.v, q, cached, table, 0.125, q_start=np.arange(B + 1) * n)
+
+
+@pytest.mark.parametrize("B,Hq,D,fmt,prefix,window", [
+    # a prefix for the many-row launch: workgroups of four waves, of eight
+    (64, 8, 64, FLOAT, 16600, 0), (33, 16, 256, BF16, 16000, 9000), (132, 16, 128, UE8M0, 4100, 0)])
+def test_prefix_under_many_rows(B, Hq, D, fmt, prefix, window):
+    rng = np.random.default_rng(D + prefix)
+    cached = [1 + 3 * i % 50 for i in range(B)]
+    cache, q, table, ptable, hidden = P.setup(rng, [1] * B, cached, Hq, 2, D, fmt, 64, prefix, extra=0)
+    assert attn_plan.plan(B, B, Hq, 2, D, 64 * table.shape[1], prefix).pre_wide
+    t = cache.tensors()
+    P.poison(t, cache, hidden)
+    y = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=dev())
+    L.paged_attn(P.on_dev(q), kv_len=to_dev(np.array(cached, np.int32)), page_table=to_dev(table), y=y,
+                 prefix_table=to_dev(ptable), prefix_len=prefix, window=window, **t)
+    held(y, cache.k, cache.v, q, cached, table, D ** -0.5, prefix_table=ptable, prefix_len=prefix, window=window)
