@@ -28,11 +28,12 @@
 // The values' transposition is a byte permutation of what a lane itself loads
 // (8 keys x D/16 values).  Few rows (attn_split_kernel): nothing goes through
 // LDS on the way from memory to the matrix cores, bound by HBM: 64 sequences
-// of up to 8192 keys (32 / 8 heads of 128, E4M3) 575 MB in 98 to 116 us, 5.0 to
-// 5.8 TB/s; 131072 keys of one 277 MB in 50.5 us, 5.5; a large copy runs at
+// of up to 8192 keys (32 / 8 heads of 128, E4M3) 575 MB in 100 to 117 us, 4.9 to
+// 5.8 TB/s; 131072 keys of one 277 MB in 51.5 us, 5.4; a large copy runs at
 // 5.1.  Many rows (attn_rows_kernel): conversions and transpositions are shared
-// through LDS, bound by issue and latency: 2 x 2048 tokens over 6000 keys 334
-// GFLOP in 382 to 455 us, 730 to 875 TFLOP/s; a large bf16 product runs at 1415.
+// through LDS, bound by issue: 2 x 2048 tokens over 6000 keys 334 GFLOP (one and a
+// half times that on the matrix cores) in 473 us, 706 TFLOP/s, where launches
+// follow each other, 557 us alone; a large bf16 product runs at 1415.
 #include <type_traits>
 
 #include "bsfp8_attn.h"
@@ -1222,11 +1223,13 @@ struct Rows {
 // A workgroup takes 16 W RT rows of a block and key head; every wave walks all of
 // its split of the keys.  pre: the blocks are of all tokens, the keys the
 // prefix's.  Eight waves a CU (132 KB of LDS, 256 registers), in one workgroup
-// or two: one wave's products run beside another's weights.  Four waves a
-// workgroup at 2 x 2048 over 6000 keys: matrix cores busy 28% of the time,
-// vector issue 50%, LDS 27%; eight convert and store a tile once for twice the
-// rows.  32 rows a wave share an operand read from LDS (16 would double LDS's
-// share to where it bounds; 64 leave one wave a SIMD, 689 us against 516).
+// or two: one wave's products run beside another's weights.  Eight waves a
+// workgroup at 2 x 2048 over 6000 keys: matrix cores busy 45% of the time,
+// vector issue 61%, LDS 30%; waves wait on issue 31% of theirs, on loads, LDS and
+// barriers 29%.  Four convert and store a tile for half the rows (522 us against
+// 476).  32 rows a wave share an operand read from LDS (16 would double LDS's
+// share to where it bounds; 64 leave one wave a SIMD: 689 us against 516, both with
+// one product of the weights and four waves).
 template <int KV, int D, int RT, int W>
 __global__ __launch_bounds__(64 * W, 8 / W) void attn_rows_kernel(AttnArgs a, const int pre) {
   constexpr int ROWS = 16 * W * RT;

@@ -6,9 +6,9 @@
 // head; a cached row is the activation codec of fp8_quant_act over the head
 // (one scale per token and head), or bf16.
 //
-// The angle is a product of a whole number and an fp32 one, exact in 64 bits;
-// whole turns leave it there, and what is left (at most half a turn) goes to
-// fp32.  The rotated key is quantized from fp32, not rounded to bf16 between.
+// The angle is a product of a whole number and an fp32 one, taken in 64 bits
+// (exact for positions below 2^29); whole turns leave it there, and what is left
+// (at most half a turn) goes to fp32.  The rotated key is quantized from fp32, not rounded to bf16 between.
 //
 // Bound by HBM for a prompt (8192 tokens of 32 + 8 + 8 heads of 128, FP8 cache:
 // 185 MB in 34.7 us, 5.3 TB/s; a large copy runs at 5.1), by the launch for a
@@ -89,8 +89,9 @@ __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvArgs a) {
   }
 
   // PER_WAVE: the next head's values are under way while one is computed, and
-  // read once (8192 tokens of 32 + 8 + 8 heads from memory: 36 us, 42 without the
-  // hint; 37 and 32 where the last-level cache still has them)
+  // read once, past the caches (tokens of 32 + 8 + 8 heads, with the hint and without:
+  // from memory 4096 20 us, 24; 8192 36, 42; where the launch before has just
+  // written them 2048 12.8, 11.1; 4096 18.7, 17.7; 8192 36.8, 39.4)
   auto ld = [](const uint16_t* p) { return PER_WAVE ? ld_stream16(p) : *(const uint4*)p; };
   auto source = [&](int r) {
     const uint16_t* p = r < nq ? a.q + t * a.ldq + (int64_t)r * D

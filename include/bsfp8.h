@@ -489,7 +489,7 @@ BSFP8_API int32_t rope_inv_freq(int32_t scaling, int64_t rot_dim, double base, d
  *   k, v       bf16 [T][Hkv][D], row strides ldk and ldv.  Both NULL: no
  *              cache (slots and the caches are not looked at).
  *   positions  DEVICE int32 [T];  inv_freq DEVICE fp32 [rot_dim / 2].  The
- *              angle is exact (64 bits) before its sine and cosine are taken.
+ *              angle is taken in 64 bits (exact for positions below 2^29).
  *              rot_dim 0: neither is looked at.
  *   slots      DEVICE int64 [T]: page * page_size + place in the page; a token
  *              whose slot is negative or >= num_pages * page_size is not
@@ -525,8 +525,8 @@ BSFP8_API int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_
  * stands at position prefix_len + kv_len[b] - 1, the others before it.  A
  * token sees the keys at its own position and before, with a window only the
  * last `window` of these (itself among them).  No key seen: y = 0.  The
- * prefix's keys and values are read once for the batch, not once per
- * sequence.  Deterministic: the same call gives the same bits.
+ * prefix's keys and values are read once per 16 to 256 query rows of the batch
+ * (tokens times query heads of a key head), not once per sequence.  Deterministic: the same call gives the same bits.
  *
  *   q           bf16 [T][Hq][D], row stride ldq (ldq % 8 == 0).
  *   q_start     DEVICE int32 [B+1], not decreasing (else y stays as it is),
