@@ -542,7 +542,8 @@ BSFP8_API int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_
  *               the prefix; own keys begin on a page of their own.  Not
  *               looked at for prefix_len 0.
  *   k_cache .. kv_fmt, num_pages, page_size   as rope_kv_append writes them;
- *               value scales beyond 2^75 are outside the contract, those
+ *               value scales beyond 2^75 and bf16 values beyond 2^83 are
+ *               outside the contract (sums of e^(s_j) v_j are fp32), scales
  *               below 2^-85 lose precision; 0 is a value of zeros.  A key
  *               whose e^(s_j) is below 2^-126 of the largest adds nothing.
  *               What they hold behind a sequence's or the prefix's last key,

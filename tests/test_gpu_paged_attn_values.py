@@ -293,3 +293,19 @@ def test_prefix_under_many_rows(B, Hq, D, fmt, prefix, window):
     L.paged_attn(P.on_dev(q), kv_len=to_dev(np.array(cached, np.int32)), page_table=to_dev(table), y=y,
                  prefix_table=to_dev(ptable), prefix_len=prefix, window=window, **t)
     held(y, cache.k, cache.v, q, cached, table, D ** -0.5, prefix_table=ptable, prefix_len=prefix, window=window)
+
+
+@pytest.mark.parametrize("fmt", [FLOAT, UE8M0, BF16])
+@pytest.mark.parametrize("T,room", [(1, 2), (40, ROOM)])
+def test_largest_values(fmt, T, room):
+    """Thousands of values of the largest size that is allowed, under scores
+    that rise slowly: a reference that stays behind them."""
+    rng = np.random.default_rng(81)
+    n, D = 3000, 64
+    u = rng.standard_normal(D)
+    q = F.bf16_round(u + 0.01 * rng.standard_normal((T, 4, D)))
+    k = (np.linspace(0.0, 6.0, n)[:, None] * u / (u @ u) * 8.0)[:, None]      # 0 to 6: under 2^10 of the first
+    v = 2.0 ** 82 * rng.choice([-1.0, 1.0], (n, 1, D)) * rng.uniform(1.0, 2.0, (n, 1, D))
+    t, (kv, vv), order = appended(F.bf16_round(k), F.bf16_round(v), fmt, 16, rng=rng)
+    y, table = attend(q, t, n, order, room)
+    held(y, kv, vv, q, [n], table, D ** -0.5, q_start=[0, T])
