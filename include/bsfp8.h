@@ -548,7 +548,8 @@ BSFP8_API int32_t rope_kv_append(const void* q, int64_t ldq, void* q_out, int64_
  *               whose e^(s_j) is below 2^-126 of the largest adds nothing.
  *               What they hold behind a sequence's or the prefix's last key,
  *               or before the window, reaches no result, NaN and infinities
- *               included.
+ *               included; a key or value that a row sees and that is not finite
+ *               leaves the row, or its elements, infinite or NaN.
  *   scale       > 0; scores beyond fp32's range are outside the contract.
  *   window      0: none.
  *   y           out, bf16 [T][Hq][D] (dense); must not overlap an input.
