@@ -19,7 +19,7 @@
 // element to which that key's value adds nothing consists of (a value row of
 // zeros has the scale 1).  The second half of the products costs few rows
 // nothing (64 x 8192 112 us, 113 with it), many rows a quarter (2 x 2048 over
-// 6000 keys 385 us, 480).
+// 6000 keys 387 us, 473).
 //
 // Layout.  The score tile is computed transposed, keys x rows: a lane then
 // holds 8 keys of one row, which is what the second product wants of it as an
